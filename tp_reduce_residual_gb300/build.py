@@ -48,7 +48,7 @@ MODES = {
 }
 
 SOURCES = ["bn_device.cuh", "bn_internal.h", "bn_kernels.cu", "bn_abi.cu", "bn_wide.h",
-           "bn_wide.cu", "bn_noalloc.cu", "bn_cluster.h", "bn_cluster.cu"]
+           "bn_wide.cu", "bn_noalloc.cu", "bn_cluster.h", "bn_cluster.cu", "bn_host.h"]
 
 
 def nvcc() -> str:

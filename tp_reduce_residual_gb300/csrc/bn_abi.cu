@@ -20,6 +20,7 @@
 
 #include "../../include/beamnorm.h"
 #include "bn_cluster.h"
+#include "bn_host.h"
 #include "bn_internal.h"
 #include "bn_wide.h"
 
@@ -35,6 +36,8 @@ constexpr int kVersion = 10200;  // 1.2.0
 
 thread_local char g_msg[512] = "";
 
+}  // namespace
+
 bn_status fail(bn_status st, const char *fmt, ...)
 {
     va_list ap;
@@ -48,6 +51,10 @@ bn_status cuda_fail(cudaError_t e, const char *what)
 {
     return fail(BN_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
+
+void clear_message() { g_msg[0] = '\0'; }
+
+namespace {
 
 // ---- tuning overrides (process-wide) -------------------------------------------
 
@@ -68,17 +75,11 @@ int tiny_for(int mode, float eps)
 
 // ---- per-device state ------------------------------------------------------------
 
-struct DeviceInfo {
-    int sms = 0;
-    int smem_optin = 0;      // dynamic + static shared memory one CTA may use
-    int smem_per_sm = 0;     // shared memory of one SM
-    int smem_reserved = 0;   // shared memory the system reserves per CTA
-    unsigned *err = nullptr;  // address of g_bn_device_error on this device
-};
-
 std::once_flag g_dev_once[kMaxDevices];
 DeviceInfo g_dev[kMaxDevices];
 cudaError_t g_dev_status[kMaxDevices];
+
+}  // namespace
 
 bn_status device_info(const DeviceInfo **out)
 {
@@ -108,13 +109,7 @@ bn_status device_info(const DeviceInfo **out)
 
 bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
-struct Range {
-    const void *p;
-    size_t bytes;
-    const char *name;
-};
-
-bool overlaps(const Range &x, const Range &y)
+static bool overlaps(const Range &x, const Range &y)
 {
     if (!x.p || !y.p || x.bytes == 0 || y.bytes == 0) return false;
     const uintptr_t a0 = reinterpret_cast<uintptr_t>(x.p), a1 = a0 + x.bytes;
@@ -136,6 +131,8 @@ bn_status check_overlaps(const Range *writes, int nw, const Range *reads, int nr
     }
     return BN_OK;
 }
+
+namespace {
 
 bn_status check_shape(int R, int T, int k, int H, bool fin)
 {
@@ -172,17 +169,9 @@ bn_status check_eps(float eps)
     return BN_OK;
 }
 
-#define BN_REQUIRE(cond, ...)                                      \
-    do {                                                           \
-        if (!(cond)) return fail(BN_ERR_INVALID, __VA_ARGS__);     \
-    } while (0)
-#define BN_TRY(expr)                         \
-    do {                                     \
-        bn_status _st = (expr);              \
-        if (_st != BN_OK) return _st;        \
-    } while (0)
+}  // namespace
 
-bn_status check_ptr16(const void *p, const char *name, bool required = true)
+bn_status check_ptr16(const void *p, const char *name, bool required)
 {
     if (!p) {
         if (required) return fail(BN_ERR_INVALID, "%s is NULL", name);
@@ -198,6 +187,10 @@ bn_status check_ptr4(const void *p, const char *name)
     if (!aligned(p, 4)) return fail(BN_ERR_INVALID, "%s is not 4-byte aligned", name);
     return BN_OK;
 }
+
+bool dependent_launch() { return g_tune_pdl.load() != 1; }
+
+namespace {
 
 // ---- launch shape ----------------------------------------------------------------
 

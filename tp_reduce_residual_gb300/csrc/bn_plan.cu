@@ -1,0 +1,157 @@
+// bn_plan.cu -- the plan that groups token slots by expert.
+//
+// Slot i = t * k + j of ids goes to place
+//   perm[i] = offsets[id_i] + number of slots i' < i with the same id,
+// offsets[e] = number of slots of experts below e, and rows[perm[i]] = t: a
+// stable counting sort, so every place is decided by the ids alone.  Slots
+// without an expert (id -1) come after all groups, from place offsets[E] on.
+//
+// One launch, no scratch memory: a cluster of up to 16 CTAs splits the slots,
+// each warp a run of them.  Every warp counts its run per expert in shared
+// memory; a scan over the warps, the CTAs (their totals read through
+// distributed shared memory) and the experts turns counts into places; a second
+// pass over the run hands them out.  Within 32 slots __match_any_sync finds
+// equal ids.  Latency bounds it: the bytes are a few hundred KB.
+#include "../../include/beamnorm.h"
+#include "bn_device.cuh"
+#include "bn_experts.h"
+
+namespace bn {
+using namespace dev;
+
+namespace {
+
+constexpr unsigned kAll = 0xffffffffu;
+
+__device__ __forceinline__ int bucket_of(const PlanArgs &a, int slot)
+{
+    const int id = __ldg(a.ids + slot);
+    return (unsigned)id < (unsigned)a.E ? id : a.E;
+}
+
+__device__ __forceinline__ unsigned ld_cluster(uint32_t addr)
+{
+    unsigned v;
+    asm volatile("ld.shared::cluster.u32 %0, [%1];" : "=r"(v) : "r"(addr));
+    return v;
+}
+
+__global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int per_warp)
+{
+    extern __shared__ unsigned smem[];
+    const int nb = a.E + 1;                   // experts, and the slots without one
+    const int warps = blockDim.x >> 5, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    unsigned *count = smem;                   // [warps][nb]
+    unsigned *total = count + warps * nb;     // [nb] this CTA's slots of each expert
+    unsigned *base = total + nb;              // [nb] first place of this CTA's slots
+    __shared__ unsigned sums[33];
+    const uint32_t cta = cluster_ctarank(), ctas = cluster_nctarank();
+
+    for (int i = threadIdx.x; i < warps * nb; i += blockDim.x) count[i] = 0;
+    griddep_launch_dependents();
+    griddep_wait();
+    __syncthreads();
+
+    const long long first = ((long long)cta * warps + warp) * per_warp;
+    const int lo = (int)min(first, (long long)a.slots);
+    const int hi = (int)min(first + per_warp, (long long)a.slots);
+    unsigned *mine = count + warp * nb;
+    bool bad = false;
+    for (int i = lo + lane; i < hi; i += 32) {  // counting needs no order
+        const int id = __ldg(a.ids + i);
+        bad |= id < -1 || id >= a.E;
+        atomicAdd(mine + ((unsigned)id < (unsigned)a.E ? id : a.E), 1u);
+    }
+    if (bad) atomicOr(a.err, BN_DEVERR_EXPERT_RANGE);
+    __syncthreads();
+    for (int b = threadIdx.x; b < nb; b += blockDim.x) {
+        unsigned run = 0;
+        for (int w = 0; w < warps; ++w) {
+            const unsigned c = count[w * nb + b];
+            count[w * nb + b] = run;
+            run += c;
+        }
+        total[b] = run;
+    }
+    cluster_sync_all();
+    // experts in chunks of one per thread, with a carry between chunks
+    unsigned carry = 0;
+    for (int b0 = 0; b0 < nb; b0 += blockDim.x) {
+        const int b = b0 + threadIdx.x;
+        unsigned all = 0, before = 0;
+        if (b < nb) {
+            const uint32_t at = smem_addr(total + b);
+            for (uint32_t c = 0; c < ctas; ++c) {
+                const unsigned v = c == cta ? total[b] : ld_cluster(mapa(at, c));
+                before += c < cta ? v : 0u;
+                all += v;
+            }
+        }
+        unsigned run = all;  // inclusive scan over the block
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const unsigned v = __shfl_up_sync(kAll, run, o);
+            if (lane >= o) run += v;
+        }
+        if (lane == 31) sums[warp] = run;
+        __syncthreads();
+        if (warp == 0) {
+            const unsigned own = lane < warps ? sums[lane] : 0u;
+            unsigned s = own;
+#pragma unroll
+            for (int o = 1; o < 32; o <<= 1) {
+                const unsigned v = __shfl_up_sync(kAll, s, o);
+                if (lane >= o) s += v;
+            }
+            sums[lane] = s - own;
+            if (lane == 31) sums[32] = s;
+        }
+        __syncthreads();
+        const unsigned start = carry + sums[warp] + run - all;
+        carry += sums[32];
+        if (b < nb) {
+            base[b] = start + before;
+            if (cta == 0) a.offsets[b] = (int)start;
+        }
+        __syncthreads();
+    }
+    // hand out the places, in slot order
+    const unsigned below = (1u << lane) - 1u;
+    for (int i0 = lo; i0 < hi; i0 += 32) {
+        const int i = i0 + lane;
+        const int b = i < hi ? bucket_of(a, i) : -1;
+        const unsigned same = __match_any_sync(kAll, b);
+        unsigned place = 0;
+        if (b >= 0) place = base[b] + mine[b] + __popc(same & below);
+        __syncwarp();
+        if (b >= 0 && (same & below) == 0) mine[b] += __popc(same);
+        __syncwarp();
+        if (b >= 0) {
+            a.rows[place] = (int)((unsigned)i / (unsigned)a.k);
+            for (int r = 0; r < a.R; ++r) a.perm[(long long)r * a.slots + i] = (int)place;
+        }
+    }
+    cluster_sync_all();  // no CTA leaves while its totals may be read
+}
+
+}  // namespace
+
+cudaError_t launch_plan(const PlanArgs &a, bool pdl, cudaStream_t st)
+{
+    // 512 slots a CTA, up to 16 CTAs of 512 threads; then longer runs per warp
+    const int threads = 512, warps = threads / 32;
+    int ctas = 1;
+    while (ctas < 16 && (long long)ctas * 512 < a.slots) ctas *= 2;
+    const long long share = ((long long)a.slots + ctas * warps - 1) / (ctas * warps);
+    const int per_warp = (int)((share + 31) / 32 * 32);
+    const size_t smem = sizeof(unsigned) * ((size_t)warps + 2) * (size_t)(a.E + 1);
+    cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                         (int)smem);
+    if (e == cudaSuccess && ctas > 8)
+        e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(plan_kernel, dim3((unsigned)ctas), dim3(threads), smem, pdl, ctas, st, a,
+                         per_warp);
+}
+
+}  // namespace bn

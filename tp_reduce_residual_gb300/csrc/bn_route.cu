@@ -1,0 +1,505 @@
+// bn_route.cu -- routing of tokens to experts, and its gradient.
+//
+// Forward, for one token's logits x[0..E):
+//   s_e = 1 / (1 + exp(-x_e))  or  exp(x_e - max x) / sum exp(x - max x)
+//   key_e = s_e + bias_e; without a bias, and unless groups are ranked by a sum
+//     of scores, key_e = x_e (the scores rise with the logits)
+//   groups > 1: a group's rank is the sum of its `group_top` largest keys; the
+//     `top_groups` groups of the highest rank stay
+//   ids = the k largest keys left, equal keys by rising index
+//   w   = scale * s_id, or scale * s_id / sum over the k of s
+// A logit or bias of -inf takes its expert out; slots for which no expert is
+// left get id -1 and weight 0.  A NaN logit or key takes its expert out and
+// makes the row's weights NaN.
+//
+// The order of keys is decided as in exact arithmetic.  Keys that are logits
+// compare exactly.  Sums s + bias are computed in 32 bits with a bound on their
+// error; where two keys (or two groups' ranks) whose order matters differ by
+// less than the bound, the row is selected again with 64-bit scores.
+//
+// One warp per token: a lane holds VPT consecutive experts in registers and the
+// warp takes the largest key k times (redux.sync).  What bounds it is
+// instruction issue, about k * (2 redux + 3 VPT) for the selection.
+#include <cfloat>
+#include <cmath>
+
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "../../include/beamnorm.h"
+#include "bn_device.cuh"
+#include "bn_experts.h"
+
+namespace bn {
+using namespace dev;
+
+namespace {
+
+constexpr int kWarps = 4;           // tokens per block
+constexpr unsigned kAll = 0xffffffffu;
+constexpr int kNone = 0x7fffffff;
+
+template <typename T> __device__ __forceinline__ float to_f32(T v);
+template <> __device__ __forceinline__ float to_f32(float v) { return v; }
+template <> __device__ __forceinline__ float to_f32(__nv_bfloat16 v) { return __bfloat162float(v); }
+template <> __device__ __forceinline__ float to_f32(__half v) { return __half2float(v); }
+
+template <typename T> __device__ __forceinline__ T from_f32(float v);
+template <> __device__ __forceinline__ float from_f32(float v) { return v; }
+template <> __device__ __forceinline__ __nv_bfloat16 from_f32(float v) { return __float2bfloat16_rn(v); }
+template <> __device__ __forceinline__ __half from_f32(float v) { return __float2half_rn(v); }
+
+__device__ __forceinline__ float warp_max(float v)
+{
+    float m;
+    asm volatile("redux.sync.max.f32 %0, %1, 0xffffffff;" : "=f"(m) : "f"(v));
+    return m;
+}
+__device__ __forceinline__ double warp_max(double v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmax(v, __shfl_xor_sync(kAll, v, o));
+    return v;
+}
+__device__ __forceinline__ float warp_min(float v) { return -warp_max(-v); }
+__device__ __forceinline__ float warp_sum(float v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+__device__ __forceinline__ double warp_sum(double v)
+{
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(kAll, v, o);
+    return v;
+}
+
+// Elements [lane * VPT, lane * VPT + VPT) of a row of n, `fill` past the end.
+template <typename T, int VPT>
+__device__ __forceinline__ void load_row(const T *row, int n, int lane, bool vec, float fill, float *x)
+{
+    constexpr int W = 16 / (int)sizeof(T);  // elements per 16-byte load
+    if constexpr (VPT >= W) {
+        if (vec) {
+#pragma unroll
+            for (int c = 0; c < VPT / W; ++c) {
+                const int i = lane * VPT + c * W;
+                union { uint4 q; T t[W]; } u;
+                if (i < n) {  // n is a multiple of W
+                    u.q = __ldg(reinterpret_cast<const uint4 *>(row + i));
+#pragma unroll
+                    for (int j = 0; j < W; ++j) x[c * W + j] = to_f32(u.t[j]);
+                } else {
+#pragma unroll
+                    for (int j = 0; j < W; ++j) x[c * W + j] = fill;
+                }
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = lane * VPT + j;
+        x[j] = i < n ? to_f32(row[i]) : fill;
+    }
+}
+
+__device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-x)); }
+__device__ __forceinline__ double sigmoid(double x) { return 1.0 / (1.0 + exp(-x)); }
+
+// Error bound of a 32-bit score: expf is within 2 units in the last place
+// (2^-22 relative), the addition and the division within 2^-24 each: 1.5 * 2^-22
+// of s <= 1 for the sigmoid.  The softmax's sum of at most 1024 terms (32 in a
+// lane, 5 levels) adds 37 * 2^-24 and x - max its own rounding, at most
+// max(d exp(-d)) * 2^-24: under 2^-18 of the largest probability together.
+constexpr float kSigmoidError = 1.5f * 0x1p-22f;
+constexpr float kSoftmaxError = 0x1p-18f;
+
+// Take the n largest of the warp's keys, one per round; lane j ends with the
+// j-th id (-1 where nothing is left) and its key.
+template <typename F, int VPT>
+__device__ __forceinline__ void take(F *key, int lane, int n, int &id, F &at)
+{
+    id = -1;
+    at = -INFINITY;
+    F best = key[0];
+    int bi = 0;
+#pragma unroll
+    for (int j = 1; j < VPT; ++j)
+        if (key[j] > best) { best = key[j]; bi = j; }
+    for (int r = 0; r < n; ++r) {
+        const F m = warp_max(best);
+        if (!(m > (F)-INFINITY)) break;
+        const int i = __reduce_min_sync(kAll, best == m ? lane * VPT + bi : kNone);
+        if (lane == r) { id = i; at = m; }
+        if (i / VPT == lane) {
+            best = -INFINITY;
+            const int gone = i % VPT;
+            bi = 0;
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) {
+                if (j == gone) key[j] = -INFINITY;
+                if (key[j] > best) { best = key[j]; bi = j; }
+            }
+        }
+    }
+}
+
+template <typename F>
+__device__ __forceinline__ void push2(F v, F &a, F &b)
+{
+    if (v > a) { b = a; a = v; }
+    else if (v > b) b = v;
+}
+
+// Mask out the keys of all but the top_groups groups of the highest rank.
+// `slot` is the warp's shared memory for VPT * 32 keys.  Returns how far the
+// lowest rank that stays is above the highest that goes (inf if none goes).
+template <typename F, int VPT>
+__device__ __forceinline__ F keep_groups(F *key, int lane, const RouteArgs &a, F *slot, F &largest)
+{
+    const int size = a.E / a.groups;
+    F r1 = -INFINITY, r2 = -INFINITY;  // lane g: the two largest keys of group g
+    const int lanes = size / VPT;      // lanes per group, when groups are whole lanes
+    if (size % VPT == 0 && (lanes & (lanes - 1)) == 0) {
+        F p = -INFINITY, q = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) push2(key[j], p, q);
+        for (int o = 1; o < lanes; o <<= 1) {
+            const F po = __shfl_xor_sync(kAll, p, o), qo = __shfl_xor_sync(kAll, q, o);
+            push2(po, p, q);
+            push2(qo, p, q);
+        }
+        const int src = min(lane * lanes, 31);
+        r1 = __shfl_sync(kAll, p, src);
+        r2 = __shfl_sync(kAll, q, src);
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) slot[lane * VPT + j] = key[j];
+        __syncwarp();
+        if (lane < a.groups)
+            for (int i = 0; i < size; ++i) push2(slot[lane * size + i], r1, r2);
+        __syncwarp();
+    }
+    F rank = -INFINITY;
+    if (lane < a.groups && r1 > (F)-INFINITY)
+        rank = a.group_top > 1 && r2 > (F)-INFINITY ? r1 + r2 : r1;
+    int ahead = 0;
+    for (int g = 0; g < a.groups; ++g) {
+        const F o = __shfl_sync(kAll, rank, g);
+        ahead += (o > rank || (o == rank && g < lane)) ? 1 : 0;
+    }
+    const bool keep = lane < a.groups && ahead < a.top_groups;
+    const unsigned kept = __ballot_sync(kAll, keep);
+    const F low = -warp_max(keep && rank > (F)-INFINITY ? -rank : (F)-INFINITY);
+    const F high = warp_max(!keep && lane < a.groups ? rank : (F)-INFINITY);
+    largest = warp_max(rank > (F)-INFINITY ? (rank < 0 ? -rank : rank) : (F)0);
+    if (size % VPT == 0) {  // a lane's experts are one group's
+        const int g = lane * VPT / size;
+        const bool out = g >= a.groups || !((kept >> g) & 1u);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (out) key[j] = -INFINITY;
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int e = lane * VPT + j;
+            if (e < a.E && !((kept >> (e / size)) & 1u)) key[j] = -INFINITY;
+        }
+    }
+    return high > (F)-INFINITY ? low - high : (F)INFINITY;
+}
+
+// The selection with 64-bit scores, for rows whose order 32 bits do not tell.
+template <typename T, int VPT>
+__device__ __noinline__ int select64(const T *row, const RouteArgs &a, int lane, double *slot)
+{
+    float x[VPT];
+    load_row<T, VPT>(row, a.E, lane, a.vec, -INFINITY, x);
+    double key[VPT];
+    if (a.sigmoid) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) key[j] = sigmoid((double)x[j]);
+    } else {
+        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) m = fmaxf(m, x[j]);
+        m = warp_max(m);
+        double sum = 0;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            key[j] = x[j] > -INFINITY ? exp((double)x[j] - (double)m) : 0.0;
+            sum += key[j];
+        }
+        sum = warp_sum(sum);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) key[j] /= sum;
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int e = lane * VPT + j;
+        const double b = a.bias && e < a.E ? (double)__ldg(a.bias + e) : 0.0;
+        key[j] += b;
+        if (!(x[j] > -INFINITY) || !(key[j] > -INFINITY)) key[j] = -INFINITY;
+    }
+    if (a.groups > 1) {
+        double unused;
+        keep_groups<double, VPT>(key, lane, a, slot, unused);
+    }
+    int id;
+    double at;
+    take<double, VPT>(key, lane, a.k, id, at);
+    return id;
+}
+
+// SUMS: the keys are s + bias (or group ranks are sums of scores), else logits.
+template <typename T, int VPT, bool SUMS>
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
+{
+    __shared__ double slots[SUMS ? kWarps : 1][SUMS ? 32 * VPT : 1];
+    __shared__ float fslots[SUMS ? 1 : kWarps][SUMS ? 1 : 32 * VPT];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = blockIdx.x * kWarps + warp;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (t >= a.T) return;
+    const T *row = static_cast<const T *>(a.logits) + (long long)t * a.ld;
+
+    float key[VPT];
+    load_row<T, VPT>(row, a.E, lane, a.vec, -INFINITY, key);
+    bool nan = false;
+    float top = -INFINITY;
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        nan |= key[j] != key[j];
+        top = fmaxf(top, key[j]);  // a NaN is passed over
+    }
+    // softmax statistics, where a score depends on the whole row
+    float inv = 0.0f;
+    if (!a.sigmoid && (SUMS || !a.renormalize)) {
+        top = warp_max(top);
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) sum += key[j] > -INFINITY ? expf(key[j] - top) : 0.0f;
+        sum = warp_sum(sum);
+        inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // 0: every expert is masked
+    }
+    float *slot = SUMS ? reinterpret_cast<float *>(slots[warp]) : fslots[SUMS ? 0 : warp];
+    float serr = 0.0f;
+    if constexpr (SUMS) {
+        serr = a.sigmoid ? kSigmoidError : kSoftmaxError * inv;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int e = lane * VPT + j;
+            const float x = key[j];
+            const float b = a.bias && e < a.E ? __ldg(a.bias + e) : 0.0f;
+            const float v = (a.sigmoid ? sigmoid(x) : expf(x - top) * inv) + b;
+            nan |= x > -INFINITY && v != v;
+            key[j] = x > -INFINITY && v > -INFINITY ? v : -INFINITY;
+        }
+    } else {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (!(key[j] > -INFINITY)) key[j] = -INFINITY;
+    }
+    nan = __any_sync(kAll, nan);
+
+    bool sure = true;
+    if (a.groups > 1) {
+        float largest;
+        const float gap = keep_groups<float, VPT>(key, lane, a, slot, largest);
+        // a rank is one or two keys: twice a key's error each, and its own rounding
+        if constexpr (SUMS) sure = gap > 4.0f * serr + 0x1p-21f * largest;
+    }
+    int id;
+    float at;
+    take<float, VPT>(key, lane, SUMS ? a.k + 1 : a.k, id, at);
+    if constexpr (SUMS) {
+        const float x = id >= 0 ? to_f32(row[id]) : 0.0f;
+        const float b = id >= 0 && a.bias ? __ldg(a.bias + id) : 0.0f;
+        const int idn = __shfl_down_sync(kAll, id, 1);
+        const float atn = __shfl_down_sync(kAll, at, 1), xn = __shfl_down_sync(kAll, x, 1),
+                    bnx = __shfl_down_sync(kAll, b, 1);
+        bool ok = true;
+        if (lane < a.k && id >= 0 && idn >= 0) {
+            const float bound = 2.0f * serr + 0x1p-22f * fmaxf(fabsf(at), fabsf(atn)) + 0x1p-120f;
+            // equal logits and biases have equal keys: the index decides
+            ok = at - atn > bound || (x == xn && b == bnx);
+        }
+        sure = __all_sync(kAll, ok) && sure;
+        if (!sure) id = select64<T, VPT>(row, a, lane, slots[warp]);
+        if (lane >= a.k) id = -1;
+    }
+
+    const bool on = lane < a.k && id >= 0;
+    const float x = on ? to_f32(row[id]) : -INFINITY;
+    float w;
+    if (a.sigmoid) {
+        w = on ? sigmoid(x) : 0.0f;
+        if (a.renormalize) w = w / fmaxf(warp_sum(w), 1e-30f);
+    } else if (a.renormalize) {
+        const float m = warp_max(x);
+        w = on ? expf(x - m) : 0.0f;
+        w = w / fmaxf(warp_sum(w), 1e-30f);
+    } else {
+        w = on ? expf(x - top) * inv : 0.0f;
+    }
+    if (lane < a.k) {
+        w = nan ? NAN : on ? w * a.scale : 0.0f;
+        const long long at_out = (long long)t * a.k + lane;
+        a.ids[at_out] = on ? id : -1;
+        for (int r = 0; r < a.R; ++r) a.w[(long long)r * a.T * a.k + at_out] = w;
+    }
+}
+
+// Gradient of the weights with respect to the logits; the choice of experts
+// (and with it the bias) has none.  With c = scale * sum over the shards of dw:
+//   softmax, renormalised:  dx_j = w_j (c_j - sum_i w_i c_i),  w = softmax over the chosen
+//   softmax:                dx_e = p_e (c_e - sum_j p_j c_j)   for every e (c_e = 0 unless chosen)
+//   sigmoid:                dx_j = c_j s_j (1 - s_j)
+//   sigmoid, renormalised:  c_j is first replaced by (c_j - sum_i (s_i / S) c_i) / S, S = sum of s
+// 1 - s is computed as sigmoid(-x), which keeps its digits near s = 1.  One
+// warp per token: the chosen slots sit on lanes, are scattered into the warp's
+// row in shared memory, and the row is written once with 16-byte stores, so the
+// kernel is bounded by that store stream.
+template <typename T, int VPT, bool DENSE>
+__global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBackwardArgs a)
+{
+    __shared__ __align__(16) float rows[kWarps][32 * VPT];
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int t = blockIdx.x * kWarps + warp;
+    griddep_launch_dependents();
+    griddep_wait();
+    if (t >= a.T) return;
+    const T *row = static_cast<const T *>(a.logits) + (long long)t * a.ld;
+    float *buf = rows[warp];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) buf[j * 32 + lane] = 0.0f;
+    int id = -1;
+    float c = 0.0f;
+    if (lane < a.k) {
+        const long long at = (long long)t * a.k + lane;
+        id = a.ids[at];
+        if (id < -1 || id >= a.E) {
+            atomicOr(a.err, BN_DEVERR_EXPERT_RANGE);
+            id = -1;
+        }
+        if (id >= 0) {
+            for (int r = 0; r < a.R; ++r) c += a.dw[(long long)r * a.T * a.k + at];
+            c *= a.scale;
+        }
+    }
+    const bool on = id >= 0;
+    const float x = on ? to_f32(row[id]) : -INFINITY;
+    __syncwarp();
+    float p[DENSE ? VPT : 1];
+    float dot = 0.0f;
+    if constexpr (DENSE) {
+        load_row<T, VPT>(row, a.E, lane, a.vec, -INFINITY, p);
+        float top = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) top = fmaxf(top, p[j]);
+        top = warp_max(top);
+        float sum = 0.0f;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            p[j] = p[j] == -INFINITY ? 0.0f : expf(p[j] - top);  // NaN stays
+            sum += p[j];
+        }
+        sum = warp_sum(sum);
+        const float inv = sum == 0.0f ? 0.0f : 1.0f / sum;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) p[j] *= inv;
+        dot = warp_sum(on && x != -INFINITY ? expf(x - top) * inv * c : 0.0f);
+        if (on) atomicAdd(buf + id, c);
+    } else {
+        float d;
+        if (a.sigmoid) {
+            const float s = on ? sigmoid(x) : 0.0f;
+            if (a.renormalize) {
+                const float total = fmaxf(warp_sum(s), 1e-30f);
+                c = (c - warp_sum(s / total * c)) / total;
+            }
+            d = on ? c * s * sigmoid(-x) : 0.0f;
+        } else {
+            const float m = warp_max(x);
+            float w = on && x != -INFINITY ? expf(x - m) : 0.0f;
+            w = w / fmaxf(warp_sum(w), 1e-30f);
+            d = w * (c - warp_sum(w * c));
+        }
+        if (on) atomicAdd(buf + id, d);
+    }
+    __syncwarp();
+    T *out = static_cast<T *>(a.dlogits) + (long long)t * a.E;
+    constexpr int W = 16 / (int)sizeof(T);
+    float v[VPT];
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        v[j] = buf[lane * VPT + j];
+        if constexpr (DENSE) v[j] = p[j] * (v[j] - dot);
+    }
+    if constexpr (VPT >= W) {
+        if (a.vec) {
+#pragma unroll
+            for (int q = 0; q < VPT / W; ++q) {
+                union { uint4 u; T e[W]; } pack;
+#pragma unroll
+                for (int j = 0; j < W; ++j) pack.e[j] = from_f32<T>(v[q * W + j]);
+                const int i = lane * VPT + q * W;
+                if (i < a.E) *reinterpret_cast<uint4 *>(out + i) = pack.u;
+            }
+            return;
+        }
+    }
+#pragma unroll
+    for (int j = 0; j < VPT; ++j) {
+        const int i = lane * VPT + j;
+        if (i < a.E) out[i] = from_f32<T>(v[j]);
+    }
+}
+
+template <typename T, int VPT>
+cudaError_t route_vpt(const RouteArgs &a, bool pdl, cudaStream_t st)
+{
+    const dim3 grid((unsigned)((a.T + kWarps - 1) / kWarps)), block(kWarps * 32);
+    const bool sums = a.bias || (a.groups > 1 && a.group_top > 1);
+    if (sums) return launch_kernel(route_kernel<T, VPT, true>, grid, block, 0, pdl, 1, st, a);
+    return launch_kernel(route_kernel<T, VPT, false>, grid, block, 0, pdl, 1, st, a);
+}
+
+template <typename T, int VPT>
+cudaError_t backward_vpt(const RouteBackwardArgs &a, bool pdl, cudaStream_t st)
+{
+    const dim3 grid((unsigned)((a.T + kWarps - 1) / kWarps)), block(kWarps * 32);
+    if (!a.sigmoid && !a.renormalize)
+        return launch_kernel(route_backward_kernel<T, VPT, true>, grid, block, 0, pdl, 1, st, a);
+    return launch_kernel(route_backward_kernel<T, VPT, false>, grid, block, 0, pdl, 1, st, a);
+}
+
+// The smallest power of two of experts per lane that holds the row.
+#define BN_BY_EXPERTS(call, T, a)                     \
+    ((a).E <= 32    ? call<T, 1>(a, pdl, st)          \
+     : (a).E <= 64  ? call<T, 2>(a, pdl, st)          \
+     : (a).E <= 128 ? call<T, 4>(a, pdl, st)          \
+     : (a).E <= 256 ? call<T, 8>(a, pdl, st)          \
+     : (a).E <= 512 ? call<T, 16>(a, pdl, st)         \
+                    : call<T, 32>(a, pdl, st))
+
+}  // namespace
+
+cudaError_t launch_route(const RouteArgs &a, int dtype, bool pdl, cudaStream_t st)
+{
+    if (dtype == 0) return BN_BY_EXPERTS(route_vpt, __nv_bfloat16, a);
+    if (dtype == 1) return BN_BY_EXPERTS(route_vpt, __half, a);
+    return BN_BY_EXPERTS(route_vpt, float, a);
+}
+
+cudaError_t launch_route_backward(const RouteBackwardArgs &a, int dtype, bool pdl, cudaStream_t st)
+{
+    if (dtype == 0) return BN_BY_EXPERTS(backward_vpt, __nv_bfloat16, a);
+    if (dtype == 1) return BN_BY_EXPERTS(backward_vpt, __half, a);
+    return BN_BY_EXPERTS(backward_vpt, float, a);
+}
+
+}  // namespace bn

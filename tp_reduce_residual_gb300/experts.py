@@ -1,0 +1,289 @@
+"""Python binding of the operators around the experts of a mixture-of-experts layer.
+
+``route`` chooses each token's experts and weights from the router's logits
+(``route_backward`` is its gradient), ``plan`` groups the token slots by expert,
+``quantize_fp4`` / ``dequantize_fp4`` take rows to 4-bit microscaled floating
+point and back, and ``expert_product`` multiplies grouped rows with each
+expert's weights.  ``plan(...).perm``, ``route(...)``'s weights and the product
+are what ``beamnorm.finalize_reduce_norm`` takes.
+
+As in ``beamnorm``, a function checks its arguments, then calls the C entry
+point with raw device pointers and the current CUDA stream; the arithmetic runs
+in the library's kernels and there is no fallback.
+"""
+from __future__ import annotations
+
+import ctypes
+from dataclasses import dataclass
+from typing import NamedTuple, Optional
+
+import torch
+
+from . import beamnorm as _bn
+
+SCORES = {"softmax": 0, "sigmoid": 1}
+FORMATS = {"nvfp4": 0, "mxfp4": 1}
+#: values along a row that share a scale
+BLOCK = {"nvfp4": 16, "mxfp4": 32}
+_CHUNK = {"nvfp4": 64, "mxfp4": 128}   # values along a row in one scale tile
+_DTYPES = {torch.bfloat16: 0, torch.float16: 1, torch.float32: 2}
+
+_FLOAT32, _INT32, _UINT8 = torch.float32, torch.int32, torch.uint8
+
+
+class Plan(NamedTuple):
+    """Where token slots go when they are grouped by expert: perm [R,T,k] the
+    place of each slot, offsets [E+1] the groups' first places, rows [T*k] the
+    token at each place (all int32)."""
+    perm: torch.Tensor
+    offsets: torch.Tensor
+    rows: torch.Tensor
+
+
+@dataclass
+class FP4:
+    """Quantised rows: ``data`` uint8 [..., K/2] (element 2i in the low half of
+    byte i) and ``scales`` uint8 [tiles, chunks, 512] in the layout that
+    ``include/beamnorm.h`` describes at bn_fp4_scale_bytes.  ``offsets`` are the
+    ragged groups' first rows (int32 [groups+1]) or None: one group per leading
+    index of a 3-D ``data``, one group for a 2-D one."""
+    data: torch.Tensor
+    scales: torch.Tensor
+    format: str
+    offsets: Optional[torch.Tensor] = None
+    tensor_scale: float = 1.0
+
+    @property
+    def shape(self):
+        return (*self.data.shape[:-1], 2 * self.data.shape[-1])
+
+
+def _call(fn, args, t, stream):
+    """One C call with the tensor's device current, on ``stream`` or the current one."""
+    if stream is None:
+        stream = torch.cuda.current_stream(t.device).cuda_stream
+    else:
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
+    if t.device.index == torch.cuda.current_device():
+        status = fn(*args, stream)
+    else:
+        with torch.cuda.device(t.device):
+            status = fn(*args, stream)
+    if status:
+        _bn._check(status)
+
+
+def _name(table, value, what):
+    if value not in table:
+        raise ValueError(f"{what} must be one of {', '.join(table)} (got {value!r})")
+    return table[value]
+
+
+def _dtype(t, name, fp32=True):
+    d = _DTYPES.get(t.dtype)
+    if d is None or (d == 2 and not fp32):
+        raise TypeError(f"{name} must be torch.bfloat16, torch.float16{' or torch.float32' if fp32 else ''} (got {t.dtype})")
+    return d
+
+
+def _rows2d(t, name):
+    """A 2-D CUDA tensor whose rows are contiguous; returns its row stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
+    if t.dim() != 2:
+        raise ValueError(f"{name} must have 2 dimensions (got {t.dim()})")
+    T, n = t.shape
+    if n > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    ld = t.stride(0) if T > 1 else n
+    if ld < n:
+        raise ValueError(f"{name} must have rows that do not overlap (row stride {ld} below {n})")
+    return ld
+
+
+def route(logits, k: int, bias=None, score: str = "softmax", groups: int = 1, top_groups: int = 1,
+          group_top: int = 1, renormalize: bool = True, scale: float = 1.0, shards: int = 1,
+          ids=None, w=None, stream=None):
+    """Each token's k experts and their weights: ``(ids [T,k] int32, w [shards,T,k] FP32)``.
+
+    ``logits`` [T,E] BF16, FP16 or FP32 (any row stride).  Experts rank by
+    score + ``bias`` [E] (FP32, for the choice only), equal ones by index;
+    weights are the scores (``renormalize``: over their sum) times ``scale``.
+    With ``groups`` > 1 only the ``top_groups`` groups of consecutive experts
+    with the largest sum of their ``group_top`` (1 or 2) best are left.  Logits
+    of -inf take experts out; slots without an expert get id -1, weight 0."""
+    ld = _rows2d(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    dtype = _dtype(logits, "logits")
+    if ids is None:
+        ids = torch.empty((T, k), dtype=_INT32, device=dev)
+    if w is None:
+        w = torch.empty((shards, T, k), dtype=_FLOAT32, device=dev)
+    args = (logits.data_ptr(), dtype, ld, T, E, int(k), _bn._opt(bias, "bias", _FLOAT32, (E,), dev),
+            _name(SCORES, score, "score"), int(groups), int(top_groups), int(group_top),
+            1 if renormalize else 0, float(scale), int(shards),
+            _bn._need(ids, "ids", _INT32, (T, k), dev), _bn._need(w, "w", _FLOAT32, (shards, T, k), dev))
+    _call(_bn.load().bn_route, args, logits, stream)
+    return ids, w
+
+
+def route_backward(logits, ids, dw, score: str = "softmax", renormalize: bool = True,
+                   scale: float = 1.0, dlogits=None, stream=None) -> torch.Tensor:
+    """Gradient of ``route``'s weights: dlogits [T,E] in the logits' dtype from
+    ``dw`` [shards,T,k] FP32 (summed over the shards) and the chosen ``ids``."""
+    ld = _rows2d(logits, "logits")
+    T, E = logits.shape
+    dev = logits.device
+    dtype = _dtype(logits, "logits")
+    if not isinstance(dw, torch.Tensor) or dw.dim() != 3:
+        raise ValueError("dw must be a tensor of 3 dimensions [shards, T, k]")
+    R, _, k = dw.shape
+    if dlogits is None:
+        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
+    args = (logits.data_ptr(), dtype, ld, T, E, k, _bn._need(ids, "ids", _INT32, (T, k), dev),
+            _bn._need(dw, "dw", _FLOAT32, (R, T, k), dev), R, _name(SCORES, score, "score"),
+            1 if renormalize else 0, float(scale), _bn._need(dlogits, "dlogits", logits.dtype, (T, E), dev))
+    _call(_bn.load().bn_route_backward, args, logits, stream)
+    return dlogits
+
+
+def plan(ids, experts: int, shards: int = 1, perm=None, offsets=None, rows=None, stream=None) -> Plan:
+    """Group the slots of ``ids`` [T,k] by expert, in slot order within each;
+    slots with id -1 come last.  ``perm`` is repeated for ``shards`` shards."""
+    if not isinstance(ids, torch.Tensor) or ids.dim() != 2:
+        raise ValueError("ids must be a tensor of 2 dimensions [T, k]")
+    T, k = ids.shape
+    dev = ids.device
+    E = int(experts)
+    args = (_bn._need(ids, "ids", _INT32, (T, k), dev), T, k, E, int(shards))
+    if perm is None:
+        perm = torch.empty((shards, T, k), dtype=_INT32, device=dev)
+    if offsets is None:
+        offsets = torch.empty((E + 1,), dtype=_INT32, device=dev)
+    if rows is None:
+        rows = torch.empty((T * k,), dtype=_INT32, device=dev)
+    args += (_bn._need(perm, "perm", _INT32, (shards, T, k), dev),
+             _bn._need(offsets, "offsets", _INT32, (E + 1,), dev),
+             _bn._need(rows, "rows", _INT32, (T * k,), dev))
+    _call(_bn.load().bn_expert_plan, args, ids, stream)
+    return Plan(perm, offsets, rows)
+
+
+def fp4_scales_shape(M: int, K: int, format: str, groups: int = 1, ragged: bool = False):
+    """Shape of the scales of M rows of K values: [tiles, chunks, 512]."""
+    tiles = M // 128 + groups + 1 if ragged else groups * (-(-(M // groups) // 128))
+    return tiles, -(-K // _CHUNK[format]), 512
+
+
+def _layout(q: FP4, name: str):
+    """(M, K, groups, offsets pointer) of quantised rows, after checks."""
+    if not isinstance(q, FP4):
+        raise TypeError(f"{name} must be an FP4")
+    _name(FORMATS, q.format, "format")
+    data = q.data
+    if data.dim() not in (2, 3) or (data.dim() == 3 and q.offsets is not None):
+        raise ValueError(f"{name}.data must be [M, K/2], or [groups, rows, K/2] without offsets")
+    dev = data.device
+    _bn._need(data, f"{name}.data", _UINT8, data.shape, dev)
+    K = 2 * data.shape[-1]
+    groups = data.shape[0] if data.dim() == 3 else 1
+    M = groups * data.shape[-2] if data.dim() == 3 else data.shape[0]
+    op = None
+    if q.offsets is not None:
+        groups = q.offsets.numel() - 1
+        op = _bn._need(q.offsets, f"{name}.offsets", _INT32, (groups + 1,), dev)
+    _bn._need(q.scales, f"{name}.scales", _UINT8,
+              fp4_scales_shape(M, K, q.format, max(groups, 1), op is not None), dev)
+    return M, K, groups, op
+
+
+def quantize_fp4(x, format: str, rows=None, offsets=None, tensor_scale: float = 1.0,
+                 data=None, scales=None, stream=None) -> FP4:
+    """Rows of ``x`` ([n,K], or [groups,n,K] such as weights; BF16 or FP16) in
+    4-bit floating point.  ``rows`` (int32 [M]) picks the rows, ``offsets``
+    (int32 [groups+1]) are the ragged groups of the result, as ``plan`` gives
+    them; ``tensor_scale`` is a power of two."""
+    fmt = _name(FORMATS, format, "format")
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    dev = x.device
+    lead = None
+    if x.dim() == 3:
+        if rows is not None or offsets is not None:
+            raise ValueError("a 3-D x has equal groups: it takes neither rows nor offsets")
+        if not x.is_contiguous():
+            raise ValueError("a 3-D x must be contiguous")
+        lead = x.shape[:2]
+        x = x.view(-1, x.shape[2])
+    ld = _rows2d(x, "x")
+    n, K = x.shape
+    if n <= 1:
+        ld = -(-K // 8) * 8
+    dtype = _dtype(x, "x", fp32=False)
+    M, rp = n, None
+    if rows is not None:
+        M = rows.numel()
+        rp = _bn._need(rows, "rows", _INT32, (M,), dev)
+    groups, op = 1, None
+    if offsets is not None:
+        groups = offsets.numel() - 1
+        op = _bn._need(offsets, "offsets", _INT32, (groups + 1,), dev)
+    elif lead is not None:
+        groups = lead[0]
+    if K % 32 or K == 0:
+        raise ValueError(f"x has rows of {K} values, not a positive multiple of 32")
+    if M and groups < 1:
+        raise ValueError("offsets must have 2 entries or more")
+    dshape = (*lead, K // 2) if lead is not None else (M, K // 2)
+    sshape = fp4_scales_shape(M, K, format, max(groups, 1), op is not None)
+    if data is None:
+        data = torch.empty(dshape, dtype=_UINT8, device=dev)
+    if scales is None:
+        scales = torch.empty(sshape, dtype=_UINT8, device=dev)
+    args = (x.data_ptr(), dtype, ld, n, rp, M, K, op, max(groups, 1), fmt, float(tensor_scale),
+            _bn._need(data, "data", _UINT8, dshape, dev), _bn._need(scales, "scales", _UINT8, sshape, dev))
+    _call(_bn.load().bn_quantize_fp4, args, x, stream)
+    return FP4(data, scales, format, offsets, float(tensor_scale))
+
+
+def dequantize_fp4(q: FP4, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """The values of quantised rows ([..., K]) in BF16, FP16 or FP32."""
+    M, K, groups, op = _layout(q, "q")
+    dev = q.data.device
+    if out is None:
+        out = torch.empty(q.shape, dtype=dtype, device=dev)
+    d = _dtype(out, "out")
+    args = (q.data.data_ptr(), q.scales.data_ptr(), M, K, op, max(groups, 1), FORMATS[q.format],
+            float(q.tensor_scale), _bn._need(out, "out", out.dtype, q.shape, dev), d)
+    _call(_bn.load().bn_dequantize_fp4, args, q.data, stream)
+    return out
+
+
+def expert_product(a: FP4, w: FP4, scale: float = 1.0, out=None, stream=None) -> torch.Tensor:
+    """out [M,N] BF16: each row of ``a`` ([M,K], grouped by ``a.offsets``) times
+    its group's weights of ``w`` ([E,N,K]; [N,K] is one expert), times ``scale``
+    and both tensor scales.  Rows past the last group are zeros."""
+    M, K, groups, op = _layout(a, "a")
+    wM, wK, E, wo = _layout(w, "w")
+    if wo is not None:
+        raise ValueError("w must have equal groups (no offsets)")
+    if a.data.dim() != 2:
+        raise ValueError("a.data must be [M, K/2]")
+    if wK != K or a.format != w.format:
+        raise ValueError(f"a has rows of {K} {a.format} values, w of {wK} {w.format} values")
+    if groups != E:
+        raise ValueError(f"a has {groups} groups, w has {E} experts")
+    dev = a.data.device
+    if w.data.device != dev:
+        raise ValueError(f"w is on {w.data.device}, expected {dev}")
+    N = w.data.shape[-2]
+    if out is None:
+        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
+    args = (a.data.data_ptr(), a.scales.data_ptr(), M, w.data.data_ptr(), w.scales.data_ptr(), E, N, K,
+            op, FORMATS[a.format], float(scale) * a.tensor_scale * w.tensor_scale,
+            _bn._need(out, "out", torch.bfloat16, (M, N), dev))
+    _call(_bn.load().bn_expert_product, args, a.data, stream)
+    return out
