@@ -100,6 +100,8 @@ typedef enum {
 /* Device-side error bits (see bn_check_device_error). */
 #define BN_DEVERR_PERM_RANGE 1u  /* a perm value outside [0, T*k): clamped to 0, never trapped */
 #define BN_DEVERR_TIMEOUT 2u     /* a pipeline wait gave up after its time limit */
+#define BN_DEVERR_EXPERT_RANGE 4u /* an expert id outside [-1, E): taken as -1 */
+#define BN_DEVERR_OFFSETS 8u     /* a group offset outside [0, M] or falling: clamped, the group empty */
 
 typedef struct {
     float *sum;    /* [T, H] FP32, or NULL */
@@ -286,6 +288,124 @@ BN_API bn_status bn_residual_norm_only(const float *sum, int T, int H, uint16_t 
 BN_API bn_status bn_finalize_only(const uint16_t *expert_out, const int32_t *perm,
                            const float *w, const uint16_t *shared,
                            int R, int T, int k, int H, uint16_t *z_out, void *stream);
+
+/* ---- around the experts: routing, plan, 4-bit operands, products ---------- */
+
+/* What a mixture-of-experts layer computes between the router's logits and the
+ * finalize above: which experts each token takes and with which weights
+ * (bn_route, and for training bn_route_backward), the places of the token
+ * slots when they are grouped by expert (bn_expert_plan: perm is the finalize's
+ * perm), the grouped rows in 4-bit microscaled floating point
+ * (bn_quantize_fp4, bn_dequantize_fp4) and their product with each expert's
+ * weights (bn_expert_product: its out is one shard's expert_out).
+ *
+ * The conventions above hold except where stated: logits and gradients need
+ * only their own element's alignment, int32 and FP32 buffers 4 bytes, the
+ * others 16.  With T == 0 or M == 0 nothing is enqueued and pointers are not
+ * examined (bn_expert_plan still writes offsets).  E <= 1024, k <= 16, R <= 16;
+ * T * k < 2^31. */
+
+typedef enum { BN_BF16 = 0, BN_FP16 = 1, BN_FP32 = 2 } bn_dtype;
+typedef enum { BN_SCORE_SOFTMAX = 0, BN_SCORE_SIGMOID = 1 } bn_score;
+
+/* 4-bit formats: codes 0 0.5 1 1.5 2 3 4 6 with a sign, in blocks along K that
+ * share a scale: BN_NVFP4 16 values and an 8-bit float (e4m3), BN_MXFP4 32
+ * values and a power of two (e8m0). */
+typedef enum { BN_NVFP4 = 0, BN_MXFP4 = 1 } bn_fp4;
+
+/* Choose k experts for each token.
+ *   logits   [T, E] of `dtype`, rows `ld` elements apart
+ *   bias     [E] FP32 added to the scores for the choice only, or NULL
+ *   score    s = softmax(logits) or sigmoid(logits)
+ *   groups   E / groups consecutive experts each (at most 32 groups).  A group
+ *            ranks by the sum of its group_top (1 or 2) largest s + bias; only
+ *            the top_groups highest stay.  1: no groups.
+ *   ids      [T, k] int32: the k largest s + bias, falling, equal ones (and
+ *            equal groups) by rising index.  The order is that of exact
+ *            arithmetic on the given logits and biases, up to 64-bit rounding.
+ *   w        [R, T, k] FP32, the same for every shard: scale * s, or
+ *            scale * s / (sum of the k chosen s) with renormalize
+ * A logit or bias of -inf takes its expert out.  Slots without an expert left
+ * get id -1 and weight 0.  A NaN takes its expert out and makes all k weights
+ * of its row NaN.
+ * Source: none -- the pages describe no router; it has no counterpart there. */
+BN_API bn_status bn_route(const void *logits, bn_dtype dtype, long long ld, int T, int E, int k,
+                          const float *bias, bn_score score, int groups, int top_groups,
+                          int group_top, int renormalize, float scale, int R, int32_t *ids,
+                          float *w, void *stream);
+
+/* Gradient of bn_route's weights: dlogits [T, E] (dense, of `dtype`) from dw
+ * [R, T, k] FP32, summed over the shards in order.  The choice itself has no
+ * gradient, nor has the bias.  Slots with id -1 add nothing.  ids outside
+ * [-1, E) set BN_DEVERR_EXPERT_RANGE and add nothing.
+ * Source: none -- it has no counterpart on the pages. */
+BN_API bn_status bn_route_backward(const void *logits, bn_dtype dtype, long long ld, int T, int E,
+                                   int k, const int32_t *ids, const float *dw, int R,
+                                   bn_score score, int renormalize, float scale, void *dlogits,
+                                   void *stream);
+
+/* Group the T * k token slots by expert, keeping their order within each.
+ *   perm     [R, T, k] int32: the place of each slot, the same for every shard
+ *   offsets  [E + 1] int32: expert e has the places offsets[e] .. offsets[e+1]-1
+ *   rows     [T * k] int32: the token at each place
+ * Slots with id -1 come after every group.  ids outside [-1, E) set
+ * BN_DEVERR_EXPERT_RANGE and count as -1.
+ * Source: none -- the pages take the permutation as given; it has no counterpart there. */
+BN_API bn_status bn_expert_plan(const int32_t *ids, int T, int k, int E, int R, int32_t *perm,
+                                int32_t *offsets, int32_t *rows, void *stream);
+
+/* Bytes of the scales of M quantised rows of K values: ragged groups (offsets
+ * given) or equal ones.  0 on invalid arguments.  The scales lie in tiles of 128
+ * rows by 4 scales, 512 bytes each: row r of a tile has its 4 scale bytes at
+ * (r % 32) * 16 + (r / 32) * 4; the tiles of 128 rows follow one another in the
+ * order of K (64 values a tile for BN_NVFP4, 128 for BN_MXFP4).  Group g's row
+ * tiles start at tile (offsets[g] >> 7) + g, or g * ceil(M / groups / 128)
+ * without offsets.  Pure host logic.
+ * Source: no passage: library utility. */
+BN_API size_t bn_fp4_scale_bytes(int M, int K, int groups, int ragged, bn_fp4 format);
+
+/* Quantise rows to 4 bits: row m of the result is row rows[m] (or m) of x.
+ *   x        [x_rows, K] BF16 or FP16, rows `ld` elements apart (ld % 8 == 0)
+ *   rows     [M] int32 or NULL; values outside [0, x_rows) set
+ *            BN_DEVERR_PERM_RANGE and read row 0
+ *   offsets  [groups + 1] int32 (groups <= 1024; rows past the last offset are a
+ *            group of their own) or NULL: equal groups of M / groups rows
+ *   tensor_scale  a power of two in [2^-64, 2^64]; a value is
+ *            code * block scale * tensor_scale
+ *   data     [M, K / 2]: element 2i in the low half of byte i
+ *   scales   bn_fp4_scale_bytes() bytes; places of no row are not written
+ * K is a multiple of 32.  With v = x / tensor_scale, the scale of a block is the e4m3
+ * value next to max|v| / 6, at most 448 (BN_NVFP4), or
+ * 2^(floor(log2 max|v|) - 2) (BN_MXFP4); codes are v / scale to the nearest,
+ * half way to the even code, at most 6, all exactly decided.  A block with an
+ * infinity or a NaN gets a NaN scale and its values are NaN.
+ * Source: none -- it has no counterpart on the pages. */
+BN_API bn_status bn_quantize_fp4(const void *x, bn_dtype dtype, long long ld, int x_rows,
+                                 const int32_t *rows, int M, int K, const int32_t *offsets,
+                                 int groups, bn_fp4 format, float tensor_scale, uint8_t *data,
+                                 uint8_t *scales, void *stream);
+
+/* The values [M, K] of quantised rows, in BF16, FP16 or FP32 (BF16 and FP32
+ * hold every value exactly within their range).
+ * Source: none -- it has no counterpart on the pages. */
+BN_API bn_status bn_dequantize_fp4(const uint8_t *data, const uint8_t *scales, int M, int K,
+                                   const int32_t *offsets, int groups, bn_fp4 format,
+                                   float tensor_scale, void *out, bn_dtype dtype, void *stream);
+
+/* out[m, n] = bf16(alpha * sum over k of a[m, k] * w[e, n, k]) for the rows m of
+ * group e, accumulated in FP32 on the tensor core.
+ *   a, a_scales  M quantised rows, grouped by `offsets`
+ *   w, w_scales  [E, N, K] quantised as E equal groups of N rows
+ *   offsets      [E + 1] int32, or NULL when E == 1 (every row)
+ *   alpha        the product of the operands' tensor scales, and any factor
+ *   out          [M, N] BF16; rows past the last offset are zeros
+ * N is a multiple of 8, K of 32.  Offsets that fall or leave [0, M] set
+ * BN_DEVERR_OFFSETS; they are clamped.
+ * Source: none -- the pages take the experts' rows as given; it has no counterpart there. */
+BN_API bn_status bn_expert_product(const uint8_t *a, const uint8_t *a_scales, int M,
+                                   const uint8_t *w, const uint8_t *w_scales, int E, int N, int K,
+                                   const int32_t *offsets, bn_fp4 format, float alpha,
+                                   uint16_t *out, void *stream);
 
 /* ---- queries and errors ------------------------------------------------ */
 

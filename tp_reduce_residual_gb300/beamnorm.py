@@ -24,7 +24,7 @@ HERE = os.path.dirname(os.path.abspath(__file__))
 LIB_PATH = os.path.join(HERE, "_build", "libbeamnorm.so")
 
 OK, ERR_INVALID, ERR_UNSUPPORTED, ERR_CUDA, ERR_DEVICE = 0, 1, 2, 3, 4
-DEVERR_PERM_RANGE, DEVERR_TIMEOUT = 1, 2
+DEVERR_PERM_RANGE, DEVERR_TIMEOUT, DEVERR_EXPERT_RANGE, DEVERR_OFFSETS = 1, 2, 4, 8
 
 # Every symbol declared in include/beamnorm.h.
 EXPORTS = (
@@ -35,6 +35,8 @@ EXPORTS = (
     "bn_finalize_workspace_bytes", "bn_finalize_reduce_norm_ws",
     "bn_finalize_reduce_residual_norm_ws", "bn_finalize_reduce_norm_noalloc",
     "bn_residual_norm_only", "bn_supports_op", "bn_shutdown",
+    "bn_route", "bn_route_backward", "bn_expert_plan", "bn_fp4_scale_bytes", "bn_quantize_fp4",
+    "bn_dequantize_fp4", "bn_expert_product",
 )
 
 # bn_op values of the entry points, for launch_info()
@@ -84,6 +86,7 @@ _lock = threading.Lock()
 _P = ctypes.c_void_p
 _I = ctypes.c_int
 _F = ctypes.c_float
+_L = ctypes.c_longlong
 
 
 def load() -> ctypes.CDLL:
@@ -123,6 +126,13 @@ def load() -> ctypes.CDLL:
                                                     _P, dbgp, _P, ctypes.c_size_t, _P],
             "bn_finalize_reduce_norm_noalloc": [_P, _P, _P, _P, _I, _I, _I, _I, _P, _P, _P, _F, _P,
                                                 dbgp, _P],
+            "bn_route": [_P, _I, _L, _I, _I, _I, _P, _I, _I, _I, _I, _I, _F, _I, _P, _P, _P],
+            "bn_route_backward": [_P, _I, _L, _I, _I, _I, _P, _P, _I, _I, _I, _F, _P, _P],
+            "bn_expert_plan": [_P, _I, _I, _I, _I, _P, _P, _P, _P],
+            "bn_fp4_scale_bytes": [_I, _I, _I, _I, _I],
+            "bn_quantize_fp4": [_P, _I, _L, _I, _P, _I, _I, _P, _I, _I, _F, _P, _P, _P],
+            "bn_dequantize_fp4": [_P, _P, _I, _I, _P, _I, _I, _F, _P, _I, _P],
+            "bn_expert_product": [_P, _P, _I, _P, _P, _I, _I, _I, _P, _I, _F, _P, _P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -131,6 +141,7 @@ def load() -> ctypes.CDLL:
         L.bn_shutdown.argtypes = []
         L.bn_shutdown.restype = None
         L.bn_finalize_workspace_bytes.restype = ctypes.c_size_t
+        L.bn_fp4_scale_bytes.restype = ctypes.c_size_t
         L.bn_last_error.restype = ctypes.c_char_p
         L.bn_status_string.restype = ctypes.c_char_p
         _lib = L

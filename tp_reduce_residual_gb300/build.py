@@ -1,8 +1,8 @@
 """Build libbeamnorm.so in-tree for sm_103a (GB300).
 
 Nine objects, one per kernel mode, are compiled from one template source in
-parallel, plus the small-T finalize object, the static-scratch object and the
-C-ABI object; everything
+parallel, plus the small-T finalize object, the static-scratch object, the
+C-ABI object and the objects of the operators around the experts; everything
 is compiled with ``-fmad=false`` so that the FP32 epilogue is never
 contracted into FMAs ("Fuse Beam's TP all-reduce with its sandwich norms",
 "Details", "Build" bullet).  nvcc cross-compiles without a GPU.  The result is
@@ -47,8 +47,12 @@ MODES = {
     "resnorm_only": 2 | 8,
 }
 
+# the operators around the experts, one object each
+EXPERTS = ["bn_experts_abi", "bn_route", "bn_plan", "bn_fp4", "bn_product"]
+
 SOURCES = ["bn_device.cuh", "bn_internal.h", "bn_kernels.cu", "bn_abi.cu", "bn_wide.h",
-           "bn_wide.cu", "bn_noalloc.cu", "bn_cluster.h", "bn_cluster.cu", "bn_host.h"]
+           "bn_wide.cu", "bn_noalloc.cu", "bn_cluster.h", "bn_cluster.cu", "bn_host.h",
+           "bn_experts.h", *(f"{n}.cu" for n in EXPERTS)]
 
 
 def nvcc() -> str:
@@ -105,6 +109,9 @@ def build(force: bool = False, verbose_ptxas: bool = False, jobs: int = 0) -> st
     noalloc_obj = os.path.join(OUT_DIR, "bn_noalloc.o")
     cmds.append([cc, *ARCH, *NVCC_FLAGS, *inc, "-c", os.path.join(CSRC, "bn_noalloc.cu"),
                  "-o", noalloc_obj])
+    for name in EXPERTS:
+        cmds.append([cc, *ARCH, *NVCC_FLAGS, *extra, *inc, "-c", os.path.join(CSRC, f"{name}.cu"),
+                     "-o", os.path.join(OUT_DIR, f"{name}.o")])
     jobs = jobs or min(len(cmds), max(1, os.cpu_count() or 1))
     logs = []
     with cf.ThreadPoolExecutor(max_workers=jobs) as ex:

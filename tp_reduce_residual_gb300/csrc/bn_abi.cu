@@ -1309,9 +1309,11 @@ bn_status bn_check_device_error(void *stream, unsigned *bits)
     }
     if (bits) *bits = v;
     if (v != 0)
-        return fail(BN_ERR_DEVICE, "device error bits 0x%x%s%s", v,
+        return fail(BN_ERR_DEVICE, "device error bits 0x%x%s%s%s%s", v,
                     (v & BN_DEVERR_PERM_RANGE) ? " (perm index out of range)" : "",
-                    (v & BN_DEVERR_TIMEOUT) ? " (pipeline wait timed out)" : "");
+                    (v & BN_DEVERR_TIMEOUT) ? " (pipeline wait timed out)" : "",
+                    (v & BN_DEVERR_EXPERT_RANGE) ? " (expert id out of range)" : "",
+                    (v & BN_DEVERR_OFFSETS) ? " (group offsets out of range)" : "");
     return BN_OK;
 }
 
