@@ -40,6 +40,15 @@ constexpr int kThreads = 192;           // producer, product, 4 output warps
 constexpr int kTmemColumns = 512;       // two accumulators, scales from column 256 on
 constexpr int kScaleColumn = 256;
 
+// One thread of a converged warp.  The product's and the copies' operands live in
+// uniform registers; behind elect.sync the compiler knows that one thread runs.
+__device__ __forceinline__ bool elect_one()
+{
+    uint32_t e;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
+    return e != 0;
+}
+
 struct Sched {
     int tiles_f;      // feature tiles of an expert
     long long total;  // tiles of all experts
@@ -141,7 +150,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     __shared__ int abort_flag;
     int *start = reinterpret_cast<int *>(raw + (base - smem_addr(raw)) + kStagesP * kStageBytes);
     int *cum = start + p.E + 1;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+    const int warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     const uint32_t full = smem_addr(bars), empty = full + 8 * kStagesP, acc_full = empty + 8 * kStagesP,
                    acc_empty = acc_full + 16, done = acc_empty + 16;
 
@@ -212,7 +221,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     constexpr int kChunksPerStage = MX ? 2 : 4;
 
     if (warp == 0) {
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t it = 0;  // stages filled
             bool ok = true;
             for (long long id = blockIdx.x; ok && id < sched.total; id += gridDim.x) {
@@ -243,7 +252,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (lane == 0) {
+        if (elect_one()) {
             uint32_t it = 0, n = 0;
             bool ok = true;
             for (long long id = blockIdx.x; ok && id < sched.total; id += gridDim.x, ++n) {
@@ -265,18 +274,27 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                     fence_after();
                     const uint32_t at = base + s * kStageBytes;
                     const uint32_t sa = tmem + kScaleColumn + (it & 1u) * 32u, sb = sa + 16u;
-                    const int nc = min(kChunksPerStage, p.chunks - k * kChunksPerStage);
-                    for (int c = 0; c < nc; ++c) {
-                        copy_scales(sa + 4 * c, scales_desc(at + kOffSA + 512 * c));
-                        copy_scales(sb + 4 * c, scales_desc(at + kOffSB + 512 * c));
-                    }
-                    const int steps = min(4, (p.K - k * 256 + 63) / 64);
                     const uint64_t da = codes_desc(at), db = codes_desc(at + kOffB);
-                    for (int j = 0; j < steps; ++j) {
+                    const uint64_t dsa = scales_desc(at + kOffSA), dsb = scales_desc(at + kOffSB);
+                    auto scales = [&](int c) {
+                        copy_scales(sa + 4 * c, dsa + 32 * c);
+                        copy_scales(sb + 4 * c, dsb + 32 * c);
+                    };
+                    auto step = [&](int j) {
                         const uint32_t col = MX ? 4 * (j >> 1) : 4 * j;
                         const uint32_t half = MX ? (j & 1u) * 2u : 0u;  // which 2 of the 4 scale bytes
                         product<MX>(d, da + 2 * j, db + 2 * j, idesc | (half << 4) | (half << 29), sa + col, sb + col,
                                     k > 0 || j > 0);
+                    };
+                    if (k * 256 + 256 <= p.K) {  // unrolled: the issuing thread sets the pace
+#pragma unroll
+                        for (int c = 0; c < kChunksPerStage; ++c) scales(c);
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) step(j);
+                    } else {
+                        const int nc = p.chunks - k * kChunksPerStage, steps = (p.K - k * 256 + 63) / 64;
+                        for (int c = 0; c < nc; ++c) scales(c);
+                        for (int j = 0; j < steps; ++j) step(j);
                     }
                     commit(empty + 8 * s);
                 }
