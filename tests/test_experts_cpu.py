@@ -107,6 +107,7 @@ def test_dequantize_refuses(L, kw, status, needle):
     (dict(offsets=None), 1, "offsets is NULL"), (dict(offsets=at(4) + 2), 1, "offsets is not"), (dict(alpha=math.inf), 1, "alpha"),
     (dict(a=at(0) + 8), 1, "a is not 16-byte"), (dict(w=None), 1, "w is NULL"), (dict(out=at(2)), 1, "out overlaps w"),
     (dict(out=at(0)), 1, "out overlaps a"), (dict(E=1024, N=2 ** 21), 2, "E*N"), (dict(format=9), 1, "format"),
+    (dict(E=1024, N=2 ** 20, K=2 ** 20), 2, "scale tiles"),
 ])
 def test_product_refuses(L, kw, status, needle):
     a = dict(a=at(0), a_scales=at(1), M=8, w=at(2), w_scales=at(3), E=4, N=64, K=64, offsets=at(4), format=0, alpha=1.0, out=at(5),

@@ -70,6 +70,7 @@ struct ProductArgs {
     int M, E, N, K;
     const int32_t *offsets;   // [E + 1] or null (E = 1, all rows)
     const uint8_t *a_scales, *w_scales;
+    long long a_tiles;        // row tiles of a_scales
     int chunks;               // scale chunks of 512 bytes per row tile
     float alpha;
     uint16_t *out;            // [M, N] BF16

@@ -320,6 +320,10 @@ bn_status bn_expert_product(const uint8_t *a, const uint8_t *a_scales, int M, co
     if (E > kMaxExperts) return fail(BN_ERR_UNSUPPORTED, "E=%d above the served maximum %d", E, kMaxExperts);
     if ((long long)E * N >= (1LL << 31))
         return fail(BN_ERR_UNSUPPORTED, "E*N=%lld weight rows do not fit int32", (long long)E * N);
+    const int chunks = (K + (format == BN_MXFP4 ? 127 : 63)) / (format == BN_MXFP4 ? 128 : 64);
+    const long long a_tiles = scale_tiles(M, E, offsets != nullptr), w_tiles = (long long)E * ((N + 127) / 128);
+    if ((a_tiles > w_tiles ? a_tiles : w_tiles) * chunks >= (1LL << 31))
+        return fail(BN_ERR_UNSUPPORTED, "M=%d, E=%d, N=%d, K=%d: the scale tiles do not fit int32", M, E, N, K);
     if (M == 0) return BN_OK;
     BN_TRY(check_ptr16(a, "a"));
     BN_TRY(check_ptr16(a_scales, "a_scales"));
@@ -342,8 +346,9 @@ bn_status bn_expert_product(const uint8_t *a, const uint8_t *a_scales, int M, co
     p.K = K;
     p.offsets = offsets;
     p.a_scales = a_scales;
+    p.a_tiles = a_tiles;
     p.w_scales = w_scales;
-    p.chunks = (K + (format == BN_MXFP4 ? 127 : 63)) / (format == BN_MXFP4 ? 128 : 64);
+    p.chunks = chunks;
     p.alpha = alpha;
     p.out = out;
     p.err = d->err;

@@ -5,14 +5,19 @@
 // with a and w codes times block scales (bn_fp4.cu), summed in 32 bits by the
 // tensor core.  Rows past the last group are written as zeros.
 //
-// The tensor core computes a tile of 128 output features by up to 128 rows:
-// weights are the M operand, rows the N operand, so that the few rows an expert
-// has in a decode batch cost a narrow tile (N = 16 upwards) and each weight is
-// read once.  Persistent CTAs, one per SM, walk the tiles; six stages of 256
-// values of K are filled by TMA (codes, 128-byte swizzle) and bulk copies
+// Weights are the tensor core's M operand and rows its N operand, so that the few
+// rows an expert has in a decode batch cost a narrow product (N = 16 upwards)
+// and each weight is read once.  Persistent CTAs walk the output tiles; stages of
+// 256 values of K are filled by TMA (codes, 128-byte swizzle) and bulk copies
 // (scales), one thread copies scales to tensor memory and issues the products
-// (tcgen05, block-scaled), four warps read the accumulators (two of 128 columns,
-// so that a tile's output overlaps the next one's product), scale and store.
+// (tcgen05, block-scaled), the output warps take the accumulator out as BF16,
+// hand it back, and store it.
+//
+// Two shapes.  One CTA: tiles of 128 features by 128 rows, two accumulators.  A
+// pair of CTAs (cta_group::2): tiles of 256 features by 256 rows, of which each
+// CTA loads half the weights and half the rows; twice the products for the same
+// bytes, because what bounds large groups is the filling of shared memory from
+// L2 (64 bytes a cycle and SM).
 #include <mutex>
 
 #include <cuda.h>
@@ -28,17 +33,28 @@ using namespace dev;
 namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
-constexpr int kTile = 128;              // features, and rows, of an output tile
+constexpr int kHalf = 128;              // features, and at most rows, that one CTA loads for a tile
 constexpr int kTileBytes = 128;         // codes of a stage: 256 values of K
-constexpr int kBoxRows = 32;            // rows of one TMA box of the row operand
-constexpr int kStagesP = 6;
-constexpr int kOffB = kTile * kTileBytes;
-constexpr int kOffSA = 2 * kTile * kTileBytes;
-constexpr int kOffSB = kOffSA + 2048;
-constexpr int kStageBytes = kOffSB + 2048;
-constexpr int kThreads = 192;           // producer, product, 4 output warps
-constexpr int kTmemColumns = 512;       // two accumulators, scales from column 256 on
+constexpr int kBoxRows = 32;            // rows of the smaller TMA box of the row operand
+constexpr int kTmemColumns = 512;       // accumulators, scales from column 256 on
 constexpr int kScaleColumn = 256;
+
+template <bool PAIR>
+struct Shape {
+    static constexpr int kCtas = PAIR ? 2 : 1;
+    static constexpr int kTile = PAIR ? 256 : 128;  // features, and rows, of an output tile
+    static constexpr int kAccs = PAIR ? 1 : 2;      // accumulators of kTile columns
+    static constexpr int kStep = PAIR ? 32 : 16;    // rows of a product are rounded up to this
+    static constexpr int kStages = PAIR ? 5 : 6;
+    static constexpr int kRowAtoms = kTile / 128;   // scale tiles of the row operand
+    static constexpr int kOffB = kHalf * kTileBytes;
+    static constexpr int kOffSA = 2 * kHalf * kTileBytes;
+    static constexpr int kOffSB = kOffSA + 2048;
+    static constexpr int kStageBytes = kOffSB + kRowAtoms * 2048;
+    static constexpr int kOutWarps = PAIR ? 8 : 4;
+    static constexpr int kThreads = 64 + 32 * kOutWarps;  // copies, products, output
+    static constexpr int kScaleStride = 16 + 16 * kRowAtoms;  // tensor memory columns of a stage's scales
+};
 
 // One thread of a converged warp.  The product's and the copies' operands live in
 // uniform registers; behind elect.sync the compiler knows that one thread runs.
@@ -48,6 +64,11 @@ __device__ __forceinline__ bool elect_one()
     asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
     return e != 0;
 }
+
+struct Maps {
+    CUtensorMap a, a_small, w;   // codes: boxes of 128 (a_small: 32) rows by 128 bytes
+    CUtensorMap a_scales, w_scales;  // scale tiles: boxes of a stage's by 512 bytes
+};
 
 struct Sched {
     int tiles_f;      // feature tiles of an expert
@@ -60,6 +81,7 @@ struct Tile {
 
 // Tile `id`: experts in order; of one expert, the row tiles of a feature tile
 // next to each other, so that CTAs that run together share its weights in L2.
+template <int TILE>
 __device__ __forceinline__ Tile tile_of(long long id, const Sched &s, const int *start, const int *cum, int E)
 {
     const int tt = (int)(id / s.tiles_f);
@@ -74,17 +96,25 @@ __device__ __forceinline__ Tile tile_of(long long id, const Sched &s, const int 
     t.e = lo;
     t.f = local / nt;
     const int r = local % nt;
-    t.row0 = start[lo] + r * kTile;
-    t.rows = min(kTile, start[lo + 1] - t.row0);
-    t.stile = (start[lo] >> 7) + lo + r;
+    t.row0 = start[lo] + r * TILE;
+    t.rows = min(TILE, start[lo + 1] - t.row0);
+    t.stile = (start[lo] >> 7) + lo + r * (TILE / 128);
     return t;
 }
 
+// A box into this CTA's shared memory; its bytes count on `bar`, which for a
+// pair is the first CTA's.
+template <bool PAIR>
 __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
 {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-        "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
 }
 
 // Shared-memory operand descriptors.  Codes: rows of 128 bytes, 128-byte
@@ -99,33 +129,55 @@ __device__ __forceinline__ uint64_t scales_desc(uint32_t addr)
     return (uint64_t)((addr & 0x3ffffu) >> 4) | (1ull << 16) | (8ull << 32) | (1ull << 46);
 }
 
+// The tensor core's instructions, for one CTA or issued once for a pair.
+template <bool PAIR>
 __device__ __forceinline__ void copy_scales(uint32_t tmem, uint64_t desc)
 {
-    asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    if constexpr (PAIR)
+        asm volatile("tcgen05.cp.cta_group::2.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
+    else
+        asm volatile("tcgen05.cp.cta_group::1.32x128b.warpx4 [%0], %1;" ::"r"(tmem), "l"(desc) : "memory");
 }
 
-template <bool MX>
+#define BN_PRODUCT(group, vec)                                                                                \
+    asm volatile(                                                                                             \
+        "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"                                                     \
+        "tcgen05.mma.cta_group::" group ".kind::mxf4nvf4.block_scale.scale_vec::" vec                         \
+        " [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb),      \
+        "r"((uint32_t)accumulate) : "memory")
+
+template <bool MX, bool PAIR>
 __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t sa,
                                         uint32_t sb, bool accumulate)
 {
-    if constexpr (MX)
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::2X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-                "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)accumulate) : "memory");
-    else
-        asm volatile(
-            "{\n\t.reg .pred p;\n\tsetp.ne.u32 p, %6, 0;\n\t"
-            "tcgen05.mma.cta_group::1.kind::mxf4nvf4.block_scale.scale_vec::4X [%0], %1, %2, %3, [%4], [%5], p;\n\t}" ::
-                "r"(d), "l"(a), "l"(b), "r"(idesc), "r"(sa), "r"(sb), "r"((uint32_t)accumulate) : "memory");
+    if constexpr (PAIR && MX) BN_PRODUCT("2", "2X");
+    else if constexpr (PAIR) BN_PRODUCT("2", "4X");
+    else if constexpr (MX) BN_PRODUCT("1", "2X");
+    else BN_PRODUCT("1", "4X");
 }
+#undef BN_PRODUCT
 
+// Arrive on `bar` (of both CTAs of a pair) when every product so far has ended.
+template <bool PAIR>
 __device__ __forceinline__ void commit(uint32_t bar)
 {
-    asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    if constexpr (PAIR)
+        asm volatile(
+            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
+            "h"((uint16_t)3) : "memory");
+    else
+        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+
+// Arrive on a barrier of the pair's first CTA.  What it orders are reads of tensor
+// memory, which the tcgen05 fences cover; a release at cluster scope would wait for
+// the CTA's stores in flight (1350 cycles measured).
+__device__ __forceinline__ void arrive_first(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa(bar, 0)) : "memory");
+}
 
 __device__ __forceinline__ void read16(uint32_t tmem, uint32_t *v)
 {
@@ -138,44 +190,77 @@ __device__ __forceinline__ void read16(uint32_t tmem, uint32_t *v)
         : "r"(tmem) : "memory");
 }
 
-template <bool MX>
-__global__ void __launch_bounds__(kThreads, 1)
-product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant__ CUtensorMap map_w,
-               const __grid_constant__ ProductArgs p)
+// Each lane of eight holds eight rows of its own feature (two a word); after it,
+// lane i holds the eight features of row i.
+__device__ __forceinline__ uint4 transpose8(const uint32_t *w, int lane)
 {
+    uint32_t a[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const uint32_t o = __shfl_xor_sync(kAll, w[i], 1);
+        a[i] = lane & 1 ? __byte_perm(o, w[i], 0x7632) : __byte_perm(w[i], o, 0x5410);
+    }
+    uint32_t b[2][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const uint32_t keep = lane & 2 ? a[2 * i + 1] : a[2 * i];
+        const uint32_t o = __shfl_xor_sync(kAll, lane & 2 ? a[2 * i] : a[2 * i + 1], 2);
+        b[i][0] = lane & 2 ? o : keep;
+        b[i][1] = lane & 2 ? keep : o;
+    }
+    const uint32_t o0 = __shfl_xor_sync(kAll, lane & 4 ? b[0][0] : b[1][0], 4);
+    const uint32_t o1 = __shfl_xor_sync(kAll, lane & 4 ? b[0][1] : b[1][1], 4);
+    return lane & 4 ? make_uint4(o0, o1, b[1][0], b[1][1]) : make_uint4(b[0][0], b[0][1], o0, o1);
+}
+
+template <bool MX, bool PAIR>
+__global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
+product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ ProductArgs p)
+{
+    using S = Shape<PAIR>;
+    constexpr int kStages = S::kStages, kTile = S::kTile;
     extern __shared__ __align__(1024) uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-    __shared__ __align__(8) uint64_t bars[2 * kStagesP + 5];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    int *start = reinterpret_cast<int *>(raw + (base - smem_addr(raw)) + kStagesP * kStageBytes);
+    int *start = reinterpret_cast<int *>(raw + (base - smem_addr(raw)) + kStages * S::kStageBytes);
     int *cum = start + p.E + 1;
     const int warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    const uint32_t full = smem_addr(bars), empty = full + 8 * kStagesP, acc_full = empty + 8 * kStagesP,
-                   acc_empty = acc_full + 16, done = acc_empty + 16;
+    // full: the copies of a stage have landed (a pair's on the first CTA's barrier);
+    // empty: the products have read it
+    const uint32_t full = smem_addr(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, done = acc_empty + 16;
+    const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
+    const int unit = (int)blockIdx.x / S::kCtas, units = (int)gridDim.x / S::kCtas;
 
     griddep_launch_dependents();
     if (threadIdx.x == 0) {
         abort_flag = 0;
-        for (int i = 0; i < kStagesP; ++i) {
+        for (int i = 0; i < kStages; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
-            mbar_init(acc_empty + 8 * i, 128);
+            mbar_init(acc_empty + 8 * i, S::kCtas * S::kOutWarps);
         }
         mbar_init(done, 1);
         fence_mbarrier_init();
     }
     if (warp == 2) {
-        asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
-                     "r"(kTmemColumns) : "memory");
-        asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        if constexpr (PAIR) {
+            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
+                         "r"(kTmemColumns) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
+        } else {
+            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
+                         "r"(kTmemColumns) : "memory");
+            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+        }
     }
     griddep_wait();
     // the groups' first rows and the row tiles before each group
-    for (int e = threadIdx.x; e <= p.E; e += kThreads) {
+    for (int e = threadIdx.x; e <= p.E; e += S::kThreads) {
         const int o = p.offsets ? __ldg(p.offsets + e) : e * p.M;
         if (o < 0 || o > p.M) atomicOr(p.err, BN_DEVERR_OFFSETS);
         start[e] = min(max(o, 0), p.M);
@@ -206,6 +291,7 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
     }
     fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();  // the pair's barriers are ready
     fence_after();
     const uint32_t tmem = tmem_slot;
 
@@ -222,69 +308,91 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
 
     if (warp == 0) {
         if (elect_one()) {
+            const int wtiles = (p.N + 127) / 128;  // scale tiles of one expert
             uint32_t it = 0;  // stages filled
             bool ok = true;
-            for (long long id = blockIdx.x; ok && id < sched.total; id += gridDim.x) {
-                const Tile t = tile_of(id, sched, start, cum, p.E);
-                const int boxes = (t.rows + kBoxRows - 1) / kBoxRows;
-                const uint8_t *sw = p.w_scales + ((long long)t.e * sched.tiles_f + t.f) * p.chunks * 512;
-                const uint8_t *sa = p.a_scales + (long long)t.stile * p.chunks * 512;
+            for (long long id = unit; ok && id < sched.total; id += units) {
+                const Tile t = tile_of<kTile>(id, sched, start, cum, p.E);
+                const int f0 = t.f * kTile + (int)rank * kHalf;
+                // this CTA's rows of the product's N operand: all, or half of the rounded count
+                const int columns = (t.rows + S::kStep - 1) / S::kStep * S::kStep;
+                const int nb = PAIR ? columns / 2 : columns, b0 = t.row0 + (PAIR ? (int)rank * nb : 0);
+                const int boxes = nb > kHalf / 2 ? 0 : (nb + kBoxRows - 1) / kBoxRows;  // 0: one of kHalf rows
+                const uint32_t codes = (uint32_t)(kHalf + (boxes ? boxes * kBoxRows : kHalf)) * kTileBytes;
+                const int atoms = (t.rows + 127) / 128;
+                constexpr uint32_t kScaleBytes = kChunksPerStage * 512;
+                const uint32_t bytes = S::kCtas * (codes + (1 + atoms) * kScaleBytes);
+                // past the last features any scales will do
+                const int sw = (t.e * wtiles + min(f0 / kHalf, wtiles - 1)) * p.chunks;
+                const int sa = t.stile * p.chunks;
                 for (int k = 0; k < nk; ++k, ++it) {
-                    const uint32_t s = it % kStagesP;
-                    if (!wait_phase<false, kPipe>(empty + 8 * s, ((it / kStagesP) & 1u) ^ 1u, ctl)) {
+                    const uint32_t s = it % kStages;
+                    if (!wait_phase<PAIR, kPipe>(empty + 8 * s, ((it / kStages) & 1u) ^ 1u, ctl)) {
                         ok = false;
                         break;
                     }
-                    const uint32_t at = base + s * kStageBytes, bar = full + 8 * s;
-                    const int c0 = k * kChunksPerStage;
-                    const uint32_t sbytes = (uint32_t)min(kChunksPerStage, p.chunks - c0) * 512u;
-                    mbar_arrive_expect_tx(bar, (uint32_t)(kTile + boxes * kBoxRows) * kTileBytes + 2 * sbytes);
-                    tma_2d(at, &map_w, k * kTileBytes, t.e * p.N + t.f * kTile, bar);
+                    const uint32_t at = base + s * S::kStageBytes;
+                    const uint32_t bar = PAIR ? mapa(full + 8 * s, 0) : full + 8 * s;
+                    if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
+                    const int x = k * kTileBytes, c = k * kChunksPerStage;
+                    tma_2d<PAIR>(at, &maps.w, x, t.e * p.N + f0, bar);
+                    if (boxes == 0)
+                        tma_2d<PAIR>(at + S::kOffB, &maps.a, x, b0, bar);
                     for (int b = 0; b < boxes; ++b)
-                        tma_2d(at + kOffB + b * kBoxRows * kTileBytes, &map_a, k * kTileBytes, t.row0 + b * kBoxRows, bar);
-                    bulk_g2s(at + kOffSA, sw + (long long)c0 * 512, sbytes, bar);
-                    bulk_g2s(at + kOffSB, sa + (long long)c0 * 512, sbytes, bar);
+                        tma_2d<PAIR>(at + S::kOffB + b * kBoxRows * kTileBytes, &maps.a_small, x, b0 + b * kBoxRows, bar);
+                    // a row's last stage may fetch the next row tile's scales too: they are not used
+                    tma_2d<PAIR>(at + S::kOffSA, &maps.w_scales, 0, sw + c, bar);
+                    tma_2d<PAIR>(at + S::kOffSB, &maps.a_scales, 0, sa + c, bar);
+                    if (PAIR && atoms > 1)
+                        tma_2d<PAIR>(at + S::kOffSB + 2048, &maps.a_scales, 0, sa + p.chunks + c, bar);
                 }
             }
-            // no copy may be in flight into a CTA that leaves
-            for (uint32_t i = it > kStagesP ? it - kStagesP : 0; i < it; ++i)
-                wait_phase<false, kDrain>(full + 8 * (i % kStagesP), (i / kStagesP) & 1u, ctl);
+            // no copy, and no arrival of a product, may be in flight into a CTA that leaves
+            const uint32_t old = it > kStages ? it - kStages : 0;
+            for (uint32_t i = old; ok && i < it; ++i)
+                ok = wait_phase<PAIR, kPipe>(empty + 8 * (i % kStages), (i / kStages) & 1u, ctl);
+            if (!ok) {  // after a timeout: wait for the copies, and where their barrier is the other CTA's, for a while
+                for (uint32_t i = old; rank == 0 && i < it; ++i)
+                    wait_phase<false, kDrain>(full + 8 * (i % kStages), (i / kStages) & 1u, ctl);
+                for (const long long t0 = clock64(); rank != 0 && clock64() - t0 < (1 << 22);) {}
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
-        if (elect_one()) {
+        // one thread issues the products; of a pair's, the first CTA's
+        if (rank == 0 && elect_one()) {
             uint32_t it = 0, n = 0;
             bool ok = true;
-            for (long long id = blockIdx.x; ok && id < sched.total; id += gridDim.x, ++n) {
-                const Tile t = tile_of(id, sched, start, cum, p.E);
-                const uint32_t buf = n & 1u;
-                if (!wait_phase<false, kPipe>(acc_empty + 8 * buf, ((n >> 1) & 1u) ^ 1u, ctl)) break;
+            for (long long id = unit; ok && id < sched.total; id += units, ++n) {
+                const Tile t = tile_of<kTile>(id, sched, start, cum, p.E);
+                const uint32_t buf = n % S::kAccs;
+                if (!wait_phase<PAIR, kPipe>(acc_empty + 8 * buf, ((n / S::kAccs) & 1u) ^ 1u, ctl)) break;
                 fence_after();
-                const uint32_t columns = (uint32_t)(t.rows + 15) / 16 * 16;
+                const uint32_t columns = (uint32_t)((t.rows + S::kStep - 1) / S::kStep * S::kStep);
                 // E2M1 operands, both with K along the row; E8M0 scales for MXFP4; N / 8, M / 16
                 const uint32_t idesc = (1u << 7) | (1u << 10) | ((columns >> 3) << 17) | ((MX ? 1u : 0u) << 23) |
                                        ((kTile >> 4) << 24);
                 const uint32_t d = tmem + buf * kTile;
+                const bool two = S::kRowAtoms > 1 && columns > 128;
                 for (int k = 0; k < nk; ++k, ++it) {
-                    const uint32_t s = it % kStagesP;
-                    if (!wait_phase<false, kPipe>(full + 8 * s, (it / kStagesP) & 1u, ctl)) {
-                        ok = false;
-                        break;
-                    }
+                    const uint32_t s = it % kStages;
+                    ok = wait_phase<PAIR, kPipe>(full + 8 * s, (it / kStages) & 1u, ctl);
+                    if (!ok) break;
                     fence_after();
-                    const uint32_t at = base + s * kStageBytes;
-                    const uint32_t sa = tmem + kScaleColumn + (it & 1u) * 32u, sb = sa + 16u;
-                    const uint64_t da = codes_desc(at), db = codes_desc(at + kOffB);
-                    const uint64_t dsa = scales_desc(at + kOffSA), dsb = scales_desc(at + kOffSB);
+                    const uint32_t at = base + s * S::kStageBytes;
+                    const uint32_t sa = tmem + kScaleColumn + (it & 1u) * S::kScaleStride, sb = sa + 16u;
+                    const uint64_t da = codes_desc(at), db = codes_desc(at + S::kOffB);
+                    const uint64_t dsa = scales_desc(at + S::kOffSA), dsb = scales_desc(at + S::kOffSB);
                     auto scales = [&](int c) {
-                        copy_scales(sa + 4 * c, dsa + 32 * c);
-                        copy_scales(sb + 4 * c, dsb + 32 * c);
+                        copy_scales<PAIR>(sa + 4 * c, dsa + 32 * c);
+                        copy_scales<PAIR>(sb + 4 * S::kRowAtoms * c, dsb + 32 * c);
+                        if (two) copy_scales<PAIR>(sb + 4 * S::kRowAtoms * c + 4, dsb + 128 + 32 * c);
                     };
                     auto step = [&](int j) {
-                        const uint32_t col = MX ? 4 * (j >> 1) : 4 * j;
+                        const uint32_t c = MX ? j >> 1 : j;
                         const uint32_t half = MX ? (j & 1u) * 2u : 0u;  // which 2 of the 4 scale bytes
-                        product<MX>(d, da + 2 * j, db + 2 * j, idesc | (half << 4) | (half << 29), sa + col, sb + col,
-                                    k > 0 || j > 0);
+                        product<MX, PAIR>(d, da + 2 * j, db + 2 * j, idesc | (half << 4) | (half << 29), sa + 4 * c,
+                                          sb + 4 * S::kRowAtoms * c, k > 0 || j > 0);
                     };
                     if (k * 256 + 256 <= p.K) {  // unrolled: the issuing thread sets the pace
 #pragma unroll
@@ -296,52 +404,77 @@ product_kernel(const __grid_constant__ CUtensorMap map_a, const __grid_constant_
                         for (int c = 0; c < nc; ++c) scales(c);
                         for (int j = 0; j < steps; ++j) step(j);
                     }
-                    commit(empty + 8 * s);
+                    commit<PAIR>(empty + 8 * s);
                 }
-                if (ok) commit(acc_full + 8 * buf);
+                if (ok) commit<PAIR>(acc_full + 8 * buf);
             }
-            commit(done);  // every product has ended before tensor memory is freed
+            commit<PAIR>(done);  // every product has ended before tensor memory is freed
             wait_phase<false, kDrain>(done, 0, ctl);
         }
         __syncwarp();
     } else {
-        const int quad = warp & 3;  // the lanes of tensor memory that this warp reads
+        const int quad = warp & 3;         // the lanes of tensor memory that this warp reads
+        const int half = (warp - 2) >> 2;  // of a pair's columns
         uint32_t n = 0;
-        for (long long id = blockIdx.x; id < sched.total; id += gridDim.x, ++n) {
-            const Tile t = tile_of(id, sched, start, cum, p.E);
-            const uint32_t buf = n & 1u;
-            if (!wait_phase<false, kPipe>(acc_full + 8 * buf, (n >> 1) & 1u, ctl)) break;
+        for (long long id = unit; id < sched.total; id += units, ++n) {
+            const Tile t = tile_of<kTile>(id, sched, start, cum, p.E);
+            const uint32_t buf = n % S::kAccs;
+            // this warp's columns: at most 128
+            const int cut = PAIR ? (t.rows + 31) / 32 * 16 : t.rows;
+            const int lo = half ? cut : 0, hi = half ? t.rows : min(cut, t.rows);
+            if (!wait_phase<PAIR, kPipe>(acc_full + 8 * buf, (n / S::kAccs) & 1u, ctl)) break;
             fence_after();
-            const int f = t.f * kTile + quad * 32 + lane;
-            const bool odd = lane & 1;
-            uint16_t *out = p.out + (long long)(t.row0 + odd) * p.N + (f & ~1);
-            for (int c = 0; c < t.rows; c += 16) {
-                uint32_t v[16];
-                read16(tmem + ((uint32_t)(quad * 32) << 16) + buf * kTile + c, v);
+            // the whole tile as BF16 in registers, so that the next product can start
+            uint32_t packed[8][8];
 #pragma unroll
-                for (int i = 0; i < 16; i += 2) {
-                    // lane pairs trade: the even lane stores two features of row c + i, the odd one of the next
-                    const float x = __uint_as_float(v[i]) * p.alpha, y = __uint_as_float(v[i + 1]) * p.alpha;
-                    const float got = __shfl_xor_sync(kAll, odd ? x : y, 1);
-                    const __nv_bfloat162 h = odd ? __floats2bfloat162_rn(got, y) : __floats2bfloat162_rn(x, got);
-                    if (c + i + odd < t.rows && f < p.N)
-                        *reinterpret_cast<__nv_bfloat162 *>(out + (long long)(c + i) * p.N) = h;
+            for (int b = 0; b < 8; ++b) {
+                if (lo + 16 * b < hi) {
+                    uint32_t v[16];
+                    read16(tmem + ((uint32_t)(quad * 32) << 16) + buf * kTile + lo + 16 * b, v);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const __nv_bfloat162 h = __floats2bfloat162_rn(__uint_as_float(v[2 * i]) * p.alpha,
+                                                                       __uint_as_float(v[2 * i + 1]) * p.alpha);
+                        packed[b][i] = *reinterpret_cast<const uint32_t *>(&h);
+                    }
                 }
             }
             fence_before();
-            mbar_arrive(acc_empty + 8 * buf);
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) arrive_first(acc_empty + 8 * buf);
+                else mbar_arrive(acc_empty + 8 * buf);
+            }
+            const int f = t.f * kTile + (int)rank * kHalf + quad * 32 + (lane & ~7);
+            uint16_t *out = p.out + (long long)(t.row0 + (lane & 7)) * p.N + f;
+#pragma unroll
+            for (int b = 0; b < 8; ++b) {
+                if (lo + 16 * b < hi) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint4 v = transpose8(packed[b] + 4 * h, lane);
+                        const int c = lo + 16 * b + 8 * h;
+                        if (c + (lane & 7) < hi && f < p.N)
+                            *reinterpret_cast<uint4 *>(out + (long long)c * p.N) = v;
+                    }
+                }
+            }
         }
         // rows of no group
         const long long first = (long long)start[p.E] * p.N / 8, last = (long long)p.M * p.N / 8;
-        for (long long i = first + (long long)blockIdx.x * 128 + (threadIdx.x - 64); i < last;
-             i += (long long)gridDim.x * 128)
+        for (long long i = first + (long long)blockIdx.x * (S::kThreads - 64) + (threadIdx.x - 64); i < last;
+             i += (long long)gridDim.x * (S::kThreads - 64))
             reinterpret_cast<uint4 *>(p.out)[i] = make_uint4(0, 0, 0, 0);
     }
     fence_before();
     __syncthreads();
+    if constexpr (PAIR) cluster_sync_all();  // the pair's products read both CTAs' shared memory
     if (warp == 2) {
         fence_after();
-        asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns));
+        if constexpr (PAIR)
+            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns));
+        else
+            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns));
     }
 }
 
@@ -353,16 +486,50 @@ EncodeFn g_encode;
 cudaError_t g_encode_status = cudaErrorUnknown;
 std::once_flag g_encode_once;
 
-// rows of `bytes` bytes, boxes of `box` rows by 128 bytes
-cudaError_t make_map(CUtensorMap *map, const uint8_t *data, long long rows, long long bytes, int box)
+// Rows of `width` elements, boxes of `box` rows by `box_width`.
+cudaError_t make_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *data, long long rows,
+                     long long width, int box, int box_width, CUtensorMapSwizzle swizzle)
 {
-    const cuuint64_t dims[2] = {(cuuint64_t)bytes, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)bytes};
-    const cuuint32_t boxes[2] = {(cuuint32_t)kTileBytes, (cuuint32_t)box}, ones[2] = {1, 1};
-    const CUresult r = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t *>(data), dims, strides, boxes,
-                                ones, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                                CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
+    const cuuint64_t strides[1] = {(cuuint64_t)(width * size)};
+    const cuuint32_t boxes[2] = {(cuuint32_t)box_width, (cuuint32_t)box}, ones[2] = {1, 1};
+    const CUresult r = g_encode(map, type, 2, const_cast<void *>(data), dims, strides, boxes, ones,
+                                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+cudaError_t make_maps(Maps *m, const ProductArgs &p, const uint8_t *a, const uint8_t *w, int fmt)
+{
+    const auto codes = [&](CUtensorMap *map, const uint8_t *data, long long rows, int box) {
+        return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, data, rows, p.K / 2, box, kTileBytes,
+                        CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    const auto scales = [&](CUtensorMap *map, const uint8_t *data, long long tiles) {
+        return make_map(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 8, data, tiles * p.chunks, 64, fmt ? 2 : 4, 64,
+                        CU_TENSOR_MAP_SWIZZLE_NONE);
+    };
+    cudaError_t e = codes(&m->a, a, p.M, kHalf);
+    if (e == cudaSuccess) e = codes(&m->a_small, a, p.M, kBoxRows);
+    if (e == cudaSuccess) e = codes(&m->w, w, (long long)p.E * p.N, kHalf);
+    if (e == cudaSuccess) e = scales(&m->a_scales, p.a_scales, p.a_tiles);
+    if (e == cudaSuccess) e = scales(&m->w_scales, p.w_scales, (long long)p.E * ((p.N + 127) / 128));
+    return e;
+}
+
+template <bool PAIR>
+cudaError_t launch_shape(const ProductArgs &p, const Maps &maps, int fmt, int sms, bool pdl, cudaStream_t st)
+{
+    using S = Shape<PAIR>;
+    const size_t smem = 1024 + (size_t)S::kStages * S::kStageBytes + 2 * sizeof(int) * (size_t)(p.E + 1);
+    auto *k = fmt ? product_kernel<true, PAIR> : product_kernel<false, PAIR>;
+    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (e != cudaSuccess) return e;
+    const long long row_tiles = (long long)p.M / S::kTile + (p.E < p.M ? p.E : p.M);
+    const long long most = row_tiles * ((p.N + S::kTile - 1) / S::kTile);
+    const long long units = sms / S::kCtas;
+    const int grid = (int)(most < units ? most : units) * S::kCtas;
+    return launch_kernel(k, dim3((unsigned)grid), dim3(S::kThreads), smem, pdl, S::kCtas, st, maps, p);
 }
 
 }  // namespace
@@ -379,18 +546,12 @@ cudaError_t launch_product(const ProductArgs &p, const uint8_t *a, const uint8_t
         g_encode = reinterpret_cast<EncodeFn>(fn);
     });
     if (g_encode_status != cudaSuccess) return g_encode_status;
-    CUtensorMap map_a, map_w;
-    cudaError_t e = make_map(&map_a, a, p.M, p.K / 2, kBoxRows);
-    if (e == cudaSuccess) e = make_map(&map_w, w, (long long)p.E * p.N, p.K / 2, kTile);
+    Maps maps;
+    const cudaError_t e = make_maps(&maps, p, a, w, fmt);
     if (e != cudaSuccess) return e;
-    const size_t smem = 1024 + (size_t)kStagesP * kStageBytes + 2 * sizeof(int) * (size_t)(p.E + 1);
-    auto *k = fmt ? product_kernel<true> : product_kernel<false>;
-    e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
-    if (e != cudaSuccess) return e;
-    const long long row_tiles = (long long)p.M / kTile + (p.E < p.M ? p.E : p.M);
-    const long long most = row_tiles * ((p.N + kTile - 1) / kTile);
-    const int grid = (int)(most < sms ? most : sms);
-    return launch_kernel(k, dim3((unsigned)grid), dim3(kThreads), smem, pdl, 1, st, map_a, map_w, p);
+    // Pairs where the average group fills more than one CTA's tile.
+    const bool pair = p.M / p.E > 128 && p.N > 128;
+    return pair ? launch_shape<true>(p, maps, fmt, sms, pdl, st) : launch_shape<false>(p, maps, fmt, sms, pdl, st);
 }
 
 }  // namespace bn
