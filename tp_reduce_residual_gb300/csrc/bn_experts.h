@@ -3,6 +3,7 @@
 // bn_fp4.cu, bn_product.cu).  Not part of the ABI.
 #pragma once
 
+#include <atomic>
 #include <cstdint>
 
 #include <cuda_runtime.h>
@@ -85,6 +86,28 @@ cudaError_t launch_quantize(const QuantArgs &, int dtype, int fmt, int sms, bool
 cudaError_t launch_dequantize(const QuantArgs &, int dtype, int fmt, int sms, bool pdl, cudaStream_t);
 cudaError_t launch_product(const ProductArgs &, const uint8_t *a, const uint8_t *w, int fmt, int sms,
                            bool pdl, cudaStream_t);
+
+// A kernel's attributes, set once per device: dynamic shared memory of up to
+// `bytes`, and clusters of more than 8 CTAs if `wide`.
+class KernelSetup {
+public:
+    template <typename... P>
+    cudaError_t operator()(void (*kernel)(P...), int bytes, bool wide = false)
+    {
+        int dev = 0;
+        cudaError_t e = cudaGetDevice(&dev);
+        if (e != cudaSuccess) return e;
+        const unsigned long long bit = dev < 64 ? 1ull << dev : 0ull;
+        if (done_.load(std::memory_order_acquire) & bit) return cudaSuccess;
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+        if (e == cudaSuccess && wide) e = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+        if (e == cudaSuccess) done_.fetch_or(bit, std::memory_order_release);
+        return e;
+    }
+
+private:
+    std::atomic<unsigned long long> done_{0};
+};
 
 // One launch, with or without programmatic dependent launch.
 template <typename... P, typename... A>

@@ -144,13 +144,11 @@ cudaError_t launch_plan(const PlanArgs &a, bool pdl, cudaStream_t st)
     while (ctas < 16 && (long long)ctas * 512 < a.slots) ctas *= 2;
     const long long share = ((long long)a.slots + ctas * warps - 1) / (ctas * warps);
     const int per_warp = (int)((share + 31) / 32 * 32);
-    const size_t smem = sizeof(unsigned) * ((size_t)warps + 2) * (size_t)(a.E + 1);
-    cudaError_t e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                                         (int)smem);
-    if (e == cudaSuccess && ctas > 8)
-        e = cudaFuncSetAttribute(plan_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1);
+    const auto smem = [&](int E) { return sizeof(unsigned) * ((size_t)warps + 2) * (size_t)(E + 1); };
+    static KernelSetup setup;
+    const cudaError_t e = setup(plan_kernel, (int)smem(kMaxExperts), true);
     if (e != cudaSuccess) return e;
-    return launch_kernel(plan_kernel, dim3((unsigned)ctas), dim3(threads), smem, pdl, ctas, st, a,
+    return launch_kernel(plan_kernel, dim3((unsigned)ctas), dim3(threads), smem(a.E), pdl, ctas, st, a,
                          per_warp);
 }
 

@@ -394,15 +394,20 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         product<MX, PAIR>(d, da + 2 * j, db + 2 * j, idesc | (half << 4) | (half << 29), sa + 4 * c,
                                           sb + 4 * S::kRowAtoms * c, k > 0 || j > 0);
                     };
+                    // each step's scales just before its product: they are copied while the one before runs
+                    constexpr int kSteps = MX ? 2 : 1;  // steps of one scale chunk
                     if (k * 256 + 256 <= p.K) {  // unrolled: the issuing thread sets the pace
 #pragma unroll
-                        for (int c = 0; c < kChunksPerStage; ++c) scales(c);
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) step(j);
+                        for (int j = 0; j < 4; ++j) {
+                            if (j % kSteps == 0) scales(j / kSteps);
+                            step(j);
+                        }
                     } else {
-                        const int nc = p.chunks - k * kChunksPerStage, steps = (p.K - k * 256 + 63) / 64;
-                        for (int c = 0; c < nc; ++c) scales(c);
-                        for (int j = 0; j < steps; ++j) step(j);
+                        const int steps = (p.K - k * 256 + 63) / 64;
+                        for (int j = 0; j < steps; ++j) {
+                            if (j % kSteps == 0) scales(j / kSteps);
+                            step(j);
+                        }
                     }
                     commit<PAIR>(empty + 8 * s);
                 }
@@ -521,15 +526,16 @@ template <bool PAIR>
 cudaError_t launch_shape(const ProductArgs &p, const Maps &maps, int fmt, int sms, bool pdl, cudaStream_t st)
 {
     using S = Shape<PAIR>;
-    const size_t smem = 1024 + (size_t)S::kStages * S::kStageBytes + 2 * sizeof(int) * (size_t)(p.E + 1);
+    const auto smem = [](int E) { return 1024 + (size_t)S::kStages * S::kStageBytes + 2 * sizeof(int) * (size_t)(E + 1); };
+    static KernelSetup setup[2];
     auto *k = fmt ? product_kernel<true, PAIR> : product_kernel<false, PAIR>;
-    const cudaError_t e = cudaFuncSetAttribute(k, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    const cudaError_t e = setup[fmt](k, (int)smem(kMaxExperts));
     if (e != cudaSuccess) return e;
     const long long row_tiles = (long long)p.M / S::kTile + (p.E < p.M ? p.E : p.M);
     const long long most = row_tiles * ((p.N + S::kTile - 1) / S::kTile);
     const long long units = sms / S::kCtas;
     const int grid = (int)(most < units ? most : units) * S::kCtas;
-    return launch_kernel(k, dim3((unsigned)grid), dim3(S::kThreads), smem, pdl, S::kCtas, st, maps, p);
+    return launch_kernel(k, dim3((unsigned)grid), dim3(S::kThreads), smem(p.E), pdl, S::kCtas, st, maps, p);
 }
 
 }  // namespace

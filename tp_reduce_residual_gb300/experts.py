@@ -58,19 +58,43 @@ class FP4:
         return (*self.data.shape[:-1], 2 * self.data.shape[-1])
 
 
-def _call(fn, args, t, stream):
-    """One C call with the tensor's device current, on ``stream`` or the current one."""
+# A decoded token's operators take a few microseconds on the GPU, so the checks
+# below are written for the host's time: an argument that is as it should be passes
+# in one expression, and only one that is not goes through beamnorm's checks for
+# the message.
+_raw_stream = torch._C._cuda_getCurrentRawStream
+
+
+def _call(name, args, index, stream):
+    """One C call with device ``index`` current, on ``stream`` or the current one."""
     if stream is None:
-        stream = torch.cuda.current_stream(t.device).cuda_stream
+        stream = _raw_stream(index)
     else:
         stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
-    if t.device.index == torch.cuda.current_device():
+    fn = getattr(_bn._lib or _bn.load(), name)
+    if index == torch._C._cuda_getDevice():
         status = fn(*args, stream)
     else:
-        with torch.cuda.device(t.device):
+        with torch.cuda.device(index):
             status = fn(*args, stream)
     if status:
         _bn._check(status)
+
+
+def _ptr(t, name, dtype, shape, dev):
+    """The address of a contiguous tensor of this type, shape and device."""
+    if isinstance(t, torch.Tensor) and t.dtype is dtype and t.shape == shape and t.device == dev and t.is_cuda \
+            and t.is_contiguous():
+        return t.data_ptr()
+    return _bn._need(t, name, dtype, tuple(shape), dev)
+
+
+def _out(t, name, dtype, shape, dev):
+    """An output and its address: the caller's, checked, or a new one."""
+    if t is None:
+        t = torch.empty(shape, dtype=dtype, device=dev)
+        return t, t.data_ptr()
+    return t, _ptr(t, name, dtype, shape, dev)
 
 
 def _name(table, value, what):
@@ -88,19 +112,23 @@ def _dtype(t, name, fp32=True):
 
 def _rows2d(t, name):
     """A 2-D CUDA tensor whose rows are contiguous; returns its row stride."""
+    if isinstance(t, torch.Tensor) and t.is_cuda:
+        shape = t.shape
+        if len(shape) == 2:
+            if t.is_contiguous():
+                return shape[1]
+            ld, inner = t.stride()
+            if inner == 1 or shape[1] <= 1:
+                if shape[0] <= 1:
+                    return shape[1]
+                if ld >= shape[1]:
+                    return ld
+                raise ValueError(f"{name} must have rows that do not overlap (row stride {ld} below {shape[1]})")
+            raise ValueError(f"{name} must have contiguous rows")
+        raise ValueError(f"{name} must have 2 dimensions (got {len(shape)})")
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
-    if t.dim() != 2:
-        raise ValueError(f"{name} must have 2 dimensions (got {t.dim()})")
-    T, n = t.shape
-    if n > 1 and t.stride(1) != 1:
-        raise ValueError(f"{name} must have contiguous rows")
-    ld = t.stride(0) if T > 1 else n
-    if ld < n:
-        raise ValueError(f"{name} must have rows that do not overlap (row stride {ld} below {n})")
-    return ld
+    raise ValueError(f"{name} must be a CUDA tensor (got {t.device})")
 
 
 def route(logits, k: int, bias=None, score: str = "softmax", groups: int = 1, top_groups: int = 1,
@@ -118,15 +146,11 @@ def route(logits, k: int, bias=None, score: str = "softmax", groups: int = 1, to
     T, E = logits.shape
     dev = logits.device
     dtype = _dtype(logits, "logits")
-    if ids is None:
-        ids = torch.empty((T, k), dtype=_INT32, device=dev)
-    if w is None:
-        w = torch.empty((shards, T, k), dtype=_FLOAT32, device=dev)
-    args = (logits.data_ptr(), dtype, ld, T, E, int(k), _bn._opt(bias, "bias", _FLOAT32, (E,), dev),
-            _name(SCORES, score, "score"), int(groups), int(top_groups), int(group_top),
-            1 if renormalize else 0, float(scale), int(shards),
-            _bn._need(ids, "ids", _INT32, (T, k), dev), _bn._need(w, "w", _FLOAT32, (shards, T, k), dev))
-    _call(_bn.load().bn_route, args, logits, stream)
+    bp = None if bias is None else _ptr(bias, "bias", _FLOAT32, (E,), dev)
+    ids, ip = _out(ids, "ids", _INT32, (T, k), dev)
+    w, wp = _out(w, "w", _FLOAT32, (shards, T, k), dev)
+    _call("bn_route", (logits.data_ptr(), dtype, ld, T, E, k, bp, _name(SCORES, score, "score"), groups, top_groups,
+                       group_top, 1 if renormalize else 0, scale, shards, ip, wp), dev.index, stream)
     return ids, w
 
 
@@ -141,12 +165,11 @@ def route_backward(logits, ids, dw, score: str = "softmax", renormalize: bool = 
     if not isinstance(dw, torch.Tensor) or dw.dim() != 3:
         raise ValueError("dw must be a tensor of 3 dimensions [shards, T, k]")
     R, _, k = dw.shape
-    if dlogits is None:
-        dlogits = torch.empty((T, E), dtype=logits.dtype, device=dev)
-    args = (logits.data_ptr(), dtype, ld, T, E, k, _bn._need(ids, "ids", _INT32, (T, k), dev),
-            _bn._need(dw, "dw", _FLOAT32, (R, T, k), dev), R, _name(SCORES, score, "score"),
-            1 if renormalize else 0, float(scale), _bn._need(dlogits, "dlogits", logits.dtype, (T, E), dev))
-    _call(_bn.load().bn_route_backward, args, logits, stream)
+    ip = _ptr(ids, "ids", _INT32, (T, k), dev)
+    dp = _ptr(dw, "dw", _FLOAT32, (R, T, k), dev)
+    dlogits, op = _out(dlogits, "dlogits", logits.dtype, (T, E), dev)
+    _call("bn_route_backward", (logits.data_ptr(), dtype, ld, T, E, k, ip, dp, R, _name(SCORES, score, "score"),
+                                1 if renormalize else 0, scale, op), dev.index, stream)
     return dlogits
 
 
@@ -157,18 +180,11 @@ def plan(ids, experts: int, shards: int = 1, perm=None, offsets=None, rows=None,
         raise ValueError("ids must be a tensor of 2 dimensions [T, k]")
     T, k = ids.shape
     dev = ids.device
-    E = int(experts)
-    args = (_bn._need(ids, "ids", _INT32, (T, k), dev), T, k, E, int(shards))
-    if perm is None:
-        perm = torch.empty((shards, T, k), dtype=_INT32, device=dev)
-    if offsets is None:
-        offsets = torch.empty((E + 1,), dtype=_INT32, device=dev)
-    if rows is None:
-        rows = torch.empty((T * k,), dtype=_INT32, device=dev)
-    args += (_bn._need(perm, "perm", _INT32, (shards, T, k), dev),
-             _bn._need(offsets, "offsets", _INT32, (E + 1,), dev),
-             _bn._need(rows, "rows", _INT32, (T * k,), dev))
-    _call(_bn.load().bn_expert_plan, args, ids, stream)
+    ip = _ptr(ids, "ids", _INT32, (T, k), dev)
+    perm, pp = _out(perm, "perm", _INT32, (shards, T, k), dev)
+    offsets, op = _out(offsets, "offsets", _INT32, (experts + 1,), dev)
+    rows, rp = _out(rows, "rows", _INT32, (T * k,), dev)
+    _call("bn_expert_plan", (ip, T, k, experts, shards, pp, op, rp), dev.index, stream)
     return Plan(perm, offsets, rows)
 
 
@@ -179,25 +195,25 @@ def fp4_scales_shape(M: int, K: int, format: str, groups: int = 1, ragged: bool 
 
 
 def _layout(q: FP4, name: str):
-    """(M, K, groups, offsets pointer) of quantised rows, after checks."""
+    """(M, K, groups, and the pointers of offsets, data and scales) of quantised rows, after checks."""
     if not isinstance(q, FP4):
         raise TypeError(f"{name} must be an FP4")
     _name(FORMATS, q.format, "format")
     data = q.data
-    if data.dim() not in (2, 3) or (data.dim() == 3 and q.offsets is not None):
+    shape, dev = data.shape, data.device
+    n = len(shape)
+    if n not in (2, 3) or (n == 3 and q.offsets is not None):
         raise ValueError(f"{name}.data must be [M, K/2], or [groups, rows, K/2] without offsets")
-    dev = data.device
-    _bn._need(data, f"{name}.data", _UINT8, data.shape, dev)
-    K = 2 * data.shape[-1]
-    groups = data.shape[0] if data.dim() == 3 else 1
-    M = groups * data.shape[-2] if data.dim() == 3 else data.shape[0]
+    dp = _ptr(data, f"{name}.data", _UINT8, shape, dev)
+    K = 2 * shape[-1]
+    groups = shape[0] if n == 3 else 1
+    M = groups * shape[1] if n == 3 else shape[0]
     op = None
     if q.offsets is not None:
         groups = q.offsets.numel() - 1
-        op = _bn._need(q.offsets, f"{name}.offsets", _INT32, (groups + 1,), dev)
-    _bn._need(q.scales, f"{name}.scales", _UINT8,
-              fp4_scales_shape(M, K, q.format, max(groups, 1), op is not None), dev)
-    return M, K, groups, op
+        op = _ptr(q.offsets, f"{name}.offsets", _INT32, (groups + 1,), dev)
+    sp = _ptr(q.scales, f"{name}.scales", _UINT8, fp4_scales_shape(M, K, q.format, max(groups, 1), op is not None), dev)
+    return M, K, groups, op, dp, sp
 
 
 def quantize_fp4(x, format: str, rows=None, offsets=None, tensor_scale: float = 1.0,
@@ -226,11 +242,11 @@ def quantize_fp4(x, format: str, rows=None, offsets=None, tensor_scale: float = 
     M, rp = n, None
     if rows is not None:
         M = rows.numel()
-        rp = _bn._need(rows, "rows", _INT32, (M,), dev)
+        rp = _ptr(rows, "rows", _INT32, (M,), dev)
     groups, op = 1, None
     if offsets is not None:
         groups = offsets.numel() - 1
-        op = _bn._need(offsets, "offsets", _INT32, (groups + 1,), dev)
+        op = _ptr(offsets, "offsets", _INT32, (groups + 1,), dev)
     elif lead is not None:
         groups = lead[0]
     if K % 32 or K == 0:
@@ -238,27 +254,20 @@ def quantize_fp4(x, format: str, rows=None, offsets=None, tensor_scale: float = 
     if M and groups < 1:
         raise ValueError("offsets must have 2 entries or more")
     dshape = (*lead, K // 2) if lead is not None else (M, K // 2)
-    sshape = fp4_scales_shape(M, K, format, max(groups, 1), op is not None)
-    if data is None:
-        data = torch.empty(dshape, dtype=_UINT8, device=dev)
-    if scales is None:
-        scales = torch.empty(sshape, dtype=_UINT8, device=dev)
-    args = (x.data_ptr(), dtype, ld, n, rp, M, K, op, max(groups, 1), fmt, float(tensor_scale),
-            _bn._need(data, "data", _UINT8, dshape, dev), _bn._need(scales, "scales", _UINT8, sshape, dev))
-    _call(_bn.load().bn_quantize_fp4, args, x, stream)
-    return FP4(data, scales, format, offsets, float(tensor_scale))
+    groups = max(groups, 1)
+    data, dp = _out(data, "data", _UINT8, dshape, dev)
+    scales, sp = _out(scales, "scales", _UINT8, fp4_scales_shape(M, K, format, groups, op is not None), dev)
+    _call("bn_quantize_fp4", (x.data_ptr(), dtype, ld, n, rp, M, K, op, groups, fmt, tensor_scale, dp, sp), dev.index, stream)
+    return FP4(data, scales, format, offsets, tensor_scale)
 
 
 def dequantize_fp4(q: FP4, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
     """The values of quantised rows ([..., K]) in BF16, FP16 or FP32."""
-    M, K, groups, op = _layout(q, "q")
+    M, K, groups, op, dp, sp = _layout(q, "q")
     dev = q.data.device
-    if out is None:
-        out = torch.empty(q.shape, dtype=dtype, device=dev)
-    d = _dtype(out, "out")
-    args = (q.data.data_ptr(), q.scales.data_ptr(), M, K, op, max(groups, 1), FORMATS[q.format],
-            float(q.tensor_scale), _bn._need(out, "out", out.dtype, q.shape, dev), d)
-    _call(_bn.load().bn_dequantize_fp4, args, q.data, stream)
+    out, yp = _out(out, "out", dtype if out is None else out.dtype, q.shape, dev)
+    _call("bn_dequantize_fp4", (dp, sp, M, K, op, max(groups, 1), FORMATS[q.format], q.tensor_scale, yp, _dtype(out, "out")),
+          dev.index, stream)
     return out
 
 
@@ -266,8 +275,8 @@ def expert_product(a: FP4, w: FP4, scale: float = 1.0, out=None, stream=None) ->
     """out [M,N] BF16: each row of ``a`` ([M,K], grouped by ``a.offsets``) times
     its group's weights of ``w`` ([E,N,K]; [N,K] is one expert), times ``scale``
     and both tensor scales.  Rows past the last group are zeros."""
-    M, K, groups, op = _layout(a, "a")
-    wM, wK, E, wo = _layout(w, "w")
+    M, K, groups, op, ap, sp = _layout(a, "a")
+    _, wK, E, wo, wp, wsp = _layout(w, "w")
     if wo is not None:
         raise ValueError("w must have equal groups (no offsets)")
     if a.data.dim() != 2:
@@ -280,10 +289,7 @@ def expert_product(a: FP4, w: FP4, scale: float = 1.0, out=None, stream=None) ->
     if w.data.device != dev:
         raise ValueError(f"w is on {w.data.device}, expected {dev}")
     N = w.data.shape[-2]
-    if out is None:
-        out = torch.empty((M, N), dtype=torch.bfloat16, device=dev)
-    args = (a.data.data_ptr(), a.scales.data_ptr(), M, w.data.data_ptr(), w.scales.data_ptr(), E, N, K,
-            op, FORMATS[a.format], float(scale) * a.tensor_scale * w.tensor_scale,
-            _bn._need(out, "out", torch.bfloat16, (M, N), dev))
-    _call(_bn.load().bn_expert_product, args, a.data, stream)
+    out, yp = _out(out, "out", torch.bfloat16, (M, N), dev)
+    _call("bn_expert_product", (ap, sp, M, wp, wsp, E, N, K, op, FORMATS[a.format], scale * a.tensor_scale * w.tensor_scale, yp),
+          dev.index, stream)
     return out
