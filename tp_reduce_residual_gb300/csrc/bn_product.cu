@@ -70,37 +70,55 @@ struct Maps {
     CUtensorMap a_scales, w_scales;  // scale tiles: boxes of a stage's by 512 bytes
 };
 
-struct Sched {
-    int tiles_f;      // feature tiles of an expert
-    long long total;  // tiles of all experts
-};
-
 struct Tile {
     int e, f, row0, rows, stile;
 };
 
-// Tile `id`: experts in order; of one expert, the row tiles of a feature tile
-// next to each other, so that CTAs that run together share its weights in L2.
+// The output tiles in order: experts one after another; of one expert, the row
+// tiles of a feature tile next to each other, so that CTAs that run together
+// share its weights in L2.  Every unit (a CTA or a pair) takes every step-th
+// tile.  Called by whole warps: a warp keeps its place among the experts and the
+// lanes look at the next 32 together, because the issuing warp has nothing in
+// flight while it looks for its next tile.
 template <int TILE>
-__device__ __forceinline__ Tile tile_of(long long id, const Sched &s, const int *start, const int *cum, int E)
-{
-    const int tt = (int)(id / s.tiles_f);
-    int lo = 0, hi = E;  // cum[lo] <= tt < cum[hi]
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (cum[mid] <= tt) lo = mid; else hi = mid;
+class Tiles {
+public:
+    __device__ Tiles(const int *start, const int *cum, int E, unsigned tiles_f, unsigned first, unsigned step)
+        : start_(start), cum_(cum), E_(E), e_(0), tiles_f_(tiles_f), step_(step), id_(first),
+          total_((unsigned long long)(unsigned)cum[E] * tiles_f)
+    {
     }
-    const int nt = cum[lo + 1] - cum[lo];
-    const int local = (int)(id - (long long)cum[lo] * s.tiles_f);
-    Tile t;
-    t.e = lo;
-    t.f = local / nt;
-    const int r = local % nt;
-    t.row0 = start[lo] + r * TILE;
-    t.rows = min(TILE, start[lo + 1] - t.row0);
-    t.stile = (start[lo] >> 7) + lo + r * (TILE / 128);
-    return t;
-}
+    // The next tile, or false past the last one.
+    __device__ __forceinline__ bool next(Tile &t, int lane)
+    {
+        if (id_ >= total_) return false;
+        // row tiles before this tile: 32-bit arithmetic where the tile numbers fit
+        const unsigned tt = total_ >> 32 ? (unsigned)(id_ / tiles_f_) : (unsigned)id_ / tiles_f_;
+        unsigned past;
+        do {  // experts that end at or before it
+            const int e = e_ + 1 + lane;
+            past = __popc(__ballot_sync(kAll, e <= E_ && (unsigned)cum_[min(e, E_)] <= tt));
+            e_ += (int)past;
+        } while (past == 32);
+        const unsigned c = (unsigned)cum_[e_], nt = (unsigned)cum_[e_ + 1] - c;
+        const unsigned local = (unsigned)(id_ - (unsigned long long)c * tiles_f_);
+        const int s0 = start_[e_], s1 = start_[e_ + 1];
+        t.e = e_;
+        t.f = nt == 1 ? (int)local : (int)(local / nt);
+        const int r = (int)(local - (unsigned)t.f * nt);
+        t.row0 = s0 + r * TILE;
+        t.rows = min(TILE, s1 - t.row0);
+        t.stile = (s0 >> 7) + e_ + r * (TILE / 128);
+        id_ += step_;
+        return true;
+    }
+
+private:
+    const int *start_, *cum_;
+    int E_, e_;
+    unsigned tiles_f_, step_;
+    unsigned long long id_, total_;
+};
 
 // A box into this CTA's shared memory; its bytes count on `bar`, which for a
 // pair is the first CTA's.
@@ -300,37 +318,35 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     ctl.err = p.err;
     ctl.spin = false;
     ctl.pipe_polls = kMaxSpins;
-    Sched sched;
-    sched.tiles_f = (p.N + kTile - 1) / kTile;
-    sched.total = (long long)cum[p.E] * sched.tiles_f;
+    Tiles<kTile> tiles(start, cum, p.E, (unsigned)((p.N + kTile - 1) / kTile), (unsigned)unit, (unsigned)units);
+    Tile t;
     const int nk = (p.K + 255) / 256;
     constexpr int kChunksPerStage = MX ? 2 : 4;
 
+    // The copying and the issuing warp run their loops as a whole, so that loop
+    // state stays in uniform registers; one elected thread does each stage's work.
     if (warp == 0) {
-        if (elect_one()) {
-            const int wtiles = (p.N + 127) / 128;  // scale tiles of one expert
-            uint32_t it = 0;  // stages filled
-            bool ok = true;
-            for (long long id = unit; ok && id < sched.total; id += units) {
-                const Tile t = tile_of<kTile>(id, sched, start, cum, p.E);
-                const int f0 = t.f * kTile + (int)rank * kHalf;
-                // this CTA's rows of the product's N operand: all, or half of the rounded count
-                const int columns = (t.rows + S::kStep - 1) / S::kStep * S::kStep;
-                const int nb = PAIR ? columns / 2 : columns, b0 = t.row0 + (PAIR ? (int)rank * nb : 0);
-                const int boxes = nb > kHalf / 2 ? 0 : (nb + kBoxRows - 1) / kBoxRows;  // 0: one of kHalf rows
-                const uint32_t codes = (uint32_t)(kHalf + (boxes ? boxes * kBoxRows : kHalf)) * kTileBytes;
-                const int atoms = (t.rows + 127) / 128;
-                constexpr uint32_t kScaleBytes = kChunksPerStage * 512;
-                const uint32_t bytes = S::kCtas * (codes + (1 + atoms) * kScaleBytes);
-                // past the last features any scales will do
-                const int sw = (t.e * wtiles + min(f0 / kHalf, wtiles - 1)) * p.chunks;
-                const int sa = t.stile * p.chunks;
-                for (int k = 0; k < nk; ++k, ++it) {
-                    const uint32_t s = it % kStages;
-                    if (!wait_phase<PAIR, kPipe>(empty + 8 * s, ((it / kStages) & 1u) ^ 1u, ctl)) {
-                        ok = false;
-                        break;
-                    }
+        const int wtiles = (p.N + 127) / 128;  // scale tiles of one expert
+        uint32_t it = 0;  // stages filled
+        bool ok = true;
+        while (ok && tiles.next(t, lane)) {
+            const int f0 = t.f * kTile + (int)rank * kHalf;
+            // this CTA's rows of the product's N operand: all, or half of the rounded count
+            const int columns = (t.rows + S::kStep - 1) / S::kStep * S::kStep;
+            const int nb = PAIR ? columns / 2 : columns, b0 = t.row0 + (PAIR ? (int)rank * nb : 0);
+            const int boxes = nb > kHalf / 2 ? 0 : (nb + kBoxRows - 1) / kBoxRows;  // 0: one of kHalf rows
+            const uint32_t codes = (uint32_t)(kHalf + (boxes ? boxes * kBoxRows : kHalf)) * kTileBytes;
+            const int atoms = (t.rows + 127) / 128;
+            constexpr uint32_t kScaleBytes = kChunksPerStage * 512;
+            const uint32_t bytes = S::kCtas * (codes + (1 + atoms) * kScaleBytes);
+            // past the last features any scales will do
+            const int sw = (t.e * wtiles + min(f0 / kHalf, wtiles - 1)) * p.chunks;
+            const int sa = t.stile * p.chunks;
+            for (int k = 0; k < nk; ++k, ++it) {
+                const uint32_t s = it % kStages;
+                ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(empty + 8 * s, ((it / kStages) & 1u) ^ 1u, ctl));
+                if (!ok) break;
+                if (elect_one()) {
                     const uint32_t at = base + s * S::kStageBytes;
                     const uint32_t bar = PAIR ? mapa(full + 8 * s, 0) : full + 8 * s;
                     if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, bytes);
@@ -347,26 +363,26 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         tma_2d<PAIR>(at + S::kOffSB + 2048, &maps.a_scales, 0, sa + p.chunks + c, bar);
                 }
             }
-            // no copy, and no arrival of a product, may be in flight into a CTA that leaves
-            const uint32_t old = it > kStages ? it - kStages : 0;
-            for (uint32_t i = old; ok && i < it; ++i)
-                ok = wait_phase<PAIR, kPipe>(empty + 8 * (i % kStages), (i / kStages) & 1u, ctl);
-            if (!ok) {  // after a timeout: wait for the copies, and where their barrier is the other CTA's, for a while
-                for (uint32_t i = old; rank == 0 && i < it; ++i)
-                    wait_phase<false, kDrain>(full + 8 * (i % kStages), (i / kStages) & 1u, ctl);
-                for (const long long t0 = clock64(); rank != 0 && clock64() - t0 < (1 << 22);) {}
-            }
+        }
+        // no copy, and no arrival of a product, may be in flight into a CTA that leaves
+        const uint32_t old = it > kStages ? it - kStages : 0;
+        for (uint32_t i = old; ok && i < it; ++i)
+            ok = wait_phase<PAIR, kPipe>(empty + 8 * (i % kStages), (i / kStages) & 1u, ctl);
+        if (!ok) {  // after a timeout: wait for the copies, and where their barrier is the other CTA's, for a while
+            for (uint32_t i = old; rank == 0 && i < it; ++i)
+                wait_phase<false, kDrain>(full + 8 * (i % kStages), (i / kStages) & 1u, ctl);
+            for (const long long t0 = clock64(); rank != 0 && clock64() - t0 < (1 << 22);) {}
         }
         __syncwarp();
     } else if (warp == 1) {
-        // one thread issues the products; of a pair's, the first CTA's
-        if (rank == 0 && elect_one()) {
+        // of a pair's CTAs the first issues the products
+        if (rank == 0) {
             uint32_t it = 0, n = 0;
             bool ok = true;
-            for (long long id = unit; ok && id < sched.total; id += units, ++n) {
-                const Tile t = tile_of<kTile>(id, sched, start, cum, p.E);
+            for (; ok && tiles.next(t, lane); ++n) {
                 const uint32_t buf = n % S::kAccs;
-                if (!wait_phase<PAIR, kPipe>(acc_empty + 8 * buf, ((n / S::kAccs) & 1u) ^ 1u, ctl)) break;
+                ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(acc_empty + 8 * buf, ((n / S::kAccs) & 1u) ^ 1u, ctl));
+                if (!ok) break;
                 fence_after();
                 const uint32_t columns = (uint32_t)((t.rows + S::kStep - 1) / S::kStep * S::kStep);
                 // E2M1 operands, both with K along the row; E8M0 scales for MXFP4; N / 8, M / 16
@@ -376,7 +392,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 const bool two = S::kRowAtoms > 1 && columns > 128;
                 for (int k = 0; k < nk; ++k, ++it) {
                     const uint32_t s = it % kStages;
-                    ok = wait_phase<PAIR, kPipe>(full + 8 * s, (it / kStages) & 1u, ctl);
+                    ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(full + 8 * s, (it / kStages) & 1u, ctl));
                     if (!ok) break;
                     fence_after();
                     const uint32_t at = base + s * S::kStageBytes;
@@ -394,40 +410,43 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         product<MX, PAIR>(d, da + 2 * j, db + 2 * j, idesc | (half << 4) | (half << 29), sa + 4 * c,
                                           sb + 4 * S::kRowAtoms * c, k > 0 || j > 0);
                     };
-                    // each step's scales just before its product: they are copied while the one before runs
+                    // each step's scales just before its product
                     constexpr int kSteps = MX ? 2 : 1;  // steps of one scale chunk
-                    if (k * 256 + 256 <= p.K) {  // unrolled: the issuing thread sets the pace
+                    if (elect_one()) {
+                        if (k * 256 + 256 <= p.K) {  // unrolled: the issuing thread sets the pace
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            if (j % kSteps == 0) scales(j / kSteps);
-                            step(j);
+                            for (int j = 0; j < 4; ++j) {
+                                if (j % kSteps == 0) scales(j / kSteps);
+                                step(j);
+                            }
+                        } else {
+                            const int steps = (p.K - k * 256 + 63) / 64;
+                            for (int j = 0; j < steps; ++j) {
+                                if (j % kSteps == 0) scales(j / kSteps);
+                                step(j);
+                            }
                         }
-                    } else {
-                        const int steps = (p.K - k * 256 + 63) / 64;
-                        for (int j = 0; j < steps; ++j) {
-                            if (j % kSteps == 0) scales(j / kSteps);
-                            step(j);
-                        }
+                        commit<PAIR>(empty + 8 * s);
+                        if (k == nk - 1) commit<PAIR>(acc_full + 8 * buf);
                     }
-                    commit<PAIR>(empty + 8 * s);
                 }
-                if (ok) commit<PAIR>(acc_full + 8 * buf);
             }
-            commit<PAIR>(done);  // every product has ended before tensor memory is freed
-            wait_phase<false, kDrain>(done, 0, ctl);
+            if (elect_one()) {
+                commit<PAIR>(done);  // every product has ended before tensor memory is freed
+                wait_phase<false, kDrain>(done, 0, ctl);
+            }
         }
         __syncwarp();
     } else {
         const int quad = warp & 3;         // the lanes of tensor memory that this warp reads
         const int half = (warp - 2) >> 2;  // of a pair's columns
         uint32_t n = 0;
-        for (long long id = unit; id < sched.total; id += units, ++n) {
-            const Tile t = tile_of<kTile>(id, sched, start, cum, p.E);
+        for (; tiles.next(t, lane); ++n) {
             const uint32_t buf = n % S::kAccs;
             // this warp's columns: at most 128
             const int cut = PAIR ? (t.rows + 31) / 32 * 16 : t.rows;
             const int lo = half ? cut : 0, hi = half ? t.rows : min(cut, t.rows);
-            if (!wait_phase<PAIR, kPipe>(acc_full + 8 * buf, (n / S::kAccs) & 1u, ctl)) break;
+            if (!__all_sync(kAll, wait_phase<PAIR, kPipe>(acc_full + 8 * buf, (n / S::kAccs) & 1u, ctl))) break;
             fence_after();
             // the whole tile as BF16 in registers, so that the next product can start
             uint32_t packed[8][8];
