@@ -26,6 +26,7 @@ struct RouteArgs {
     int32_t *ids;          // [T, k]
     float *w;              // [R, T, k]
     int vec;               // rows are 16-byte aligned and E is a multiple of a vector
+    int bias_vec;          // so is the bias
 };
 
 struct RouteBackwardArgs {

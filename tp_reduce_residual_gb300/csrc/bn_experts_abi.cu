@@ -142,6 +142,7 @@ bn_status bn_route(const void *logits, bn_dtype dtype, long long ld, int T, int 
     a.ids = ids;
     a.w = w;
     a.vec = vectors(logits, ld, E, dtype_size(dtype));
+    a.bias_vec = vectors(bias, 4, E, 4);
     return launched(launch_route(a, dtype, dependent_launch(), (cudaStream_t)stream), "launching route");
 }
 

@@ -12,14 +12,18 @@
 // left get id -1 and weight 0.  A NaN logit or key takes its expert out and
 // makes the row's weights NaN.
 //
-// The order of keys is decided as in exact arithmetic.  Keys that are logits
-// compare exactly.  Sums s + bias are computed in 32 bits with a bound on their
-// error; where two keys (or two groups' ranks) whose order matters differ by
-// less than the bound, the row is selected again with 64-bit scores.
+// The order of keys is decided as in exact arithmetic.  Logits of 16 bits compare
+// exactly.  Sums s + bias are computed in 32 bits with a bound on their error, and
+// keys give their lowest bits to an index (below); where two keys (or two groups'
+// ranks) whose order matters differ by less than the bound, the choice is made
+// again with 64-bit keys: among the few candidates if only the experts' order is
+// open, else for the whole row.
 //
-// One warp per token: a lane holds VPT consecutive experts in registers and the
-// warp takes the largest key k times (redux.sync).  What bounds it is
-// instruction issue, about k * (2 redux + 3 VPT) for the selection.
+// One warp per token: a lane holds VPT consecutive experts.  Each lane sorts its
+// keys once (an odd-even merge sorting network; the position in the lane rides in
+// the keys' lowest bits, so that a comparison is one instruction), then k rounds
+// take the largest of the 32 heads (redux.sync) and advance one lane.  What bounds
+// it is instruction issue: about 500 instructions a token at 256 experts.
 #include <cfloat>
 #include <cmath>
 
@@ -109,41 +113,43 @@ __device__ __forceinline__ float sigmoid(float x) { return 1.0f / (1.0f + expf(-
 __device__ __forceinline__ double sigmoid(double x) { return 1.0 / (1.0 + exp(-x)); }
 
 // Error bound of a 32-bit score: expf is within 2 units in the last place
-// (2^-22 relative), the addition and the division within 2^-24 each: 1.5 * 2^-22
-// of s <= 1 for the sigmoid.  The softmax's sum of at most 1024 terms (32 in a
-// lane, 5 levels) adds 37 * 2^-24 and x - max its own rounding, at most
+// (2^-22 relative), the addition within 2^-24, rcp.approx within 2^-23: under
+// 1.5 * 2^-22 of s <= 1 for the sigmoid.  The softmax's sum of at most 1024 terms
+// (32 in a lane, 5 levels) adds 37 * 2^-24 and x - max its own rounding, at most
 // max(d exp(-d)) * 2^-24: under 2^-18 of the largest probability together.
 constexpr float kSigmoidError = 1.5f * 0x1p-22f;
 constexpr float kSoftmaxError = 0x1p-18f;
 
-// Take the n largest of the warp's keys, one per round; lane j ends with the
-// j-th id (-1 where nothing is left) and its key.
-template <typename F, int VPT>
-__device__ __forceinline__ void take(F *key, int lane, int n, int &id, F &at)
+__device__ __forceinline__ float rcp_approx(float v)
 {
-    id = -1;
-    at = -INFINITY;
-    F best = key[0];
-    int bi = 0;
-#pragma unroll
-    for (int j = 1; j < VPT; ++j)
-        if (key[j] > best) { best = key[j]; bi = j; }
+    float r;
+    asm("rcp.approx.f32 %0, %1;" : "=f"(r) : "f"(v));
+    return r;
+}
+
+// ---- 64-bit selection, for rows whose order 32 bits do not tell ------------------------
+
+// Take the n largest of the warp's keys, one per round; lane j ends with the
+// j-th id (-1 where nothing is left).
+template <int VPT>
+__device__ __forceinline__ int take64(double *key, int lane, int n)
+{
+    int id = -1;
     for (int r = 0; r < n; ++r) {
-        const F m = warp_max(best);
-        if (!(m > (F)-INFINITY)) break;
-        const int i = __reduce_min_sync(kAll, best == m ? lane * VPT + bi : kNone);
-        if (lane == r) { id = i; at = m; }
-        if (i / VPT == lane) {
-            best = -INFINITY;
-            const int gone = i % VPT;
-            bi = 0;
+        double best = key[0];
+        int bi = 0;
 #pragma unroll
-            for (int j = 0; j < VPT; ++j) {
-                if (j == gone) key[j] = -INFINITY;
-                if (key[j] > best) { best = key[j]; bi = j; }
-            }
-        }
+        for (int j = 1; j < VPT; ++j)
+            if (key[j] > best) { best = key[j]; bi = j; }
+        const double m = warp_max(best);
+        if (!(m > -(double)INFINITY)) break;
+        const int i = __reduce_min_sync(kAll, best == m ? lane * VPT + bi : kNone);
+        if (lane == r) id = i;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j)
+            if (lane * VPT + j == i) key[j] = -INFINITY;
     }
+    return id;
 }
 
 template <typename F>
@@ -153,72 +159,38 @@ __device__ __forceinline__ void push2(F v, F &a, F &b)
     else if (v > b) b = v;
 }
 
-// Mask out the keys of all but the top_groups groups of the highest rank.
-// `slot` is the warp's shared memory for VPT * 32 keys.  Returns how far the
-// lowest rank that stays is above the highest that goes (inf if none goes).
-template <typename F, int VPT>
-__device__ __forceinline__ F keep_groups(F *key, int lane, const RouteArgs &a, F *slot, F &largest)
+// The groups that stay, as bits, from the two largest keys of group `lane` (lanes
+// past the groups hold -inf).  `gap`: how far the lowest rank that stays is above
+// the highest that goes (inf if none goes); `largest`: the largest rank's size.
+template <typename F>
+__device__ __forceinline__ unsigned keep_groups(F r1, F r2, int lane, const RouteArgs &a, F &gap, F &largest)
 {
-    const int size = a.E / a.groups;
-    F r1 = -INFINITY, r2 = -INFINITY;  // lane g: the two largest keys of group g
-    const int lanes = size / VPT;      // lanes per group, when groups are whole lanes
-    if (size % VPT == 0 && (lanes & (lanes - 1)) == 0) {
-        F p = -INFINITY, q = -INFINITY;
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) push2(key[j], p, q);
-        for (int o = 1; o < lanes; o <<= 1) {
-            const F po = __shfl_xor_sync(kAll, p, o), qo = __shfl_xor_sync(kAll, q, o);
-            push2(po, p, q);
-            push2(qo, p, q);
-        }
-        const int src = min(lane * lanes, 31);
-        r1 = __shfl_sync(kAll, p, src);
-        r2 = __shfl_sync(kAll, q, src);
-    } else {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) slot[lane * VPT + j] = key[j];
-        __syncwarp();
-        if (lane < a.groups)
-            for (int i = 0; i < size; ++i) push2(slot[lane * size + i], r1, r2);
-        __syncwarp();
-    }
     F rank = -INFINITY;
-    if (lane < a.groups && r1 > (F)-INFINITY)
-        rank = a.group_top > 1 && r2 > (F)-INFINITY ? r1 + r2 : r1;
+    if (lane < a.groups && r1 > (F)-INFINITY) rank = a.group_top > 1 && r2 > (F)-INFINITY ? r1 + r2 : r1;
     int ahead = 0;
     for (int g = 0; g < a.groups; ++g) {
         const F o = __shfl_sync(kAll, rank, g);
         ahead += (o > rank || (o == rank && g < lane)) ? 1 : 0;
     }
     const bool keep = lane < a.groups && ahead < a.top_groups;
-    const unsigned kept = __ballot_sync(kAll, keep);
     const F low = -warp_max(keep && rank > (F)-INFINITY ? -rank : (F)-INFINITY);
     const F high = warp_max(!keep && lane < a.groups ? rank : (F)-INFINITY);
     largest = warp_max(rank > (F)-INFINITY ? (rank < 0 ? -rank : rank) : (F)0);
-    if (size % VPT == 0) {  // a lane's experts are one group's
-        const int g = lane * VPT / size;
-        const bool out = g >= a.groups || !((kept >> g) & 1u);
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-            if (out) key[j] = -INFINITY;
-    } else {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j) {
-            const int e = lane * VPT + j;
-            if (e < a.E && !((kept >> (e / size)) & 1u)) key[j] = -INFINITY;
-        }
-    }
-    return high > (F)-INFINITY ? low - high : (F)INFINITY;
+    gap = high > (F)-INFINITY ? low - high : (F)INFINITY;
+    return __ballot_sync(kAll, keep);
 }
 
-// The selection with 64-bit scores, for rows whose order 32 bits do not tell.
-template <typename T, int VPT>
+// The whole row; `slot` is the warp's shared memory for 32 * VPT keys.
+template <typename T, int VPT, bool SUMS>
 __device__ __noinline__ int select64(const T *row, const RouteArgs &a, int lane, double *slot)
 {
     float x[VPT];
     load_row<T, VPT>(row, a.E, lane, a.vec, -INFINITY, x);
     double key[VPT];
-    if (a.sigmoid) {
+    if (!SUMS) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) key[j] = x[j];
+    } else if (a.sigmoid) {
 #pragma unroll
         for (int j = 0; j < VPT; ++j) key[j] = sigmoid((double)x[j]);
     } else {
@@ -239,45 +211,117 @@ __device__ __noinline__ int select64(const T *row, const RouteArgs &a, int lane,
 #pragma unroll
     for (int j = 0; j < VPT; ++j) {
         const int e = lane * VPT + j;
-        const double b = a.bias && e < a.E ? (double)__ldg(a.bias + e) : 0.0;
-        key[j] += b;
-        if (!(x[j] > -INFINITY) || !(key[j] > -INFINITY)) key[j] = -INFINITY;
+        key[j] += a.bias && e < a.E ? (double)__ldg(a.bias + e) : 0.0;
+        if (!(x[j] > -INFINITY) || !(key[j] > -(double)INFINITY)) key[j] = -INFINITY;
     }
     if (a.groups > 1) {
-        double unused;
-        keep_groups<double, VPT>(key, lane, a, slot, unused);
+        const int size = a.E / a.groups;
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) slot[lane * VPT + j] = key[j];
+        __syncwarp();
+        double r1 = -INFINITY, r2 = -INFINITY, gap, largest;
+        if (lane < a.groups)
+            for (int i = 0; i < size; ++i) push2(slot[lane * size + i], r1, r2);
+        const unsigned kept = keep_groups(r1, r2, lane, a, gap, largest);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int e = lane * VPT + j;
+            if (e < a.E && !((kept >> (e / size)) & 1u)) key[j] = -INFINITY;
+        }
     }
-    int id;
-    double at;
-    take<double, VPT>(key, lane, a.k, id, at);
-    return id;
+    return take64<VPT>(key, lane, a.k);
+}
+
+// The candidates, lane j < n the one of id `id`: lane j < k gets the j-th of them.
+template <typename T, bool SUMS>
+__device__ __noinline__ int order64(const T *row, const RouteArgs &a, int lane, int n, int id, int *list)
+{
+    double key = -INFINITY;
+    if (lane < n) {
+        const double x = (double)to_f32(row[id]);
+        key = SUMS ? sigmoid(x) + (a.bias ? (double)__ldg(a.bias + id) : 0.0) : x;
+    }
+    int ahead = 0;
+    for (int j = 0; j < n; ++j) {
+        const double o = __shfl_sync(kAll, key, j);
+        const int oid = __shfl_sync(kAll, id, j);
+        ahead += (o > key || (o == key && oid < id)) ? 1 : 0;
+    }
+    __syncwarp();
+    if (lane < n) list[ahead] = id;
+    __syncwarp();
+    return list[lane];
+}
+
+// ---- keys with an index in their lowest bits -----------------------------------------------
+
+// Falling values of lane-local keys; of keys equal but for these bits the lower
+// position comes first.
+template <int VPT>
+__device__ __forceinline__ float with_position(float v, int j)
+{
+    const uint32_t u = __float_as_uint(v);
+    return __uint_as_float((u & ~(uint32_t)(VPT - 1)) | ((int)u < 0 ? (uint32_t)j : (uint32_t)(VPT - 1 - j)));
+}
+template <int VPT>
+__device__ __forceinline__ int position_of(float v)
+{
+    const uint32_t u = __float_as_uint(v);
+    return (int)((u ^ ((int)u < 0 ? 0u : ~0u)) & (VPT - 1));
+}
+// What two keys are compared by.
+template <int VPT>
+__device__ __forceinline__ float without_position(float v)
+{
+    return __uint_as_float(__float_as_uint(v) & ~(uint32_t)(VPT - 1));  // -inf stays
+}
+
+// Batcher's odd-even merge sort, falling.
+template <int VPT>
+__device__ __forceinline__ void sort_keys(float *v)
+{
+#pragma unroll
+    for (int p = 1; p < VPT; p <<= 1)
+#pragma unroll
+        for (int q = p; q >= 1; q >>= 1)
+#pragma unroll
+            for (int j = q % p; j + q < VPT; j += 2 * q)
+#pragma unroll
+                for (int i = 0; i < q; ++i)
+                    if (i + j + q < VPT && (i + j) / (2 * p) == (i + j + q) / (2 * p)) {
+                        const float hi = fmaxf(v[i + j], v[i + j + q]), lo = fminf(v[i + j], v[i + j + q]);
+                        v[i + j] = hi;
+                        v[i + j + q] = lo;
+                    }
 }
 
 // SUMS: the keys are s + bias (or group ranks are sums of scores), else logits.
 template <typename T, int VPT, bool SUMS>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
+__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteArgs a)
 {
-    __shared__ double slots[SUMS ? kWarps : 1][SUMS ? 32 * VPT : 1];
-    __shared__ float fslots[SUMS ? 1 : kWarps][SUMS ? 1 : 32 * VPT];
+    __shared__ double slots[kWarps][32 * VPT];
+    __shared__ int lists[kWarps][32];
+    // 16-bit logits leave their low bits free: nothing is lost to the positions
+    constexpr bool kExact = !SUMS && sizeof(T) == 2;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int t = blockIdx.x * kWarps + warp;
     griddep_launch_dependents();
     griddep_wait();
     if (t >= a.T) return;
     const T *row = static_cast<const T *>(a.logits) + (long long)t * a.ld;
+    int *list = lists[warp];
 
     float key[VPT];
     load_row<T, VPT>(row, a.E, lane, a.vec, -INFINITY, key);
     bool nan = false;
     float top = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < VPT; ++j) {
-        nan |= key[j] != key[j];
-        top = fmaxf(top, key[j]);  // a NaN is passed over
-    }
+    for (int j = 0; j < VPT; ++j) nan |= key[j] != key[j];
     // softmax statistics, where a score depends on the whole row
     float inv = 0.0f;
     if (!a.sigmoid && (SUMS || !a.renormalize)) {
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) top = fmaxf(top, key[j]);  // a NaN is passed over
         top = warp_max(top);
         float sum = 0.0f;
 #pragma unroll
@@ -285,52 +329,112 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
         sum = warp_sum(sum);
         inv = sum == 0.0f ? 0.0f : 1.0f / sum;  // 0: every expert is masked
     }
-    float *slot = SUMS ? reinterpret_cast<float *>(slots[warp]) : fslots[SUMS ? 0 : warp];
     float serr = 0.0f;
     if constexpr (SUMS) {
         serr = a.sigmoid ? kSigmoidError : kSoftmaxError * inv;
+        float b[VPT];
+        if (a.bias)
+            load_row<float, VPT>(a.bias, a.E, lane, a.bias_vec, 0.0f, b);
+        else
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) b[j] = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const int e = lane * VPT + j;
             const float x = key[j];
-            const float b = a.bias && e < a.E ? __ldg(a.bias + e) : 0.0f;
-            const float v = (a.sigmoid ? sigmoid(x) : expf(x - top) * inv) + b;
+            const float v = (a.sigmoid ? rcp_approx(1.0f + expf(-x)) : expf(x - top) * inv) + b[j];
             nan |= x > -INFINITY && v != v;
             key[j] = x > -INFINITY && v > -INFINITY ? v : -INFINITY;
         }
-    } else {
-#pragma unroll
-        for (int j = 0; j < VPT; ++j)
-            if (!(key[j] > -INFINITY)) key[j] = -INFINITY;
     }
     nan = __any_sync(kAll, nan);
+#pragma unroll
+    for (int j = 0; j < VPT; ++j)  // + 0 makes -0 a 0: they are equal
+        key[j] = key[j] > -INFINITY ? with_position<VPT>(fminf(key[j], FLT_MAX) + 0.0f, j) : -INFINITY;
 
-    bool sure = true;
-    if (a.groups > 1) {
-        float largest;
-        const float gap = keep_groups<float, VPT>(key, lane, a, slot, largest);
-        // a rank is one or two keys: twice a key's error each, and its own rounding
-        if constexpr (SUMS) sure = gap > 4.0f * serr + 0x1p-21f * largest;
-    }
-    int id;
-    float at;
-    take<float, VPT>(key, lane, SUMS ? a.k + 1 : a.k, id, at);
-    if constexpr (SUMS) {
-        const float x = id >= 0 ? to_f32(row[id]) : 0.0f;
-        const float b = id >= 0 && a.bias ? __ldg(a.bias + id) : 0.0f;
-        const int idn = __shfl_down_sync(kAll, id, 1);
-        const float atn = __shfl_down_sync(kAll, at, 1), xn = __shfl_down_sync(kAll, x, 1),
-                    bnx = __shfl_down_sync(kAll, b, 1);
-        bool ok = true;
-        if (lane < a.k && id >= 0 && idn >= 0) {
-            const float bound = 2.0f * serr + 0x1p-22f * fmaxf(fabsf(at), fabsf(atn)) + 0x1p-120f;
-            // equal logits and biases have equal keys: the index decides
-            ok = at - atn > bound || (x == xn && b == bnx);
+    bool sure = true;  // of the groups that stay
+    float gap = INFINITY, largest = 0.0f;
+    const int size = a.E / a.groups, lanes = size / VPT;
+    const bool whole = size % VPT == 0 && (lanes & (lanes - 1)) == 0;  // a group is so many whole lanes
+    if (a.groups > 1 && !whole) {
+        float *slot = reinterpret_cast<float *>(slots[warp]);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) slot[lane * VPT + j] = without_position<VPT>(key[j]);
+        __syncwarp();
+        float r1 = -INFINITY, r2 = -INFINITY;
+        if (lane < a.groups)
+            for (int i = 0; i < size; ++i) push2(slot[lane * size + i], r1, r2);
+        const unsigned kept = keep_groups(r1, r2, lane, a, gap, largest);
+#pragma unroll
+        for (int j = 0; j < VPT; ++j) {
+            const int e = lane * VPT + j;
+            if (e < a.E && !((kept >> (e / size)) & 1u)) key[j] = -INFINITY;
         }
-        sure = __all_sync(kAll, ok) && sure;
-        if (!sure) id = select64<T, VPT>(row, a, lane, slots[warp]);
-        if (lane >= a.k) id = -1;
+        __syncwarp();
     }
+    sort_keys<VPT>(key);
+    float head = without_position<VPT>(key[0]);
+    if (a.groups > 1 && whole) {
+        float p = head, q = VPT > 1 ? without_position<VPT>(key[VPT > 1 ? 1 : 0]) : -INFINITY;
+        for (int o = 1; o < lanes; o <<= 1) {
+            const float po = __shfl_xor_sync(kAll, p, o), qo = __shfl_xor_sync(kAll, q, o);
+            q = fmaxf(fminf(p, po), fmaxf(q, qo));
+            p = fmaxf(p, po);
+        }
+        const int src = min(lane * lanes, 31);
+        const unsigned kept = keep_groups(__shfl_sync(kAll, p, src), __shfl_sync(kAll, q, src), lane, a, gap, largest);
+        const int g = lane / lanes;
+        if (g >= a.groups || !((kept >> g) & 1u)) head = -INFINITY;  // and so the lane's other keys
+    }
+    // a rank is one or two keys, each off by serr, by its rounding and by its lowest bits, and a rounded sum
+    if constexpr (!kExact) sure = gap > 4.0f * serr + (VPT + 2) * 0x1p-21f * largest;
+
+    int n = 0;             // chosen so far; lane j < n keeps the j-th key
+    float at = -INFINITY;
+    const auto choose = [&](float m) {  // m is the largest head: of equal ones the lowest lane's
+        const int src = __ffs(__ballot_sync(kAll, head == m)) - 1;
+        if (lane == n) at = m;
+        if (lane == src) {
+            list[n] = lane * VPT + position_of<VPT>(key[0]);
+#pragma unroll
+            for (int j = 0; j + 1 < VPT; ++j) key[j] = key[j + 1];
+            key[VPT - 1] = -INFINITY;
+            head = without_position<VPT>(key[0]);
+        }
+        ++n;
+    };
+    const int rounds = kExact ? a.k : a.k + 1;  // one more shows how far the last is from the next
+    float m = -INFINITY;
+    for (;;) {
+        m = warp_max(head);
+        if (m == -INFINITY || n == rounds) break;
+        choose(m);
+    }
+    __syncwarp();
+    int id = lane < n ? list[lane] : -1;
+    if constexpr (!kExact) {
+        // is the order of each and the next certain?
+        const float x = id >= 0 ? to_f32(row[id]) : 0.0f, b = id >= 0 && a.bias ? __ldg(a.bias + id) : 0.0f;
+        const float atn = __shfl_down_sync(kAll, at, 1), xn = __shfl_down_sync(kAll, x, 1),
+                    bn = __shfl_down_sync(kAll, b, 1);
+        const auto bound = [&](float v) { return 2.0f * serr + (VPT + 1) * 0x1p-22f * fabsf(v) + 0x1p-120f; };
+        // equal logits and biases have equal keys: the index decides
+        const bool open = __any_sync(kAll, lane + 1 < n && !(at - atn > bound(fmaxf(fabsf(at), fabsf(atn))) ||
+                                                             (x == xn && b == bn)));
+        if (!sure || open) {
+            // every expert that may belong among the k
+            const float last = __shfl_sync(kAll, at, a.k - 1);
+            while (sure && n < 32 && m > -INFINITY && last - m <= bound(fmaxf(fabsf(last), fabsf(m)))) {
+                choose(m);
+                m = warp_max(head);
+            }
+            __syncwarp();
+            if (!sure || n == 32 || (SUMS && !a.sigmoid))
+                id = select64<T, VPT, SUMS>(row, a, lane, slots[warp]);
+            else
+                id = order64<T, SUMS>(row, a, lane, n, lane < n ? list[lane] : -1, list);
+        }
+    }
+    if (lane >= min(n, a.k)) id = -1;
 
     const bool on = lane < a.k && id >= 0;
     const float x = on ? to_f32(row[id]) : -INFINITY;
@@ -364,7 +468,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(RouteArgs a)
 // row in shared memory, and the row is written once with 16-byte stores, so the
 // kernel is bounded by that store stream.
 template <typename T, int VPT, bool DENSE>
-__global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(RouteBackwardArgs a)
+__global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const __grid_constant__ RouteBackwardArgs a)
 {
     __shared__ __align__(16) float rows[kWarps][32 * VPT];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
