@@ -161,7 +161,8 @@ __device__ __forceinline__ void push2(F v, F &a, F &b)
 
 // The groups that stay, as bits, from the two largest keys of group `lane` (lanes
 // past the groups hold -inf).  `gap`: how far the lowest rank that stays is above
-// the highest that goes (inf if none goes); `largest`: the largest rank's size.
+// the highest that goes (inf if none goes); `largest`: the largest sum of the sizes
+// of a group's two keys.
 template <typename F>
 __device__ __forceinline__ unsigned keep_groups(F r1, F r2, int lane, const RouteArgs &a, F &gap, F &largest)
 {
@@ -175,7 +176,8 @@ __device__ __forceinline__ unsigned keep_groups(F r1, F r2, int lane, const Rout
     const bool keep = lane < a.groups && ahead < a.top_groups;
     const F low = -warp_max(keep && rank > (F)-INFINITY ? -rank : (F)-INFINITY);
     const F high = warp_max(!keep && lane < a.groups ? rank : (F)-INFINITY);
-    largest = warp_max(rank > (F)-INFINITY ? (rank < 0 ? -rank : rank) : (F)0);
+    const F size1 = r1 > (F)-INFINITY ? (r1 < 0 ? -r1 : r1) : (F)0, size2 = r2 > (F)-INFINITY ? (r2 < 0 ? -r2 : r2) : (F)0;
+    largest = warp_max(size1 + size2);
     gap = high > (F)-INFINITY ? low - high : (F)INFINITY;
     return __ballot_sync(kAll, keep);
 }
@@ -232,15 +234,59 @@ __device__ __noinline__ int select64(const T *row, const RouteArgs &a, int lane,
     return take64<VPT>(key, lane, a.k);
 }
 
+// A chosen or candidate expert's key in 64 bits (not the softmax's sums).
+template <typename T, bool SUMS>
+__device__ __forceinline__ double key64(const T *row, const RouteArgs &a, int id)
+{
+    const double x = (double)to_f32(row[id]);
+    return SUMS ? sigmoid(x) + (a.bias ? (double)__ldg(a.bias + id) : 0.0) : x;
+}
+
+// The groups that stay, by 64-bit ranks, from the row's 32-bit keys in `slot`: lane
+// g takes the four largest of group g, each known to within `error`, and ranks the
+// group by the best of their 64-bit keys.  False where more than four may count.
+template <typename T, int VPT, bool SUMS>
+__device__ __noinline__ bool groups64(const T *row, const RouteArgs &a, int lane, const float *slot, float error,
+                                      unsigned *kept)
+{
+    const int size = a.E / a.groups;
+    float v[5];
+    int e[4] = {-1, -1, -1, -1};
+#pragma unroll
+    for (int i = 0; i < 5; ++i) v[i] = -INFINITY;
+    if (lane < a.groups)
+        for (int i = 0; i < size; ++i) {
+            const int at = lane * size + i;
+            float x = slot[at];
+            int id = at;
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+                if (x > v[q]) {
+                    const float tv = v[q];
+                    const int te = e[q];
+                    v[q] = x;
+                    e[q] = id;
+                    x = tv;
+                    id = te;
+                }
+            v[4] = fmaxf(v[4], x);
+        }
+    const float need = a.group_top > 1 ? v[1] : v[0];  // a key this far below cannot count
+    const bool ok = !(need > -INFINITY) || need - v[4] > error;
+    double r1 = -INFINITY, r2 = -INFINITY, gap, largest;
+#pragma unroll
+    for (int q = 0; q < 4; ++q)
+        if (e[q] >= 0) push2(key64<T, SUMS>(row, a, e[q]), r1, r2);
+    *kept = keep_groups(r1, r2, lane, a, gap, largest);
+    return __all_sync(kAll, ok);
+}
+
 // The candidates, lane j < n the one of id `id`: lane j < k gets the j-th of them.
 template <typename T, bool SUMS>
 __device__ __noinline__ int order64(const T *row, const RouteArgs &a, int lane, int n, int id, int *list)
 {
     double key = -INFINITY;
-    if (lane < n) {
-        const double x = (double)to_f32(row[id]);
-        key = SUMS ? sigmoid(x) + (a.bias ? (double)__ldg(a.bias + id) : 0.0) : x;
-    }
+    if (lane < n) key = key64<T, SUMS>(row, a, id);
     int ahead = 0;
     for (int j = 0; j < n; ++j) {
         const double o = __shfl_sync(kAll, key, j);
@@ -260,14 +306,14 @@ __device__ __noinline__ int order64(const T *row, const RouteArgs &a, int lane, 
 template <int VPT>
 __device__ __forceinline__ float with_position(float v, int j)
 {
-    const uint32_t u = __float_as_uint(v);
-    return __uint_as_float((u & ~(uint32_t)(VPT - 1)) | ((int)u < 0 ? (uint32_t)j : (uint32_t)(VPT - 1 - j)));
+    const uint32_t u = __float_as_uint(v), mask = VPT - 1, negative = (uint32_t)((int)u >> 31);
+    return __uint_as_float((u & ~mask) | ((negative ^ (mask - j)) & mask));
 }
 template <int VPT>
 __device__ __forceinline__ int position_of(float v)
 {
-    const uint32_t u = __float_as_uint(v);
-    return (int)((u ^ ((int)u < 0 ? 0u : ~0u)) & (VPT - 1));
+    const uint32_t u = __float_as_uint(v), mask = VPT - 1, negative = (uint32_t)((int)u >> 31);
+    return (int)((u ^ ~negative) & mask);
 }
 // What two keys are compared by.
 template <int VPT>
@@ -297,7 +343,7 @@ __device__ __forceinline__ void sort_keys(float *v)
 
 // SUMS: the keys are s + bias (or group ranks are sums of scores), else logits.
 template <typename T, int VPT, bool SUMS>
-__global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constant__ RouteArgs a)
+__global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(const __grid_constant__ RouteArgs a)
 {
     __shared__ double slots[kWarps][32 * VPT];
     __shared__ int lists[kWarps][32];
@@ -338,12 +384,19 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         else
 #pragma unroll
             for (int j = 0; j < VPT; ++j) b[j] = 0.0f;
+        float v[VPT];
+        if (a.sigmoid) {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) v[j] = rcp_approx(1.0f + expf(-key[j])) + b[j];
+        } else {
+#pragma unroll
+            for (int j = 0; j < VPT; ++j) v[j] = expf(key[j] - top) * inv + b[j];
+        }
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
-            const float x = key[j];
-            const float v = (a.sigmoid ? rcp_approx(1.0f + expf(-x)) : expf(x - top) * inv) + b[j];
-            nan |= x > -INFINITY && v != v;
-            key[j] = x > -INFINITY && v > -INFINITY ? v : -INFINITY;
+            const bool in = key[j] > -INFINITY;
+            nan |= in && v[j] != v[j];
+            key[j] = in ? v[j] : -INFINITY;
         }
     }
     nan = __any_sync(kAll, nan);
@@ -351,19 +404,29 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     for (int j = 0; j < VPT; ++j)  // + 0 makes -0 a 0: they are equal
         key[j] = key[j] > -INFINITY ? with_position<VPT>(fminf(key[j], FLT_MAX) + 0.0f, j) : -INFINITY;
 
+    // How far the difference of two keys may be off: their scores' errors, the
+    // roundings of the sums with the bias, and the lowest bits of one (they are cut
+    // off, so the two errors have one sign).
+    const auto bound = [&](float v) { return 2.0f * serr + (VPT + 1) * 0x1p-23f * v + 0x1p-120f; };
     bool sure = true;  // of the groups that stay
-    float gap = INFINITY, largest = 0.0f;
+    float *slot = reinterpret_cast<float *>(slots[warp]);
     const int size = a.E / a.groups, lanes = size / VPT;
     const bool whole = size % VPT == 0 && (lanes & (lanes - 1)) == 0;  // a group is so many whole lanes
+    // of two ranks: twice as many keys, and a rounded sum each
+    const auto uncertain = [&](float gap, float largest) {
+        return !kExact && !(gap > 2.0f * bound(largest) + 0x1p-23f * largest);
+    };
     if (a.groups > 1 && !whole) {
-        float *slot = reinterpret_cast<float *>(slots[warp]);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) slot[lane * VPT + j] = without_position<VPT>(key[j]);
         __syncwarp();
-        float r1 = -INFINITY, r2 = -INFINITY;
+        float r1 = -INFINITY, r2 = -INFINITY, gap, largest;
         if (lane < a.groups)
             for (int i = 0; i < size; ++i) push2(slot[lane * size + i], r1, r2);
-        const unsigned kept = keep_groups(r1, r2, lane, a, gap, largest);
+        unsigned kept = keep_groups(r1, r2, lane, a, gap, largest);
+        if constexpr (!kExact)
+            if (uncertain(gap, largest))
+                sure = !(SUMS && !a.sigmoid) && groups64<T, VPT, SUMS>(row, a, lane, slot, bound(largest), &kept);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int e = lane * VPT + j;
@@ -374,26 +437,36 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
     sort_keys<VPT>(key);
     float head = without_position<VPT>(key[0]);
     if (a.groups > 1 && whole) {
-        float p = head, q = VPT > 1 ? without_position<VPT>(key[VPT > 1 ? 1 : 0]) : -INFINITY;
+        float p = head, q = VPT > 1 ? without_position<VPT>(key[VPT > 1 ? 1 : 0]) : -INFINITY, gap, largest;
         for (int o = 1; o < lanes; o <<= 1) {
             const float po = __shfl_xor_sync(kAll, p, o), qo = __shfl_xor_sync(kAll, q, o);
             q = fmaxf(fminf(p, po), fmaxf(q, qo));
             p = fmaxf(p, po);
         }
         const int src = min(lane * lanes, 31);
-        const unsigned kept = keep_groups(__shfl_sync(kAll, p, src), __shfl_sync(kAll, q, src), lane, a, gap, largest);
+        unsigned kept = keep_groups(__shfl_sync(kAll, p, src), __shfl_sync(kAll, q, src), lane, a, gap, largest);
+        if constexpr (!kExact)
+            if (uncertain(gap, largest)) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) slot[lane * VPT + j] = -INFINITY;
+#pragma unroll
+                for (int j = 0; j < VPT; ++j)
+                    if (key[j] > -INFINITY) slot[lane * VPT + position_of<VPT>(key[j])] = without_position<VPT>(key[j]);
+                __syncwarp();
+                sure = !(SUMS && !a.sigmoid) && groups64<T, VPT, SUMS>(row, a, lane, slot, bound(largest), &kept);
+                __syncwarp();
+            }
         const int g = lane / lanes;
         if (g >= a.groups || !((kept >> g) & 1u)) head = -INFINITY;  // and so the lane's other keys
     }
-    // a rank is one or two keys, each off by serr, by its rounding and by its lowest bits, and a rounded sum
-    if constexpr (!kExact) sure = gap > 4.0f * serr + (VPT + 2) * 0x1p-21f * largest;
 
+    const unsigned own = 1u << lane, lanes_to = own | (own - 1u);  // this lane's bit, and those up to it
     int n = 0;             // chosen so far; lane j < n keeps the j-th key
     float at = -INFINITY;
     const auto choose = [&](float m) {  // m is the largest head: of equal ones the lowest lane's
-        const int src = __ffs(__ballot_sync(kAll, head == m)) - 1;
+        const unsigned best = __ballot_sync(kAll, head == m);
         if (lane == n) at = m;
-        if (lane == src) {
+        if ((best & lanes_to) == own) {
             list[n] = lane * VPT + position_of<VPT>(key[0]);
 #pragma unroll
             for (int j = 0; j + 1 < VPT; ++j) key[j] = key[j + 1];
@@ -416,7 +489,6 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
         const float x = id >= 0 ? to_f32(row[id]) : 0.0f, b = id >= 0 && a.bias ? __ldg(a.bias + id) : 0.0f;
         const float atn = __shfl_down_sync(kAll, at, 1), xn = __shfl_down_sync(kAll, x, 1),
                     bn = __shfl_down_sync(kAll, b, 1);
-        const auto bound = [&](float v) { return 2.0f * serr + (VPT + 1) * 0x1p-22f * fabsf(v) + 0x1p-120f; };
         // equal logits and biases have equal keys: the index decides
         const bool open = __any_sync(kAll, lane + 1 < n && !(at - atn > bound(fmaxf(fabsf(at), fabsf(atn))) ||
                                                              (x == xn && b == bn)));
@@ -438,22 +510,25 @@ __global__ void __launch_bounds__(kWarps * 32) route_kernel(const __grid_constan
 
     const bool on = lane < a.k && id >= 0;
     const float x = on ? to_f32(row[id]) : -INFINITY;
-    float w;
+    float w, sum = 1.0f;
     if (a.sigmoid) {
-        w = on ? sigmoid(x) : 0.0f;
-        if (a.renormalize) w = w / fmaxf(warp_sum(w), 1e-30f);
+        w = on ? rcp_approx(1.0f + expf(-x)) : 0.0f;
+        if (a.renormalize) sum = warp_sum(w);
     } else if (a.renormalize) {
-        const float m = warp_max(x);
-        w = on ? expf(x - m) : 0.0f;
-        w = w / fmaxf(warp_sum(w), 1e-30f);
+        const float most = warp_max(x);
+        w = on ? expf(x - most) : 0.0f;
+        sum = warp_sum(w);
     } else {
         w = on ? expf(x - top) * inv : 0.0f;
     }
     if (lane < a.k) {
-        w = nan ? NAN : on ? w * a.scale : 0.0f;
-        const long long at_out = (long long)t * a.k + lane;
-        a.ids[at_out] = on ? id : -1;
-        for (int r = 0; r < a.R; ++r) a.w[(long long)r * a.T * a.k + at_out] = w;
+        w *= a.scale;
+        if (a.renormalize) w /= fmaxf(sum, 1e-30f);
+        if (nan) w = NAN;
+        const long long at_out = (long long)t * a.k + lane, shard = (long long)a.T * a.k;
+        a.ids[at_out] = id;
+        float *out = a.w + at_out;
+        for (int r = 0; r < a.R; ++r, out += shard) *out = w;
     }
 }
 
