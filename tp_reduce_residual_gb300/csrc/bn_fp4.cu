@@ -24,6 +24,8 @@
 // One warp per row (or per share of a row): a lane takes 16 values, the four
 // lanes of a scale tile row join their scale bytes into one 4-byte store.  DRAM
 // bandwidth bounds it at many rows.
+#include <type_traits>
+
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
@@ -76,11 +78,18 @@ __device__ __forceinline__ Place place_of(const QuantArgs &a, int m, int lane)
     return {g * a.tiles_per + (r >> 7), r & 127};
 }
 
-__device__ __forceinline__ uint32_t e2m1x2(float lo, float hi)
+// Eight codes, the first in the lowest four bits.
+__device__ __forceinline__ uint32_t e2m1x8(const f2 *y)
 {
+    float v[8];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f2_split(y[i], v[2 * i], v[2 * i + 1]);
     uint32_t r;
-    asm("{\n\t.reg .b8 q;\n\tcvt.rn.satfinite.e2m1x2.f32 q, %2, %1;\n\tcvt.u32.u8 %0, q;\n\t}"
-        : "=r"(r) : "f"(lo), "f"(hi));
+    asm("{\n\t.reg .b8 a, b, c, d;\n\t.reg .b16 e, f;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e2m1x2.f32 b, %4, %3;\n\t"
+        "cvt.rn.satfinite.e2m1x2.f32 c, %6, %5;\n\tcvt.rn.satfinite.e2m1x2.f32 d, %8, %7;\n\t"
+        "mov.b16 e, {a, b};\n\tmov.b16 f, {c, d};\n\tmov.b32 %0, {e, f};\n\t}"
+        : "=r"(r) : "f"(v[0]), "f"(v[1]), "f"(v[2]), "f"(v[3]), "f"(v[4]), "f"(v[5]), "f"(v[6]), "f"(v[7]));
     return r;
 }
 
@@ -103,13 +112,60 @@ __device__ __forceinline__ float e8m0_value(uint32_t code)
     return __uint_as_float(code == 255u ? 0x7fc00000u : code ? code << 23 : 0x00400000u);
 }
 
-__device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b)
+// The larger magnitudes of two pairs (a NaN where there is one); the signs are of no use.
+template <typename T> __device__ __forceinline__ uint32_t max_abs2(uint32_t a, uint32_t b);
+template <> __device__ __forceinline__ uint32_t max_abs2<__nv_bfloat16>(uint32_t a, uint32_t b)
 {
-    return __vmaxu2(a, b & 0x7fff7fffu);
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.bf16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+template <> __device__ __forceinline__ uint32_t max_abs2<__half>(uint32_t a, uint32_t b)
+{
+    uint32_t r;
+    asm("max.NaN.xorsign.abs.f16x2 %0, %1, %2;" : "=r"(r) : "r"(a), "r"(b));
+    return r;
+}
+
+// The block of 16 (half a block of 32) values in w: its codes and its scale byte.
+template <typename T, bool MX>
+__device__ __forceinline__ uint32_t quantize16(const uint32_t *w, float inv_tensor_scale, uint2 &codes)
+{
+    uint32_t top2 = max_abs2<T>(w[0], w[1]);
+#pragma unroll
+    for (int i = 2; i < 8; ++i) top2 = max_abs2<T>(top2, w[i]);
+    uint32_t top = max(top2 & 0x7fffu, (top2 >> 16) & 0x7fffu);  // bits of the largest magnitude
+    if (MX) top = max(top, __shfl_xor_sync(kAll, top, 1));
+    const bool bad = top >= Half2<T>::kInf;
+    const float amax = Half2<T>::widen(top).x * inv_tensor_scale;
+    uint32_t code;
+    float mul, scale = 1.0f;  // x * mul / scale is what is rounded
+    if (MX) {
+        const int e = (int)(__float_as_uint(amax) >> 23);  // exponent field; 0: nothing to scale
+        code = bad ? 255u : (uint32_t)max(e - 2, 0);
+        // 2^(127 - code), a subnormal for code 254
+        mul = bad ? 0.0f : __uint_as_float(code >= 254u ? 0x00400000u : (254u - code) << 23);
+    } else {
+        code = bad ? 0x7fu : e4m3(__fdiv_rn(amax, 6.0f));
+        scale = e4m3_value(code);
+        mul = bad || code == 0 ? 0.0f : __frcp_rn(scale);
+    }
+    const f2 inv2 = f2_make(inv_tensor_scale, inv_tensor_scale), mul2v = f2_make(mul, mul), neg = f2_make(-scale, -scale);
+    f2 y[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+        const float2 h = Half2<T>::widen(w[i]);
+        f2 v = f2_make(h.x, h.y);
+        if (inv_tensor_scale != 1.0f) v = mul2(v, inv2);
+        y[i] = mul2(v, mul2v);
+        if (!MX) y[i] = fma2(fma2(y[i], neg, v), mul2v, y[i]);  // the remainder makes an exact quotient exact
+    }
+    codes = bad ? make_uint2(0, 0) : make_uint2(e2m1x8(y), e2m1x8(y + 4));
+    return code;
 }
 
 template <typename T, bool MX>
-__global__ void __launch_bounds__(kRowWarps * 32) quantize_kernel(QuantArgs a, int chunks, int share)
+__global__ void __launch_bounds__(kRowWarps * 32) quantize_kernel(const __grid_constant__ QuantArgs a, int chunks, int share)
 {
     const int lane = threadIdx.x & 31;
     const int m = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
@@ -129,97 +185,76 @@ __global__ void __launch_bounds__(kRowWarps * 32) quantize_kernel(QuantArgs a, i
     uint8_t *data = a.data + (long long)m * (a.K / 2);
     // scales of this row: 4 bytes of every 512-byte tile
     uint8_t *scales = a.scales + ((long long)p.tile * chunks) * 512 + (p.r & 31) * 16 + (p.r >> 5) * 4;
-    constexpr int kChunk = MX ? 128 : 64;  // values of a row in one scale tile
-    const int end = chunks * kChunk;       // the padded row: its last scales are written as 0
-    const int k1 = min(end, (int)(blockIdx.y + 1) * share);
-    for (int k0 = blockIdx.y * share; k0 < k1; k0 += 512) {
-        const int k = k0 + lane * 16;
-        uint4 q0 = make_uint4(0, 0, 0, 0), q1 = q0;
-        if (k < a.K) q0 = __ldg(reinterpret_cast<const uint4 *>(x + k));
-        if (k < a.K) q1 = __ldg(reinterpret_cast<const uint4 *>(x + k + 8));
-        const uint32_t w[8] = {q0.x, q0.y, q0.z, q0.w, q1.x, q1.y, q1.z, q1.w};
-        uint32_t top2 = 0;
+    constexpr unsigned kChunk = MX ? 128 : 64;  // values of a row in one scale tile
+    constexpr unsigned kAhead = 2;         // steps of 512 values whose loads are in flight together
+    const unsigned end = (unsigned)chunks * kChunk;  // the padded row: its last scales are written as 0
+    const unsigned K = (unsigned)a.K, k1 = min(end, (blockIdx.y + 1) * (unsigned)share), inside = min(K, k1);
+    unsigned k = blockIdx.y * (unsigned)share + lane * 16u;
+    // `kAhead` steps from k on; FULL: all their values are inside the row
+    const auto steps = [&](auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        uint32_t w[kAhead][8];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) top2 = max_abs2(top2, w[i]);
-        uint32_t top = max(top2 & 0xffffu, top2 >> 16);  // bits of the largest magnitude
-        if (MX) top = max(top, __shfl_xor_sync(kAll, top, 1));
-        const bool bad = top >= Half2<T>::kInf;
-        const float amax = Half2<T>::widen(top).x * a.inv_tensor_scale;
-        uint32_t code;
-        float mul, scale = 1.0f;  // x * mul / scale is what is rounded
-        if (MX) {
-            const int e = (int)(__float_as_uint(amax) >> 23);  // exponent field; 0: nothing to scale
-            code = bad ? 255u : (uint32_t)max(e - 2, 0);
-            // 2^(127 - code), a subnormal for code 254
-            mul = __uint_as_float(code >= 254u ? 0x00400000u : (254u - code) << 23);
-        } else {
-            code = bad ? 0x7fu : e4m3(__fdiv_rn(amax, 6.0f));
-            scale = e4m3_value(code);
-            mul = bad || code == 0 ? 0.0f : __frcp_rn(scale);
-        }
-        if (bad) mul = 0.0f;
-        uint32_t packed[2] = {0, 0};
-#pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            float2 v = Half2<T>::widen(w[i]);
-            v.x *= a.inv_tensor_scale;
-            v.y *= a.inv_tensor_scale;
-            float2 y = make_float2(v.x * mul, v.y * mul);
-            if (!MX) {  // the remainder makes an exact quotient exact
-                y.x = __fmaf_rn(__fmaf_rn(-y.x, scale, v.x), mul, y.x);
-                y.y = __fmaf_rn(__fmaf_rn(-y.y, scale, v.y), mul, y.y);
+        for (unsigned u = 0; u < kAhead; ++u) {
+            uint4 q0 = make_uint4(0, 0, 0, 0), q1 = q0;
+            if (FULL || k + 512 * u < inside) {
+                q0 = __ldg(reinterpret_cast<const uint4 *>(x + k + 512 * u));
+                q1 = __ldg(reinterpret_cast<const uint4 *>(x + k + 512 * u + 8));
             }
-            packed[i >> 2] |= e2m1x2(y.x, y.y) << (8 * (i & 3));
+            w[u][0] = q0.x, w[u][1] = q0.y, w[u][2] = q0.z, w[u][3] = q0.w;
+            w[u][4] = q1.x, w[u][5] = q1.y, w[u][6] = q1.z, w[u][7] = q1.w;
         }
-        if (bad) packed[0] = packed[1] = 0;
-        if (k < a.K) *reinterpret_cast<uint2 *>(data + k / 2) = make_uint2(packed[0], packed[1]);
-        if (k >= a.K) code = 0;
-        // four scales of one tile row: of lanes 0..3 of four (NVFP4) or of every second of eight (MXFP4)
-        uint32_t word;
-        if (MX) {
-            word = code | (__shfl_down_sync(kAll, code, 2) << 8);
-            word |= __shfl_down_sync(kAll, word, 4) << 16;
-        } else {
-            word = code | (__shfl_down_sync(kAll, code, 1) << 8);
-            word |= __shfl_down_sync(kAll, word, 2) << 16;
+#pragma unroll
+        for (unsigned u = 0; u < kAhead; ++u) {
+            const unsigned at = k + 512 * u;
+            uint2 codes;
+            uint32_t code = quantize16<T, MX>(w[u], a.inv_tensor_scale, codes);
+            if (FULL || at < inside) *reinterpret_cast<uint2 *>(data + at / 2) = codes;
+            if (!FULL && at >= K) code = 0;
+            // four scales of one tile row: of lanes 0..3 of four (NVFP4) or of every second of eight (MXFP4)
+            uint32_t word = code | (__shfl_down_sync(kAll, code, MX ? 2 : 1) << 8);
+            word |= __shfl_down_sync(kAll, word, MX ? 4 : 2) << 16;
+            if ((lane & (MX ? 7 : 3)) == 0 && (FULL || at < k1))
+                *reinterpret_cast<uint32_t *>(scales + (size_t)(at / kChunk) * 512) = word;
         }
-        if ((lane & (MX ? 7 : 3)) == 0 && k < end)
-            *reinterpret_cast<uint32_t *>(scales + (long long)(k / kChunk) * 512) = word;
-    }
+        k += 512 * kAhead;
+    };
+    while (k - lane * 16u + 512 * kAhead <= inside) steps(std::true_type{});
+    while (k - lane * 16u < k1) steps(std::false_type{});
 }
 
-template <typename T> __device__ __forceinline__ void store16(T *out, const float *v);
-template <> __device__ __forceinline__ void store16(float *out, const float *v)
+// Eight values at an address of 16 bytes' alignment.
+template <typename T> __device__ __forceinline__ void store8(T *out, const f2 *v);
+template <> __device__ __forceinline__ void store8(float *out, const f2 *v)
 {
+    float x[8];
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-        reinterpret_cast<float4 *>(out)[i] = make_float4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+    for (int i = 0; i < 4; ++i) f2_split(v[i], x[2 * i], x[2 * i + 1]);
+    reinterpret_cast<float4 *>(out)[0] = make_float4(x[0], x[1], x[2], x[3]);
+    reinterpret_cast<float4 *>(out)[1] = make_float4(x[4], x[5], x[6], x[7]);
 }
-template <> __device__ __forceinline__ void store16(__nv_bfloat16 *out, const float *v)
+template <> __device__ __forceinline__ void store8(__nv_bfloat16 *out, const f2 *v)
 {
-    uint32_t w[8];
+    uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const __nv_bfloat162 h = __floats2bfloat162_rn(v[2 * i], v[2 * i + 1]);
+    for (int i = 0; i < 4; ++i) w[i] = round2(v[i]);
+    *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
+}
+template <> __device__ __forceinline__ void store8(__half *out, const f2 *v)
+{
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        float x, y;
+        f2_split(v[i], x, y);
+        const __half2 h = __floats2half2_rn(x, y);
         w[i] = *reinterpret_cast<const uint32_t *>(&h);
     }
-    reinterpret_cast<uint4 *>(out)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4 *>(out)[1] = make_uint4(w[4], w[5], w[6], w[7]);
-}
-template <> __device__ __forceinline__ void store16(__half *out, const float *v)
-{
-    uint32_t w[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-        const __half2 h = __floats2half2_rn(v[2 * i], v[2 * i + 1]);
-        w[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-    reinterpret_cast<uint4 *>(out)[0] = make_uint4(w[0], w[1], w[2], w[3]);
-    reinterpret_cast<uint4 *>(out)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    *reinterpret_cast<uint4 *>(out) = make_uint4(w[0], w[1], w[2], w[3]);
 }
 
 template <typename T, bool MX>
-__global__ void __launch_bounds__(kRowWarps * 32) dequantize_kernel(QuantArgs a, int chunks, int share)
+__global__ void __launch_bounds__(kRowWarps * 32) dequantize_kernel(const __grid_constant__ QuantArgs a, int chunks, int share)
 {
     const int lane = threadIdx.x & 31;
     const int m = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
@@ -230,29 +265,47 @@ __global__ void __launch_bounds__(kRowWarps * 32) dequantize_kernel(QuantArgs a,
     const uint8_t *data = a.data + (long long)m * (a.K / 2);
     const uint8_t *scales = a.scales + ((long long)p.tile * chunks) * 512 + (p.r & 31) * 16 + (p.r >> 5) * 4;
     T *out = static_cast<T *>(a.out) + (long long)m * a.K;
-    constexpr int kChunk = MX ? 128 : 64;
-    const int k1 = min(a.K, (int)(blockIdx.y + 1) * share);
-    for (int k0 = blockIdx.y * share; k0 < k1; k0 += 512) {
-        const int k = k0 + lane * 16;
-        if (k >= k1) break;
-        const uint2 q = __ldg(reinterpret_cast<const uint2 *>(data + k / 2));
-        const uint32_t b = scales[(long long)(k / kChunk) * 512 + k % kChunk / (MX ? 32 : 16)];
-        const float s = (MX ? e8m0_value(b) : e4m3_value(b)) * a.tensor_scale;
-        float v[16];
+    constexpr unsigned kChunk = MX ? 128 : 64;
+    constexpr unsigned kAhead = 4;  // steps of 256 values, 8 a lane, whose loads are in flight together
+    const unsigned k1 = min((unsigned)a.K, (blockIdx.y + 1) * (unsigned)share);
+    unsigned k = blockIdx.y * (unsigned)share + lane * 8u;
+    const auto steps = [&](auto full) {
+        constexpr bool FULL = decltype(full)::value;
+        uint32_t q[kAhead], b[kAhead];
 #pragma unroll
-        for (int i = 0; i < 8; ++i) {
-            const uint32_t byte = ((i < 4 ? q.x : q.y) >> (8 * (i & 3))) & 0xffu;
-            uint32_t h;
-            asm("{\n\t.reg .b8 q;\n\tcvt.u8.u32 q, %1;\n\tcvt.rn.f16x2.e2m1x2 %0, q;\n\t}" : "=r"(h) : "r"(byte));
-            const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h));
-            v[2 * i] = f.x * s;
-            v[2 * i + 1] = f.y * s;
+        for (unsigned u = 0; u < kAhead; ++u) {
+            const unsigned at = k + 256 * u;
+            if (FULL || at < k1) {
+                q[u] = __ldg(reinterpret_cast<const uint32_t *>(data + at / 2));
+                b[u] = __ldg(scales + (size_t)(at / kChunk) * 512 + at % kChunk / (MX ? 32 : 16));
+            }
         }
-        store16<T>(out + k, v);
-    }
+#pragma unroll
+        for (unsigned u = 0; u < kAhead; ++u) {
+            const unsigned at = k + 256 * u;
+            if (!FULL && at >= k1) break;
+            const float s = (MX ? e8m0_value(b[u]) : e4m3_value(b[u])) * a.tensor_scale;
+            const f2 s2 = f2_make(s, s);
+            uint32_t h[4];
+            asm("{\n\t.reg .b8 a, b, c, d;\n\tmov.b32 {a, b, c, d}, %4;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %0, a;\n\tcvt.rn.f16x2.e2m1x2 %1, b;\n\t"
+                "cvt.rn.f16x2.e2m1x2 %2, c;\n\tcvt.rn.f16x2.e2m1x2 %3, d;\n\t}"
+                : "=r"(h[0]), "=r"(h[1]), "=r"(h[2]), "=r"(h[3]) : "r"(q[u]));
+            f2 v[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = __half22float2(*reinterpret_cast<const __half2 *>(&h[i]));
+                v[i] = mul2(f2_make(f.x, f.y), s2);
+            }
+            store8<T>(out + at, v);
+        }
+        k += 256 * kAhead;
+    };
+    while (k - lane * 8u + 256 * kAhead <= k1) steps(std::true_type{});
+    while (k < k1) steps(std::false_type{});
 }
 
-// Values per block of a row: whole rows when there are warps enough for the
+// Values of a row per block: whole rows when there are warps enough for the
 // device, else shares of 512 values and more.
 void split_rows(const QuantArgs &a, int sms, dim3 *grid, int *share)
 {
