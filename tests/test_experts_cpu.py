@@ -51,7 +51,7 @@ def test_route_refuses(L, kw, status, needle):
 def test_no_tokens_is_no_work(L):
     assert L.bn_route(*dict(ROUTE, T=0, logits=None, ids=None, w=None).values()) == bn.OK
     assert L.bn_route_backward(None, 0, 64, 0, 64, 8, None, None, 1, 0, 1, 1.0, None, None) == bn.OK
-    assert L.bn_quantize_fp4(None, 0, 64, 0, None, 0, 64, None, 1, 0, 1.0, None, None, None) == bn.OK
+    assert L.bn_quantize_fp4(None, 0, 64, 0, None, 0, 64, None, 1, 0, 1.0, None, None, None, 0, None) == bn.OK
     assert L.bn_dequantize_fp4(None, None, 0, 64, None, 1, 0, 1.0, None, 0, None) == bn.OK
     assert L.bn_expert_product(None, None, 0, None, None, 4, 64, 64, at(0), 0, 1.0, None, None) == bn.OK
 
@@ -85,11 +85,12 @@ def test_plan_refuses(L, kw, status, needle):
     (dict(tensor_scale=math.nan), 1, "power of two"), (dict(tensor_scale=2.0 ** 65), 1, "power of two"),
     (dict(rows=None), 1, "no rows are given"), (dict(x_rows=0), 1, "x has no rows"), (dict(x=at(0) + 2), 1, "x is not 16-byte"),
     (dict(data=None), 1, "data is NULL"), (dict(scales=at(2) + 4), 1, "scales is not"), (dict(data=at(0)), 1, "data overlaps x"),
-    (dict(scales=at(4)), 1, "scales overlaps offsets"),
+    (dict(scales=at(4)), 1, "scales overlaps offsets"), (dict(work=at(5) + 8), 1, "workspace is not 16-byte"),
+    (dict(work=at(0)), 1, "workspace overlaps x"), (dict(work=at(1)), 1, "data overlaps workspace"),
 ])
 def test_quantize_refuses(L, kw, status, needle):
     a = dict(x=at(0), dtype=0, ld=64, x_rows=5, rows=at(3), M=8, K=64, offsets=at(4), groups=4, format=0, tensor_scale=0.5,
-             data=at(1), scales=at(2), stream=None)
+             data=at(1), scales=at(2), work=at(5), work_bytes=64, stream=None)
     refuses(L, "bn_quantize_fp4", status, needle, *dict(a, **kw).values())
 
 
@@ -127,6 +128,14 @@ def test_scale_bytes(L):
         for M, K, g, ragged in ((1, 64, 1, False), (300, 160, 7, True), (260, 2048, 2, False)):
             n = experts.fp4_scales_shape(M, K, fmt, g, ragged)
             assert n[0] * n[1] * n[2] == f(M, K, g, int(ragged), experts.FORMATS[fmt])
+
+
+def test_quantize_workspace_bytes(L):
+    f = L.bn_quantize_fp4_workspace_bytes
+    assert f(4096, 32768, 5120, 1) == 4096 * (2560 + 40 * 4) and f(4096, 32768, 5120, 0) == 4096 * (2560 + 80 * 4)
+    assert f(5, 50, 8192, 0) == 0 and f(16384, 32768, 5120, 0) == 0      # little work; rows taken twice
+    assert f(0, 32768, 5120, 0) == 0 and f(64, 32768, 5100, 0) == 0 and f(64, 32768, 5120, 3) == 0
+    assert experts.quantize_workspace_bytes(4096, 32768, 5120, "mxfp4") == f(4096, 32768, 5120, 1)
 
 
 def test_ragged_tiles_never_meet():

@@ -367,6 +367,35 @@ def test_quantize_grouped_rows(fmt, counts, tail):
     assert torch.equal(experts.dequantize_fp4(q).cpu().double(), want)
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp16"])
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("K", [544, 2048])
+def test_quantize_repeated_rows_through_the_workspace(fmt, dtype, K):
+    """Places that take a row many times: the same bytes with the workspace and without."""
+    g = gen(K)
+    n, M = 300, 31000
+    x = torch.randn(n, K, generator=g).to(DTYPES[dtype]).cuda()
+    rows = torch.randint(0, n, (M,), generator=g).to(torch.int32)
+    rows[17] = -3
+    rows[M - 1] = n
+    counts = torch.randint(0, 2 * M // 50, (50,), generator=g)
+    offsets = torch.cat((torch.zeros(1, dtype=torch.long), counts.cumsum(0))).clamp_max(M - 5).to(torch.int32)
+    need = experts.quantize_workspace_bytes(n, M, K, fmt)
+    assert (need > 0) == (M * K >= 1 << 24)
+    shape = experts.fp4_scales_shape(M, K, fmt, 50, True)
+    got = []
+    for work in (None, torch.empty(max(need, 16), dtype=torch.uint8, device="cuda"), torch.empty(16, dtype=torch.uint8, device="cuda")):
+        scales = torch.full(shape, 85, dtype=torch.uint8, device="cuda")
+        q = experts.quantize_fp4(x, fmt, rows=rows.cuda(), offsets=offsets.cuda(), scales=scales, workspace=work)
+        assert bn.check_device_error(raise_on_error=False) == bn.DEVERR_PERM_RANGE
+        got.append((q.data.clone(), scales))
+    for data, scales in got[1:]:
+        assert torch.equal(data, got[0][0]) and torch.equal(scales, got[0][1])
+    plain = experts.quantize_fp4(x, fmt)
+    want = experts.dequantize_fp4(plain)[rows.long().where((rows >= 0) & (rows < n), torch.zeros(1, dtype=torch.long)).cuda()]
+    assert torch.equal(experts.dequantize_fp4(experts.FP4(got[0][0], got[0][1], fmt, offsets.cuda())), want)
+
+
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 def test_quantize_weights_and_bad_rows(fmt):
     w = torch.randn(3, 136, 64, generator=gen(1)).bfloat16().cuda()

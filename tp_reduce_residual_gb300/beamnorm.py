@@ -36,6 +36,7 @@ EXPORTS = (
     "bn_finalize_reduce_residual_norm_ws", "bn_finalize_reduce_norm_noalloc",
     "bn_residual_norm_only", "bn_supports_op", "bn_shutdown",
     "bn_route", "bn_route_backward", "bn_expert_plan", "bn_fp4_scale_bytes", "bn_quantize_fp4",
+    "bn_quantize_fp4_workspace_bytes",
     "bn_dequantize_fp4", "bn_expert_product",
 )
 
@@ -130,7 +131,8 @@ def load() -> ctypes.CDLL:
             "bn_route_backward": [_P, _I, _L, _I, _I, _I, _P, _P, _I, _I, _I, _F, _P, _P],
             "bn_expert_plan": [_P, _I, _I, _I, _I, _P, _P, _P, _P],
             "bn_fp4_scale_bytes": [_I, _I, _I, _I, _I],
-            "bn_quantize_fp4": [_P, _I, _L, _I, _P, _I, _I, _P, _I, _I, _F, _P, _P, _P],
+            "bn_quantize_fp4": [_P, _I, _L, _I, _P, _I, _I, _P, _I, _I, _F, _P, _P, _P, ctypes.c_size_t, _P],
+            "bn_quantize_fp4_workspace_bytes": [_I, _I, _I, _I],
             "bn_dequantize_fp4": [_P, _P, _I, _I, _P, _I, _I, _F, _P, _I, _P],
             "bn_expert_product": [_P, _P, _I, _P, _P, _I, _I, _I, _P, _I, _F, _P, _P],
         }
@@ -142,6 +144,7 @@ def load() -> ctypes.CDLL:
         L.bn_shutdown.restype = None
         L.bn_finalize_workspace_bytes.restype = ctypes.c_size_t
         L.bn_fp4_scale_bytes.restype = ctypes.c_size_t
+        L.bn_quantize_fp4_workspace_bytes.restype = ctypes.c_size_t
         L.bn_last_error.restype = ctypes.c_char_p
         L.bn_status_string.restype = ctypes.c_char_p
         _lib = L

@@ -64,6 +64,7 @@ struct QuantArgs {
     float tensor_scale, inv_tensor_scale;
     uint8_t *data;         // [M, K / 2]
     uint8_t *scales;       // [tiles, chunks, 512]
+    uint8_t *work;         // or null: the rows of x quantised once (codes, then scale bytes side by side)
     void *out;             // [M, K] (dequantise)
     unsigned *err;
 };

@@ -1,6 +1,7 @@
 // bn_experts_abi.cu -- the C entry points around the experts: host-side
 // validation and launches.  Like the rest of the ABI, arguments are checked
-// before any CUDA call, and each call enqueues exactly one kernel or nothing.
+// before any CUDA call, and each call enqueues one kernel (two for a quantisation
+// with a workspace) or nothing.
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -228,9 +229,17 @@ size_t bn_fp4_scale_bytes(int M, int K, int groups, int ragged, bn_fp4 format)
     return scale_bytes(M, K, groups, ragged != 0, format);
 }
 
+size_t bn_quantize_fp4_workspace_bytes(int x_rows, int M, int K, bn_fp4 format)
+{
+    if (x_rows < 1 || M < 1 || K < 32 || K % 32 != 0 || (format != BN_NVFP4 && format != BN_MXFP4)) return 0;
+    if (M / 4 < x_rows || (long long)M * K < (1LL << 24)) return 0;
+    const int per = format == BN_MXFP4 ? 128 : 64;
+    return (size_t)x_rows * ((size_t)K / 2 + 4 * (size_t)((K + per - 1) / per));
+}
+
 bn_status bn_quantize_fp4(const void *x, bn_dtype dtype, long long ld, int x_rows, const int32_t *rows, int M, int K,
                           const int32_t *offsets, int groups, bn_fp4 format, float tensor_scale, uint8_t *data,
-                          uint8_t *scales, void *stream)
+                          uint8_t *scales, void *workspace, size_t workspace_bytes, void *stream)
 {
     clear_message();
     BN_TRY(check_dtype(dtype, false));
@@ -245,15 +254,19 @@ bn_status bn_quantize_fp4(const void *x, bn_dtype dtype, long long ld, int x_row
     BN_REQUIRE(aligned(rows, 4), "rows is not 4-byte aligned");
     BN_TRY(check_ptr16(data, "data"));
     BN_TRY(check_ptr16(scales, "scales"));
+    BN_TRY(check_ptr16(workspace, "workspace", false));
     const Range writes[] = {{data, (size_t)M * (K / 2), "data"},
-                            {scales, scale_bytes(M, K, groups, offsets != nullptr, format), "scales"}};
+                            {scales, scale_bytes(M, K, groups, offsets != nullptr, format), "scales"},
+                            {workspace, workspace_bytes, "workspace"}};
     const Range reads[] = {{x, span(x_rows, ld, K, 2), "x"},
                            {rows, (size_t)M * 4, "rows"},
                            {offsets, (size_t)(groups + 1) * 4, "offsets"}};
-    BN_TRY(check_overlaps(writes, 2, reads, 3));
+    BN_TRY(check_overlaps(writes, 3, reads, 3));
     const DeviceInfo *d = nullptr;
     BN_TRY(device_info(&d));
+    const size_t need = rows ? bn_quantize_fp4_workspace_bytes(x_rows, M, K, format) : 0;
     QuantArgs a = {};
+    a.work = need && workspace && workspace_bytes >= need ? static_cast<uint8_t *>(workspace) : nullptr;
     a.x = x;
     a.ld = ld;
     a.x_rows = x_rows;

@@ -22,8 +22,9 @@
 // a sum over the groups.  Scales past the end of a row are 0.
 //
 // One warp per row (or per share of a row): a lane takes 16 values, the four
-// lanes of a scale tile row join their scale bytes into one 4-byte store.  DRAM
-// bandwidth bounds it at many rows.
+// lanes of a scale tile row join their scale bytes into one 4-byte store.  About 7
+// instructions a value bound the quantisation, so rows that are repeated (a token's
+// for each of its experts) are quantised once into a workspace and copied from there.
 #include <type_traits>
 
 #include <cuda_bf16.h>
@@ -164,7 +165,8 @@ __device__ __forceinline__ uint32_t quantize16(const uint32_t *w, float inv_tens
     return code;
 }
 
-template <typename T, bool MX>
+// WORK: into a workspace, whose rows have their scale bytes side by side.
+template <typename T, bool MX, bool WORK>
 __global__ void __launch_bounds__(kRowWarps * 32) quantize_kernel(const __grid_constant__ QuantArgs a, int chunks, int share)
 {
     const int lane = threadIdx.x & 31;
@@ -180,11 +182,12 @@ __global__ void __launch_bounds__(kRowWarps * 32) quantize_kernel(const __grid_c
             src = 0;
         }
     }
-    const Place p = place_of(a, m, lane);
+    const Place p = WORK ? Place{0, 0} : place_of(a, m, lane);
     const T *x = static_cast<const T *>(a.x) + src * a.ld;
     uint8_t *data = a.data + (long long)m * (a.K / 2);
     // scales of this row: 4 bytes of every 512-byte tile
-    uint8_t *scales = a.scales + ((long long)p.tile * chunks) * 512 + (p.r & 31) * 16 + (p.r >> 5) * 4;
+    uint8_t *scales = a.scales + (WORK ? (long long)m * chunks * 4
+                                       : (long long)p.tile * chunks * 512 + (p.r & 31) * 16 + (p.r >> 5) * 4);
     constexpr unsigned kChunk = MX ? 128 : 64;  // values of a row in one scale tile
     constexpr unsigned kAhead = 2;         // steps of 512 values whose loads are in flight together
     const unsigned end = (unsigned)chunks * kChunk;  // the padded row: its last scales are written as 0
@@ -215,12 +218,45 @@ __global__ void __launch_bounds__(kRowWarps * 32) quantize_kernel(const __grid_c
             uint32_t word = code | (__shfl_down_sync(kAll, code, MX ? 2 : 1) << 8);
             word |= __shfl_down_sync(kAll, word, MX ? 4 : 2) << 16;
             if ((lane & (MX ? 7 : 3)) == 0 && (FULL || at < k1))
-                *reinterpret_cast<uint32_t *>(scales + (size_t)(at / kChunk) * 512) = word;
+                *reinterpret_cast<uint32_t *>(scales + (size_t)(at / kChunk) * (WORK ? 4 : 512)) = word;
         }
         k += 512 * kAhead;
     };
     while (k - lane * 16u + 512 * kAhead <= inside) steps(std::true_type{});
     while (k - lane * 16u < k1) steps(std::false_type{});
+}
+
+// Quantised rows from the workspace to their places.
+__global__ void __launch_bounds__(kRowWarps * 32)
+place_rows_kernel(const __grid_constant__ QuantArgs a, const uint8_t *work, const uint32_t *work_scales, unsigned chunks)
+{
+    const int lane = threadIdx.x & 31;
+    const int m = blockIdx.x * kRowWarps + (threadIdx.x >> 5);
+    griddep_launch_dependents();
+    griddep_wait();
+    if (m >= a.M) return;
+    long long src = __ldg(a.rows + m);
+    if (src < 0 || src >= a.x_rows) {
+        if (lane == 0) atomicOr(a.err, BN_DEVERR_PERM_RANGE);
+        src = 0;
+    }
+    const Place p = place_of(a, m, lane);
+    const uint4 *from = reinterpret_cast<const uint4 *>(work + src * (a.K / 2));
+    uint4 *to = reinterpret_cast<uint4 *>(a.data + (long long)m * (a.K / 2));
+    const unsigned n = (unsigned)a.K / 32;
+    constexpr unsigned kAhead = 4;
+    for (unsigned i = lane; i < n; i += 32 * kAhead) {
+        uint4 v[kAhead];
+#pragma unroll
+        for (unsigned u = 0; u < kAhead; ++u)
+            if (i + 32 * u < n) v[u] = __ldg(from + i + 32 * u);
+#pragma unroll
+        for (unsigned u = 0; u < kAhead; ++u)
+            if (i + 32 * u < n) to[i + 32 * u] = v[u];
+    }
+    uint8_t *scales = a.scales + (long long)p.tile * chunks * 512 + (p.r & 31) * 16 + (p.r >> 5) * 4;
+    for (unsigned c = lane; c < chunks; c += 32)
+        *reinterpret_cast<uint32_t *>(scales + (size_t)c * 512) = __ldg(work_scales + src * chunks + c);
 }
 
 // Eight values at an address of 16 bytes' alignment.
@@ -325,11 +361,25 @@ cudaError_t launch_quantize(const QuantArgs &a, int dtype, int fmt, int sms, boo
 {
     dim3 grid;
     int share;
-    split_rows(a, sms, &grid, &share);
     const int per = fmt ? 128 : 64, chunks = (a.K + per - 1) / per;
-    auto *k = dtype == 0 ? (fmt ? quantize_kernel<__nv_bfloat16, true> : quantize_kernel<__nv_bfloat16, false>)
-                         : (fmt ? quantize_kernel<__half, true> : quantize_kernel<__half, false>);
-    return launch_kernel(k, grid, dim3(kRowWarps * 32), 0, pdl, 1, st, a, chunks, share);
+    if (!a.work) {
+        split_rows(a, sms, &grid, &share);
+        auto *k = dtype == 0 ? (fmt ? quantize_kernel<__nv_bfloat16, true, false> : quantize_kernel<__nv_bfloat16, false, false>)
+                             : (fmt ? quantize_kernel<__half, true, false> : quantize_kernel<__half, false, false>);
+        return launch_kernel(k, grid, dim3(kRowWarps * 32), 0, pdl, 1, st, a, chunks, share);
+    }
+    QuantArgs once = a;
+    once.rows = nullptr;
+    once.M = (int)a.x_rows;
+    once.data = a.work;
+    once.scales = a.work + (size_t)a.x_rows * (a.K / 2);
+    split_rows(once, sms, &grid, &share);
+    auto *k = dtype == 0 ? (fmt ? quantize_kernel<__nv_bfloat16, true, true> : quantize_kernel<__nv_bfloat16, false, true>)
+                         : (fmt ? quantize_kernel<__half, true, true> : quantize_kernel<__half, false, true>);
+    const cudaError_t e = launch_kernel(k, grid, dim3(kRowWarps * 32), 0, pdl, 1, st, once, chunks, share);
+    if (e != cudaSuccess) return e;
+    return launch_kernel(place_rows_kernel, dim3((unsigned)((a.M + kRowWarps - 1) / kRowWarps)), dim3(kRowWarps * 32), 0, pdl,
+                         1, st, a, (const uint8_t *)a.work, (const uint32_t *)once.scales, (unsigned)chunks);
 }
 
 cudaError_t launch_dequantize(const QuantArgs &a, int dtype, int fmt, int sms, bool pdl, cudaStream_t st)

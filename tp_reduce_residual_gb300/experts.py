@@ -216,12 +216,21 @@ def _layout(q: FP4, name: str):
     return M, K, groups, op, dp, sp
 
 
+def quantize_workspace_bytes(n: int, M: int, K: int, format: str) -> int:
+    """Workspace bytes with which ``quantize_fp4`` quantises n rows once for M
+    places, or 0 where that does not pay."""
+    return (_bn._lib or _bn.load()).bn_quantize_fp4_workspace_bytes(n, M, K, _name(FORMATS, format, "format"))
+
+
 def quantize_fp4(x, format: str, rows=None, offsets=None, tensor_scale: float = 1.0,
-                 data=None, scales=None, stream=None) -> FP4:
+                 data=None, scales=None, workspace=None, stream=None) -> FP4:
     """Rows of ``x`` ([n,K], or [groups,n,K] such as weights; BF16 or FP16) in
     4-bit floating point.  ``rows`` (int32 [M]) picks the rows, ``offsets``
     (int32 [groups+1]) are the ragged groups of the result, as ``plan`` gives
-    them; ``tensor_scale`` is a power of two."""
+    them; ``tensor_scale`` is a power of two.  Where many places take the same
+    row, rows are quantised once into a ``workspace`` (a 1-D uint8 tensor of
+    ``quantize_workspace_bytes``; by default one is allocated for the call when
+    it runs on the current stream) and copied from there: the same result."""
     fmt = _name(FORMATS, format, "format")
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
@@ -257,7 +266,16 @@ def quantize_fp4(x, format: str, rows=None, offsets=None, tensor_scale: float = 
     groups = max(groups, 1)
     data, dp = _out(data, "data", _UINT8, dshape, dev)
     scales, sp = _out(scales, "scales", _UINT8, fp4_scales_shape(M, K, format, groups, op is not None), dev)
-    _call("bn_quantize_fp4", (x.data_ptr(), dtype, ld, n, rp, M, K, op, groups, fmt, tensor_scale, dp, sp), dev.index, stream)
+    wp, wn = None, 0
+    if workspace is not None:
+        wp, wn = _bn._workspace(workspace, dev)
+    elif rp is not None and M >= 4 * n and stream is None:
+        wn = quantize_workspace_bytes(n, M, K, format)
+        if wn:
+            workspace = torch.empty(wn, dtype=_UINT8, device=dev)
+            wp = workspace.data_ptr()
+    _call("bn_quantize_fp4", (x.data_ptr(), dtype, ld, n, rp, M, K, op, groups, fmt, tensor_scale, dp, sp, wp, wn), dev.index,
+          stream)
     return FP4(data, scales, format, offsets, tensor_scale)
 
 
