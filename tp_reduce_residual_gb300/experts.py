@@ -269,7 +269,7 @@ def quantize_fp4(x, format: str, rows=None, offsets=None, tensor_scale: float = 
     wp, wn = None, 0
     if workspace is not None:
         wp, wn = _bn._workspace(workspace, dev)
-    elif rp is not None and M >= 4 * n and stream is None:
+    elif rp is not None and M >= 4 * n and M * K >= 1 << 24 and stream is None:
         wn = quantize_workspace_bytes(n, M, K, format)
         if wn:
             workspace = torch.empty(wn, dtype=_UINT8, device=dev)
