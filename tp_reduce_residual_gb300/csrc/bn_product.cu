@@ -252,6 +252,11 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     const int unit = (int)blockIdx.x / S::kCtas, units = (int)gridDim.x / S::kCtas;
 
     griddep_launch_dependents();
+    if (warp == 1 && elect_one()) {
+        const CUtensorMap *maps5[] = {&maps.w, &maps.w_scales, &maps.a, &maps.a_small, &maps.a_scales};
+#pragma unroll
+        for (int i = 0; i < 5; ++i) asm volatile("prefetch.tensormap [%0];" ::"l"(maps5[i]) : "memory");
+    }
     if (threadIdx.x == 0) {
         abort_flag = 0;
         for (int i = 0; i < kStages; ++i) {
@@ -284,28 +289,28 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         start[e] = min(max(o, 0), p.M);
     }
     __syncthreads();
-    if (warp == 0) {
-        int carry = 0;
-        if (lane == 0) cum[0] = 0;
-        for (int e0 = 0; e0 < p.E; e0 += 32) {
-            const int e = e0 + lane;
-            int n = 0;
-            if (e < p.E) {
-                n = start[e + 1] - start[e];
-                if (n < 0) {  // a falling offset: an empty group
-                    atomicOr(p.err, BN_DEVERR_OFFSETS);
-                    n = 0;
-                }
-                n = (n + kTile - 1) / kTile;
-            }
-#pragma unroll
-            for (int o = 1; o < 32; o <<= 1) {
-                const int v = __shfl_up_sync(kAll, n, o);
-                if (lane >= o) n += v;
-            }
-            if (e < p.E) cum[e + 1] = carry + n;
-            carry += __shfl_sync(kAll, n, 31);
+    if (warp == 0) {  // a lane takes its share of consecutive groups
+        const int share = (p.E + 31) / 32, e0 = min(lane * share, p.E), e1 = min(e0 + share, p.E);
+        const auto tiles_of = [&](int e) { return (max(start[e + 1] - start[e], 0) + kTile - 1) / kTile; };
+        int n = 0;
+        bool falls = false;  // a falling offset: an empty group
+        for (int e = e0; e < e1; ++e) {
+            n += tiles_of(e);
+            falls |= start[e + 1] < start[e];
         }
+        if (falls) atomicOr(p.err, BN_DEVERR_OFFSETS);
+        int before = n;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int v = __shfl_up_sync(kAll, before, o);
+            if (lane >= o) before += v;
+        }
+        before -= n;
+        for (int e = e0; e < e1; ++e) {
+            cum[e] = before;
+            before += tiles_of(e);
+        }
+        if (lane == 31) cum[p.E] = before;
     }
     fence_before();
     __syncthreads();
