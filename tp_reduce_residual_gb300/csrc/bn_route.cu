@@ -234,12 +234,25 @@ __device__ __noinline__ int select64(const T *row, const RouteArgs &a, int lane,
     return take64<VPT>(key, lane, a.k);
 }
 
-// A chosen or candidate expert's key in 64 bits (not the softmax's sums).
+// The softmax's sum over the row in 64 bits; `top` is the largest logit.
+template <typename T, int VPT>
+__device__ __noinline__ double sum64(const T *row, const RouteArgs &a, int lane, float top)
+{
+    float x[VPT];
+    load_row<T, VPT>(row, a.E, lane, a.vec, -INFINITY, x);
+    double sum = 0;
+#pragma unroll 1
+    for (int j = 0; j < VPT; ++j) sum += x[j] > -INFINITY ? exp((double)x[j] - (double)top) : 0.0;
+    return warp_sum(sum);
+}
+
+// A chosen or candidate expert's key in 64 bits; `sum` as above, for the softmax.
 template <typename T, bool SUMS>
-__device__ __forceinline__ double key64(const T *row, const RouteArgs &a, int id)
+__device__ __forceinline__ double key64(const T *row, const RouteArgs &a, int id, float top, double sum)
 {
     const double x = (double)to_f32(row[id]);
-    return SUMS ? sigmoid(x) + (a.bias ? (double)__ldg(a.bias + id) : 0.0) : x;
+    if (!SUMS) return x;
+    return (a.sigmoid ? sigmoid(x) : exp(x - (double)top) / sum) + (a.bias ? (double)__ldg(a.bias + id) : 0.0);
 }
 
 // The groups that stay, by 64-bit ranks, from the row's 32-bit keys in `slot`: lane
@@ -247,7 +260,7 @@ __device__ __forceinline__ double key64(const T *row, const RouteArgs &a, int id
 // group by the best of their 64-bit keys.  False where more than four may count.
 template <typename T, int VPT, bool SUMS>
 __device__ __noinline__ bool groups64(const T *row, const RouteArgs &a, int lane, const float *slot, float error,
-                                      unsigned *kept)
+                                      float top, double sum, unsigned *kept)
 {
     const int size = a.E / a.groups;
     float v[5];
@@ -276,17 +289,18 @@ __device__ __noinline__ bool groups64(const T *row, const RouteArgs &a, int lane
     double r1 = -INFINITY, r2 = -INFINITY, gap, largest;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
-        if (e[q] >= 0) push2(key64<T, SUMS>(row, a, e[q]), r1, r2);
+        if (e[q] >= 0) push2(key64<T, SUMS>(row, a, e[q], top, sum), r1, r2);
     *kept = keep_groups(r1, r2, lane, a, gap, largest);
     return __all_sync(kAll, ok);
 }
 
 // The candidates, lane j < n the one of id `id`: lane j < k gets the j-th of them.
 template <typename T, bool SUMS>
-__device__ __noinline__ int order64(const T *row, const RouteArgs &a, int lane, int n, int id, int *list)
+__device__ __noinline__ int order64(const T *row, const RouteArgs &a, int lane, int n, int id, float top, double sum,
+                                    int *list)
 {
     double key = -INFINITY;
-    if (lane < n) key = key64<T, SUMS>(row, a, id);
+    if (lane < n) key = key64<T, SUMS>(row, a, id, top, sum);
     int ahead = 0;
     for (int j = 0; j < n; ++j) {
         const double o = __shfl_sync(kAll, key, j);
@@ -409,6 +423,11 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
     // off, so the two errors have one sign).
     const auto bound = [&](float v) { return 2.0f * serr + (VPT + 1) * 0x1p-23f * v + 0x1p-120f; };
     bool sure = true;  // of the groups that stay
+    double all = 0.0;  // the softmax's sum in 64 bits, once it is wanted
+    const auto sum_once = [&]() {
+        if (SUMS && !a.sigmoid && all == 0.0) all = sum64<T, VPT>(row, a, lane, top);
+        return all;
+    };
     float *slot = reinterpret_cast<float *>(slots[warp]);
     const int size = a.E / a.groups, lanes = size / VPT;
     const bool whole = size % VPT == 0 && (lanes & (lanes - 1)) == 0;  // a group is so many whole lanes
@@ -426,7 +445,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
         unsigned kept = keep_groups(r1, r2, lane, a, gap, largest);
         if constexpr (!kExact)
             if (uncertain(gap, largest))
-                sure = !(SUMS && !a.sigmoid) && groups64<T, VPT, SUMS>(row, a, lane, slot, bound(largest), &kept);
+                sure = groups64<T, VPT, SUMS>(row, a, lane, slot, bound(largest), top, sum_once(), &kept);
 #pragma unroll
         for (int j = 0; j < VPT; ++j) {
             const int e = lane * VPT + j;
@@ -453,7 +472,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
                 for (int j = 0; j < VPT; ++j)
                     if (key[j] > -INFINITY) slot[lane * VPT + position_of<VPT>(key[j])] = without_position<VPT>(key[j]);
                 __syncwarp();
-                sure = !(SUMS && !a.sigmoid) && groups64<T, VPT, SUMS>(row, a, lane, slot, bound(largest), &kept);
+                sure = groups64<T, VPT, SUMS>(row, a, lane, slot, bound(largest), top, sum_once(), &kept);
                 __syncwarp();
             }
         const int g = lane / lanes;
@@ -500,10 +519,10 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
                 m = warp_max(head);
             }
             __syncwarp();
-            if (!sure || n == 32 || (SUMS && !a.sigmoid))
+            if (!sure || n == 32)
                 id = select64<T, VPT, SUMS>(row, a, lane, slots[warp]);
             else
-                id = order64<T, SUMS>(row, a, lane, n, lane < n ? list[lane] : -1, list);
+                id = order64<T, SUMS>(row, a, lane, n, lane < n ? list[lane] : -1, top, sum_once(), list);
         }
     }
     if (lane >= min(n, a.k)) id = -1;
