@@ -449,6 +449,60 @@ def test_product(fmt, counts, tail, N, K):
 
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("counts,tail,N,K", [
+    # groups that average over 128 rows take pairs of CTAs: 256 features by 256 rows, in halves
+    ([129], 0, 136, 64), ([256, 257, 255], 0, 256, 288), ([1, 600, 0, 31, 513], 0, 392, 1312), ([0, 1000], 40, 904, 160),
+    ([383, 385, 128], 0, 2056, 96), ([2500, 3], 0, 264, 512)])
+def test_product_of_large_groups(fmt, counts, tail, N, K):
+    check_product(counts, tail, N, K, fmt, seed=3)
+
+
+@pytest.mark.parametrize("rows", [4, 300])
+def test_product_on_another_stream(rows):
+    """Operands made on the current stream, the product on a side stream that waits for it."""
+    a = experts.quantize_fp4(torch.ones(rows, 256, dtype=torch.bfloat16, device="cuda"), "mxfp4")
+    b = experts.quantize_fp4(torch.ones(264, 256, dtype=torch.bfloat16, device="cuda"), "mxfp4")
+    out = torch.zeros(rows, 264, dtype=torch.bfloat16, device="cuda")
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    experts.expert_product(a, b, out=out, stream=side)
+    side.synchronize()
+    assert (out == 256).all()
+
+
+def test_product_no_rows_and_binding_refusals():
+    b = experts.quantize_fp4(torch.ones(2, 16, 64, dtype=torch.bfloat16, device="cuda"), "nvfp4")
+    offsets = torch.zeros(3, dtype=torch.int32, device="cuda")
+    none = experts.quantize_fp4(torch.ones(0, 64, dtype=torch.bfloat16, device="cuda"), "nvfp4", offsets=offsets)
+    assert experts.expert_product(none, b).shape == (0, 16)
+    a = experts.quantize_fp4(torch.ones(4, 64, dtype=torch.bfloat16, device="cuda"), "nvfp4", offsets=offsets)
+    assert (experts.expert_product(a, b) == 0).all()  # rows of no group
+    one = experts.quantize_fp4(torch.ones(4, 64, dtype=torch.bfloat16, device="cuda"), "nvfp4")
+    with pytest.raises(ValueError, match="1 groups, w has 2 experts"):
+        experts.expert_product(one, b)
+    with pytest.raises(ValueError, match="no offsets"):
+        experts.expert_product(a, a)
+    mx = experts.quantize_fp4(torch.ones(4, 64, dtype=torch.bfloat16, device="cuda"), "mxfp4", offsets=offsets)
+    with pytest.raises(ValueError, match="mxfp4 values"):
+        experts.expert_product(mx, b)
+    with pytest.raises(ValueError, match="shape"):
+        experts.expert_product(a, b, out=torch.zeros(4, 8, dtype=torch.bfloat16, device="cuda"))
+    x = torch.randn(4, 64, device="cuda")
+    with pytest.raises(TypeError, match="bfloat16"):
+        experts.quantize_fp4(x, "nvfp4")
+    with pytest.raises(ValueError, match="contiguous rows"):
+        experts.route(x.T, 2)
+    with pytest.raises(ValueError, match="do not overlap"):
+        experts.route(x.as_strided((4, 64), (32, 1)), 2)
+    with pytest.raises(TypeError, match="bias must be"):
+        experts.route(x, 2, bias=torch.zeros(64, device="cuda", dtype=torch.bfloat16))
+    with pytest.raises(bn.BeamNormError, match="k=17"):
+        experts.route(x, 17)
+    with pytest.raises(ValueError, match="multiple of 32"):
+        experts.quantize_fp4(torch.ones(4, 40, dtype=torch.bfloat16, device="cuda"), "nvfp4")
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 def test_product_many_experts_and_tiles(fmt):
     g = gen(4)
     counts = torch.randint(0, 40, (150,), generator=g).tolist()
@@ -522,3 +576,14 @@ def test_layer_in_a_graph_matches_eager():
         eager_res = res0.clone()
         eager = layer(eager_res)
         assert torch.equal(got, eager) and torch.equal(got_res, eager_res)
+
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+def test_example_layer(fmt):
+    """The example's layer against 32-bit activations: rounding a value to 4 bits moves it by at most a
+    quarter (half the step from 1 to 1.5), about a tenth in the mean square; two roundings in a row and
+    the residual, which is as large as the normed sum and exact, leave under a quarter."""
+    from examples import moe_layer
+    assert moe_layer.main(["--format", fmt, "--tokens", "37", "--hidden", "512", "--width", "256"]) < 0.25
+    assert moe_layer.main(["--format", fmt, "--tokens", "3", "--hidden", "256", "--width", "128", "--shards", "1", "--experts", "6",
+                           "--topk", "2"]) < 0.25
