@@ -67,7 +67,7 @@ __device__ __forceinline__ bool elect_one()
 
 struct Maps {
     CUtensorMap a, a_small, w;   // codes: boxes of 128 (a_small: 32) rows by 128 bytes
-    CUtensorMap a_scales, w_scales;  // scale tiles: boxes of a stage's by 512 bytes
+    CUtensorMap a_scales, w_scales;  // scale tiles: boxes of a stage's chunks of 512 bytes of so many row tiles
 };
 
 struct Tile {
@@ -133,6 +133,20 @@ __device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int
         asm volatile(
             "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
             "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
+}
+
+// The same of three dimensions, from (0, y, z).
+template <bool PAIR>
+__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int y, int z, uint32_t bar)
+{
+    if constexpr (PAIR)
+        asm volatile(
+            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar) : "memory");
+    else
+        asm volatile(
+            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
+            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar) : "memory");
 }
 
 // Shared-memory operand descriptors.  Codes: rows of 128 bytes, 128-byte
@@ -341,12 +355,10 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
             const int nb = PAIR ? columns / 2 : columns, b0 = t.row0 + (PAIR ? (int)rank * nb : 0);
             const int boxes = nb > kHalf / 2 ? 0 : (nb + kBoxRows - 1) / kBoxRows;  // 0: one of kHalf rows
             const uint32_t codes = (uint32_t)(kHalf + (boxes ? boxes * kBoxRows : kHalf)) * kTileBytes;
-            const int atoms = (t.rows + 127) / 128;
             constexpr uint32_t kScaleBytes = kChunksPerStage * 512;
-            const uint32_t bytes = S::kCtas * (codes + (1 + atoms) * kScaleBytes);
+            const uint32_t bytes = S::kCtas * (codes + (1 + S::kRowAtoms) * kScaleBytes);
             // past the last features any scales will do
-            const int sw = (t.e * wtiles + min(f0 / kHalf, wtiles - 1)) * p.chunks;
-            const int sa = t.stile * p.chunks;
+            const int sw = t.e * wtiles + min(f0 / kHalf, wtiles - 1);
             for (int k = 0; k < nk; ++k, ++it) {
                 const uint32_t s = it % kStages;
                 ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(empty + 8 * s, ((it / kStages) & 1u) ^ 1u, ctl));
@@ -361,11 +373,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         tma_2d<PAIR>(at + S::kOffB, &maps.a, x, b0, bar);
                     for (int b = 0; b < boxes; ++b)
                         tma_2d<PAIR>(at + S::kOffB + b * kBoxRows * kTileBytes, &maps.a_small, x, b0 + b * kBoxRows, bar);
-                    // a row's last stage may fetch the next row tile's scales too: they are not used
-                    tma_2d<PAIR>(at + S::kOffSA, &maps.w_scales, 0, sw + c, bar);
-                    tma_2d<PAIR>(at + S::kOffSB, &maps.a_scales, 0, sa + c, bar);
-                    if (PAIR && atoms > 1)
-                        tma_2d<PAIR>(at + S::kOffSB + 2048, &maps.a_scales, 0, sa + p.chunks + c, bar);
+                    tma_3d<PAIR>(at + S::kOffSA, &maps.w_scales, c, sw, bar);
+                    // scale tiles past the group's rows are fetched too and not used
+                    tma_3d<PAIR>(at + S::kOffSB, &maps.a_scales, c, t.stile, bar);
                 }
             }
         }
@@ -407,7 +417,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     auto scales = [&](int c) {
                         copy_scales<PAIR>(sa + 4 * c, dsa + 32 * c);
                         copy_scales<PAIR>(sb + 4 * S::kRowAtoms * c, dsb + 32 * c);
-                        if (two) copy_scales<PAIR>(sb + 4 * S::kRowAtoms * c + 4, dsb + 128 + 32 * c);
+                        if (two) copy_scales<PAIR>(sb + 4 * S::kRowAtoms * c + 4, dsb + 32 * kChunksPerStage + 32 * c);
                     };
                     auto step = [&](int j) {
                         const uint32_t c = MX ? j >> 1 : j;
@@ -515,34 +525,39 @@ EncodeFn g_encode;
 cudaError_t g_encode_status = cudaErrorUnknown;
 std::once_flag g_encode_once;
 
-// Rows of `width` elements, boxes of `box` rows by `box_width`.
-cudaError_t make_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *data, long long rows,
-                     long long width, int box, int box_width, CUtensorMapSwizzle swizzle)
+// `dims` elements of `size` bytes, densely, in boxes.
+template <int RANK>
+cudaError_t make_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *data, const cuuint64_t (&dims)[RANK],
+                     const cuuint32_t (&box)[RANK], CUtensorMapSwizzle swizzle)
 {
-    const cuuint64_t dims[2] = {(cuuint64_t)width, (cuuint64_t)rows};
-    const cuuint64_t strides[1] = {(cuuint64_t)(width * size)};
-    const cuuint32_t boxes[2] = {(cuuint32_t)box_width, (cuuint32_t)box}, ones[2] = {1, 1};
-    const CUresult r = g_encode(map, type, 2, const_cast<void *>(data), dims, strides, boxes, ones,
+    cuuint64_t strides[RANK - 1], bytes = (cuuint64_t)size;
+    cuuint32_t ones[RANK];
+    for (int i = 0; i < RANK; ++i) {
+        bytes *= dims[i];
+        if (i < RANK - 1) strides[i] = bytes;
+        ones[i] = 1;
+    }
+    const CUresult r = g_encode(map, type, RANK, const_cast<void *>(data), dims, strides, box, ones,
                                 CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                                 CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
     return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
-cudaError_t make_maps(Maps *m, const ProductArgs &p, const uint8_t *a, const uint8_t *w, int fmt)
+cudaError_t make_maps(Maps *m, const ProductArgs &p, const uint8_t *a, const uint8_t *w, int fmt, int row_atoms)
 {
     const auto codes = [&](CUtensorMap *map, const uint8_t *data, long long rows, int box) {
-        return make_map(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, data, rows, p.K / 2, box, kTileBytes,
-                        CU_TENSOR_MAP_SWIZZLE_128B);
+        return make_map<2>(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, data, {(cuuint64_t)p.K / 2, (cuuint64_t)rows},
+                           {(cuuint32_t)kTileBytes, (cuuint32_t)box}, CU_TENSOR_MAP_SWIZZLE_128B);
     };
-    const auto scales = [&](CUtensorMap *map, const uint8_t *data, long long tiles) {
-        return make_map(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 8, data, tiles * p.chunks, 64, fmt ? 2 : 4, 64,
-                        CU_TENSOR_MAP_SWIZZLE_NONE);
+    const auto scales = [&](CUtensorMap *map, const uint8_t *data, long long tiles, int atoms) {
+        return make_map<3>(map, CU_TENSOR_MAP_DATA_TYPE_INT64, 8, data, {64, (cuuint64_t)p.chunks, (cuuint64_t)tiles},
+                           {64, fmt ? 2u : 4u, (cuuint32_t)atoms}, CU_TENSOR_MAP_SWIZZLE_NONE);
     };
     cudaError_t e = codes(&m->a, a, p.M, kHalf);
     if (e == cudaSuccess) e = codes(&m->a_small, a, p.M, kBoxRows);
     if (e == cudaSuccess) e = codes(&m->w, w, (long long)p.E * p.N, kHalf);
-    if (e == cudaSuccess) e = scales(&m->a_scales, p.a_scales, p.a_tiles);
-    if (e == cudaSuccess) e = scales(&m->w_scales, p.w_scales, (long long)p.E * ((p.N + 127) / 128));
+    if (e == cudaSuccess) e = scales(&m->a_scales, p.a_scales, p.a_tiles, row_atoms);
+    if (e == cudaSuccess) e = scales(&m->w_scales, p.w_scales, (long long)p.E * ((p.N + 127) / 128), 1);
     return e;
 }
 
@@ -576,11 +591,11 @@ cudaError_t launch_product(const ProductArgs &p, const uint8_t *a, const uint8_t
         g_encode = reinterpret_cast<EncodeFn>(fn);
     });
     if (g_encode_status != cudaSuccess) return g_encode_status;
-    Maps maps;
-    const cudaError_t e = make_maps(&maps, p, a, w, fmt);
-    if (e != cudaSuccess) return e;
     // Pairs where the average group fills more than one CTA's tile.
     const bool pair = p.M / p.E > 128 && p.N > 128;
+    Maps maps;
+    const cudaError_t e = make_maps(&maps, p, a, w, fmt, pair ? Shape<true>::kRowAtoms : Shape<false>::kRowAtoms);
+    if (e != cudaSuccess) return e;
     return pair ? launch_shape<true>(p, maps, fmt, sms, pdl, st) : launch_shape<false>(p, maps, fmt, sms, pdl, st);
 }
 
