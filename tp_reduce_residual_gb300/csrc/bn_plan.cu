@@ -11,7 +11,8 @@
 // memory; a scan over the warps, the CTAs (their totals read through
 // distributed shared memory) and the experts turns counts into places; a second
 // pass over the run hands them out.  Within 32 slots __match_any_sync finds
-// equal ids.  Latency bounds it: the bytes are a few hundred KB.
+// equal ids.  Latency bounds it (the bytes are a few hundred KB), so loads are
+// issued several at a time: ids eight steps ahead, the other CTAs' totals together.
 #include "../../include/beamnorm.h"
 #include "bn_device.cuh"
 #include "bn_experts.h"
@@ -23,11 +24,9 @@ namespace {
 
 constexpr unsigned kAll = 0xffffffffu;
 
-__device__ __forceinline__ int bucket_of(const PlanArgs &a, int slot)
-{
-    const int id = __ldg(a.ids + slot);
-    return (unsigned)id < (unsigned)a.E ? id : a.E;
-}
+constexpr int kThreads = 512;
+constexpr int kMostCtas = 16;
+constexpr int kAhead = 8;  // steps of 32 slots whose ids are loaded together
 
 __device__ __forceinline__ unsigned ld_cluster(uint32_t addr)
 {
@@ -36,7 +35,7 @@ __device__ __forceinline__ unsigned ld_cluster(uint32_t addr)
     return v;
 }
 
-__global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int per_warp)
+__global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a, int per_warp)
 {
     extern __shared__ unsigned smem[];
     const int nb = a.E + 1;                   // experts, and the slots without one
@@ -57,15 +56,29 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int per_warp)
     const int hi = (int)min(first + per_warp, (long long)a.slots);
     unsigned *mine = count + warp * nb;
     bool bad = false;
-    for (int i = lo + lane; i < hi; i += 32) {  // counting needs no order
-        const int id = __ldg(a.ids + i);
-        bad |= id < -1 || id >= a.E;
-        atomicAdd(mine + ((unsigned)id < (unsigned)a.E ? id : a.E), 1u);
+    int id[kAhead];
+    const auto load = [&](int i0) {
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + 32 * u + lane;
+            id[u] = i < hi ? __ldg(a.ids + i) : -1;
+        }
+    };
+    const auto bucket_of = [&](int v) { return (unsigned)v < (unsigned)a.E ? v : a.E; };
+    for (int i0 = lo; i0 < hi; i0 += 32 * kAhead) {  // counting needs no order
+        load(i0);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u)
+            if (i0 + 32 * u + lane < hi) {
+                bad |= id[u] < -1 || id[u] >= a.E;
+                atomicAdd(mine + bucket_of(id[u]), 1u);
+            }
     }
     if (bad) atomicOr(a.err, BN_DEVERR_EXPERT_RANGE);
     __syncthreads();
     for (int b = threadIdx.x; b < nb; b += blockDim.x) {
         unsigned run = 0;
+#pragma unroll 8
         for (int w = 0; w < warps; ++w) {
             const unsigned c = count[w * nb + b];
             count[w * nb + b] = run;
@@ -81,10 +94,13 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int per_warp)
         unsigned all = 0, before = 0;
         if (b < nb) {
             const uint32_t at = smem_addr(total + b);
-            for (uint32_t c = 0; c < ctas; ++c) {
-                const unsigned v = c == cta ? total[b] : ld_cluster(mapa(at, c));
-                before += c < cta ? v : 0u;
-                all += v;
+            unsigned v[kMostCtas];
+#pragma unroll
+            for (uint32_t c = 0; c < kMostCtas; ++c) v[c] = c < ctas ? ld_cluster(mapa(at, c)) : 0u;
+#pragma unroll
+            for (uint32_t c = 0; c < kMostCtas; ++c) {
+                before += c < cta ? v[c] : 0u;
+                all += v[c];
             }
         }
         unsigned run = all;  // inclusive scan over the block
@@ -117,18 +133,23 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int per_warp)
     }
     // hand out the places, in slot order
     const unsigned below = (1u << lane) - 1u;
-    for (int i0 = lo; i0 < hi; i0 += 32) {
-        const int i = i0 + lane;
-        const int b = i < hi ? bucket_of(a, i) : -1;
-        const unsigned same = __match_any_sync(kAll, b);
-        unsigned place = 0;
-        if (b >= 0) place = base[b] + mine[b] + __popc(same & below);
-        __syncwarp();
-        if (b >= 0 && (same & below) == 0) mine[b] += __popc(same);
-        __syncwarp();
-        if (b >= 0) {
-            a.rows[place] = (int)((unsigned)i / (unsigned)a.k);
-            for (int r = 0; r < a.R; ++r) a.perm[(long long)r * a.slots + i] = (int)place;
+    for (int i0 = lo; i0 < hi; i0 += 32 * kAhead) {
+        load(i0);
+#pragma unroll
+        for (int u = 0; u < kAhead; ++u) {
+            const int i = i0 + 32 * u + lane;
+            if (i - lane >= hi) break;
+            const int b = i < hi ? bucket_of(id[u]) : -1;
+            const unsigned same = __match_any_sync(kAll, b);
+            unsigned place = 0;
+            if (b >= 0) place = base[b] + mine[b] + __popc(same & below);
+            __syncwarp();
+            if (b >= 0 && (same & below) == 0) mine[b] += __popc(same);
+            __syncwarp();
+            if (b >= 0) {
+                a.rows[place] = (int)((unsigned)i / (unsigned)a.k);
+                for (int r = 0; r < a.R; ++r) a.perm[(long long)r * a.slots + i] = (int)place;
+            }
         }
     }
     cluster_sync_all();  // no CTA leaves while its totals may be read
@@ -138,17 +159,18 @@ __global__ void __launch_bounds__(1024) plan_kernel(PlanArgs a, int per_warp)
 
 cudaError_t launch_plan(const PlanArgs &a, bool pdl, cudaStream_t st)
 {
-    // 512 slots a CTA, up to 16 CTAs of 512 threads; then longer runs per warp
-    const int threads = 512, warps = threads / 32;
+    // A slot a thread, up to 16 CTAs; then longer runs per warp.  CTAs of 1024 threads
+    // take as long at 131072 slots (13.4 us against 13.6) and longer at 1528 (4.5, 3.5).
+    constexpr int warps = kThreads / 32;
     int ctas = 1;
-    while (ctas < 16 && (long long)ctas * 512 < a.slots) ctas *= 2;
+    while (ctas < kMostCtas && (long long)ctas * kThreads < a.slots) ctas *= 2;
     const long long share = ((long long)a.slots + ctas * warps - 1) / (ctas * warps);
     const int per_warp = (int)((share + 31) / 32 * 32);
-    const auto smem = [&](int E) { return sizeof(unsigned) * ((size_t)warps + 2) * (size_t)(E + 1); };
+    const auto smem = [](int E) { return sizeof(unsigned) * (size_t)(warps + 2) * (size_t)(E + 1); };
     static KernelSetup setup;
     const cudaError_t e = setup(plan_kernel, (int)smem(kMaxExperts), true);
     if (e != cudaSuccess) return e;
-    return launch_kernel(plan_kernel, dim3((unsigned)ctas), dim3(threads), smem(a.E), pdl, ctas, st, a,
+    return launch_kernel(plan_kernel, dim3((unsigned)ctas), dim3(kThreads), smem(a.E), pdl, ctas, st, a,
                          per_warp);
 }
 
