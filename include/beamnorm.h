@@ -303,7 +303,8 @@ BN_API bn_status bn_finalize_only(const uint16_t *expert_out, const int32_t *per
  * only their own element's alignment, int32 and FP32 buffers 4 bytes, the
  * others 16.  With T == 0 or M == 0 nothing is enqueued and pointers are not
  * examined (bn_expert_plan still writes offsets).  E <= 1024, k <= 16, R <= 16;
- * T * k < 2^31. */
+ * T * k and M at most 2^31 - 1024.  wait_limit_polls does not apply to the
+ * product, whose waits keep the default limit (BN_DEVERR_TIMEOUT). */
 
 typedef enum { BN_BF16 = 0, BN_FP16 = 1, BN_FP32 = 2 } bn_dtype;
 typedef enum { BN_SCORE_SOFTMAX = 0, BN_SCORE_SIGMOID = 1 } bn_score;

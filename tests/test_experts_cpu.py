@@ -69,7 +69,7 @@ def test_route_backward_refuses(L, kw, status, needle):
 
 @pytest.mark.parametrize("kw,status,needle", [
     (dict(T=-1), 1, "T=-1"), (dict(k=17), 1, "k=17"), (dict(E=0), 1, "E=0"), (dict(E=1025), 2, "E=1025"), (dict(R=17), 1, "R=17"),
-    (dict(T=2 ** 28), 2, "T*k"), (dict(ids=None), 1, "ids is NULL"), (dict(offsets=None), 1, "offsets is NULL"),
+    (dict(T=2 ** 28), 2, "T*k"), (dict(T=2 ** 31 - 1000, k=1), 2, "T*k"), (dict(ids=None), 1, "ids is NULL"), (dict(offsets=None), 1, "offsets is NULL"),
     (dict(rows=at(0)), 1, "rows overlaps ids"), (dict(perm=at(2)), 1, "perm overlaps offsets"), (dict(perm=at(1) + 2), 1, "perm is not"),
 ])
 def test_plan_refuses(L, kw, status, needle):
@@ -108,7 +108,7 @@ def test_dequantize_refuses(L, kw, status, needle):
     (dict(offsets=None), 1, "offsets is NULL"), (dict(offsets=at(4) + 2), 1, "offsets is not"), (dict(alpha=math.inf), 1, "alpha"),
     (dict(a=at(0) + 8), 1, "a is not 16-byte"), (dict(w=None), 1, "w is NULL"), (dict(out=at(2)), 1, "out overlaps w"),
     (dict(out=at(0)), 1, "out overlaps a"), (dict(E=1024, N=2 ** 21), 2, "E*N"), (dict(format=9), 1, "format"),
-    (dict(E=1024, N=2 ** 20, K=2 ** 20), 2, "scale tiles"),
+    (dict(E=1024, N=2 ** 20, K=2 ** 20), 2, "scale tiles"), (dict(M=2 ** 31 - 1), 2, "M=2147483647"),
 ])
 def test_product_refuses(L, kw, status, needle):
     a = dict(a=at(0), a_scales=at(1), M=8, w=at(2), w_scales=at(3), E=4, N=64, K=64, offsets=at(4), format=0, alpha=1.0, out=at(5),

@@ -540,6 +540,40 @@ def test_product_bad_offsets_are_reported():
     assert bn.check_device_error(raise_on_error=False) == bn.DEVERR_OFFSETS
 
 
+def test_offsets_past_32_bits():
+    """Logits, codes, values and products whose last elements lie past 2^31 elements or bytes."""
+    g = gen(30)
+    T, ld, E = 520, 1 << 22, 64
+    x = torch.randn(T, E, generator=g)
+    far = torch.empty((T - 1) * ld + E, dtype=torch.bfloat16, device="cuda").as_strided((T, E), (ld, 1))
+    far.copy_(x)
+    ids, w = experts.route(far, 4)
+    near = experts.route(x.bfloat16().cuda(), 4)
+    assert torch.equal(ids, near[0]) and torch.equal(w, near[1])
+    dw = torch.randn(1, T, 4, generator=g).cuda()
+    assert torch.equal(experts.route_backward(far, ids, dw), experts.route_backward(x.bfloat16().cuda(), ids, dw))
+    del far
+    n, M, K = 9, 140000, 32768  # 2.3 GB of codes, 9.2 GB of values
+    x = torch.randn(n, K, generator=g).bfloat16().cuda()
+    rows = torch.randint(0, n, (M,), generator=g).to(torch.int32).cuda()
+    offsets = torch.tensor([0, 70001, M], dtype=torch.int32, device="cuda")
+    small = experts.dequantize_fp4(experts.quantize_fp4(x, "mxfp4"))
+    for work in (None, torch.empty(16, dtype=torch.uint8, device="cuda")):
+        q = experts.quantize_fp4(x, "mxfp4", rows=rows, offsets=offsets, workspace=work)
+        v = experts.dequantize_fp4(q)
+        for lo in (0, 65536, 70000, 131072, M - 100):
+            assert torch.equal(v[lo:lo + 100], small[rows[lo:lo + 100].long()])
+        del q, v
+    M, N, K = 300000, 8192, 64  # 2.5 G products
+    x = torch.randn(n, K, generator=g).bfloat16().cuda()
+    rows = torch.randint(0, n, (M,), generator=g).to(torch.int32).cuda()
+    b = experts.quantize_fp4(torch.randn(N, K, generator=g).bfloat16().cuda(), "nvfp4")
+    want = experts.expert_product(experts.quantize_fp4(x, "nvfp4"), b)
+    got = experts.expert_product(experts.quantize_fp4(x, "nvfp4", rows=rows), b)
+    for lo in (0, 131072, 262100, M - 100):
+        assert torch.equal(got[lo:lo + 100], want[rows[lo:lo + 100].long()])
+
+
 def test_layer_in_a_graph_matches_eager():
     """Route, plan, quantise, product and finalize, captured once and replayed on new inputs."""
     g = gen(20)

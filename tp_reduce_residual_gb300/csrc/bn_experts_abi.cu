@@ -14,6 +14,9 @@
 namespace bn {
 namespace {
 
+// Rows and slots are counted in int32, rounded up to tiles and blocks.
+constexpr long long kMaxRows = (1LL << 31) - 1024;
+
 size_t dtype_size(int dtype) { return dtype == BN_FP32 ? 4 : 2; }
 
 bn_status check_dtype(int dtype, bool fp32)
@@ -33,7 +36,7 @@ bn_status check_route(int dtype, long long ld, int T, int E, int k, int R, int s
     BN_REQUIRE(ld >= E, "ld=%lld below E=%d", ld, E);
     BN_REQUIRE(score == BN_SCORE_SOFTMAX || score == BN_SCORE_SIGMOID, "score %d is unknown", score);
     if (E > kMaxExperts) return fail(BN_ERR_UNSUPPORTED, "E=%d above the served maximum %d", E, kMaxExperts);
-    if ((long long)T * k >= (1LL << 31))
+    if ((long long)T * k > kMaxRows)
         return fail(BN_ERR_UNSUPPORTED, "T*k=%lld does not fit int32 slot indices", (long long)T * k);
     return BN_OK;
 }
@@ -86,6 +89,7 @@ bn_status check_fp4(int fmt, int M, int K, int groups, const int32_t *offsets)
     BN_REQUIRE(aligned(offsets, 4), "offsets is not 4-byte aligned");
     if (offsets && groups > kMaxExperts)
         return fail(BN_ERR_UNSUPPORTED, "groups=%d above the served maximum %d", groups, kMaxExperts);
+    if (M > kMaxRows) return fail(BN_ERR_UNSUPPORTED, "M=%d above the served maximum %lld", M, kMaxRows);
     if (K > (1 << 20)) return fail(BN_ERR_UNSUPPORTED, "K=%d above the served maximum %d", K, 1 << 20);
     return BN_OK;
 }
@@ -195,7 +199,7 @@ bn_status bn_expert_plan(const int32_t *ids, int T, int k, int E, int R, int32_t
     BN_REQUIRE(k >= 1 && k <= kMaxK, "k=%d outside [1, %d]", k, kMaxK);
     BN_REQUIRE(R >= 1 && R <= kMaxR, "R=%d outside [1, %d]", R, kMaxR);
     if (E > kMaxExperts) return fail(BN_ERR_UNSUPPORTED, "E=%d above the served maximum %d", E, kMaxExperts);
-    if ((long long)T * k >= (1LL << 31))
+    if ((long long)T * k > kMaxRows)
         return fail(BN_ERR_UNSUPPORTED, "T*k=%lld does not fit int32 slot indices", (long long)T * k);
     BN_TRY(check_ptr4(offsets, "offsets"));
     if (T > 0) {

@@ -51,21 +51,22 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a, int per_warp
     griddep_wait();
     __syncthreads();
 
-    const long long first = ((long long)cta * warps + warp) * per_warp;
-    const int lo = (int)min(first, (long long)a.slots);
-    const int hi = (int)min(first + per_warp, (long long)a.slots);
+    // unsigned: a step past the last of almost 2^31 slots stays a number past it
+    const unsigned long long first = ((unsigned long long)cta * warps + warp) * (unsigned)per_warp;
+    const unsigned lo = (unsigned)min(first, (unsigned long long)a.slots);
+    const unsigned hi = (unsigned)min(first + (unsigned)per_warp, (unsigned long long)a.slots);
     unsigned *mine = count + warp * nb;
     bool bad = false;
     int id[kAhead];
-    const auto load = [&](int i0) {
+    const auto load = [&](unsigned i0) {
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int i = i0 + 32 * u + lane;
+            const unsigned i = i0 + 32 * u + lane;
             id[u] = i < hi ? __ldg(a.ids + i) : -1;
         }
     };
     const auto bucket_of = [&](int v) { return (unsigned)v < (unsigned)a.E ? v : a.E; };
-    for (int i0 = lo; i0 < hi; i0 += 32 * kAhead) {  // counting needs no order
+    for (unsigned i0 = lo; i0 < hi; i0 += 32 * kAhead) {  // counting needs no order
         load(i0);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u)
@@ -133,11 +134,11 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a, int per_warp
     }
     // hand out the places, in slot order
     const unsigned below = (1u << lane) - 1u;
-    for (int i0 = lo; i0 < hi; i0 += 32 * kAhead) {
+    for (unsigned i0 = lo; i0 < hi; i0 += 32 * kAhead) {
         load(i0);
 #pragma unroll
         for (int u = 0; u < kAhead; ++u) {
-            const int i = i0 + 32 * u + lane;
+            const unsigned i = i0 + 32 * u + lane;
             if (i - lane >= hi) break;
             const int b = i < hi ? bucket_of(id[u]) : -1;
             const unsigned same = __match_any_sync(kAll, b);
@@ -147,7 +148,7 @@ __global__ void __launch_bounds__(kThreads) plan_kernel(PlanArgs a, int per_warp
             if (b >= 0 && (same & below) == 0) mine[b] += __popc(same);
             __syncwarp();
             if (b >= 0) {
-                a.rows[place] = (int)((unsigned)i / (unsigned)a.k);
+                a.rows[place] = (int)(i / (unsigned)a.k);
                 for (int r = 0; r < a.R; ++r) a.perm[(long long)r * a.slots + i] = (int)place;
             }
         }
