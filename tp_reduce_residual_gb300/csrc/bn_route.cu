@@ -23,7 +23,11 @@
 // keys once (an odd-even merge sorting network; the position in the lane rides in
 // the keys' lowest bits, so that a comparison is one instruction), then k rounds
 // take the largest of the 32 heads (redux.sync) and advance one lane.  What bounds
-// it is instruction issue: about 500 instructions a token at 256 experts.
+// it is instruction issue: 1160 instructions a token at 256 experts in 8 groups with
+// a bias and k = 8 (ncu), of which the rounds are a third.  16384 such tokens take
+// 25.0 us (IPC 3.1; the bytes alone would take 1.4), one token 3.1.  Searching the
+// lane's 8 keys again after each round, with indexes apart, took 1590 instructions
+// and 47 us, 20 of them a tail of rows that were selected whole in 64 bits.
 #include <cfloat>
 #include <cmath>
 
@@ -559,8 +563,8 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
 //   sigmoid, renormalised:  c_j is first replaced by (c_j - sum_i (s_i / S) c_i) / S, S = sum of s
 // 1 - s is computed as sigmoid(-x), which keeps its digits near s = 1.  One
 // warp per token: the chosen slots sit on lanes, are scattered into the warp's
-// row in shared memory, and the row is written once with 16-byte stores, so the
-// kernel is bounded by that store stream.
+// row in shared memory, and the row is written once with 16-byte stores.  16384
+// tokens of 128 FP32 logits, dense: 6.1 us for 18 MB; 4096 of 256 BF16, sparse: 3.3.
 template <typename T, int VPT, bool DENSE>
 __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const __grid_constant__ RouteBackwardArgs a)
 {
