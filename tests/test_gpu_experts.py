@@ -450,9 +450,12 @@ def test_product(fmt, counts, tail, N, K):
 
 @pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
 @pytest.mark.parametrize("counts,tail,N,K", [
-    # groups that average over 128 rows take pairs of CTAs: 256 features by 256 rows, in halves
+    # where tiles of one CTA take more than one round over the device, pairs of CTAs run: 256 features by
+    # 256 rows, in halves
     ([129], 0, 136, 64), ([256, 257, 255], 0, 256, 288), ([1, 600, 0, 31, 513], 0, 392, 1312), ([0, 1000], 40, 904, 160),
-    ([383, 385, 128], 0, 2056, 96), ([2500, 3], 0, 264, 512)])
+    ([383, 385, 128], 0, 2056, 96), ([2500, 3], 0, 264, 512), ([700], 0, 4360, 160), ([0, 1300, 31, 257], 50, 2312, 96),
+    ([33] * 40 + [900, 0, 513], 0, 1544, 288), ([2100, 1], 7, 1288, 1312),
+    ([300, 0, 511, 257, 1, 256, 129, 385], 30, 2056, 352)])
 def test_product_of_large_groups(fmt, counts, tail, N, K):
     check_product(counts, tail, N, K, fmt, seed=3)
 

@@ -585,6 +585,23 @@ cudaError_t launch_shape(const ProductArgs &p, const Maps &maps, int fmt, int sm
     return launch_kernel(k, dim3((unsigned)grid), dim3(S::kThreads), smem(p.E), pdl, S::kCtas, st, maps, p);
 }
 
+// Which shape: rounds of tiles over the device, a pair's costing about 1.25 of a
+// CTA's.  The groups' sizes are on the device; as many groups as rows allow are taken
+// to be in use and to leave half a tile each.  Measured, one CTA / pairs (us), groups
+// averaging r rows: 32 experts of 4096 x 4096, r = 48 52 / 52, 128 62 / 56, 256 95 /
+// 72, 512 169 / 114; 32 of 1024 x 2048, r = 48 9.3 / 10.1, 160 13.6 / 14.7, 192 16.4 /
+// 13.3; 8 of 512 x 1024, r = 512 6.5 / 8.4; one of 8192 x 8192, r = 256 15.1 / 15.8,
+// 384 25.0 / 16.4.
+bool take_pairs(const ProductArgs &p, int sms)
+{
+    const long long groups = p.E < p.M ? p.E : p.M;
+    const auto rounds = [&](int tile, int units) {
+        const long long even = p.M / tile + groups / 2, rows = even > groups ? even : groups;
+        return (rows * ((p.N + tile - 1) / tile) + units - 1) / units;
+    };
+    return 5 * rounds(Shape<true>::kTile, sms / 2) < 4 * rounds(Shape<false>::kTile, sms);
+}
+
 }  // namespace
 
 cudaError_t launch_product(const ProductArgs &p, const uint8_t *a, const uint8_t *w, int fmt, int sms, bool pdl,
@@ -599,8 +616,7 @@ cudaError_t launch_product(const ProductArgs &p, const uint8_t *a, const uint8_t
         g_encode = reinterpret_cast<EncodeFn>(fn);
     });
     if (g_encode_status != cudaSuccess) return g_encode_status;
-    // Pairs where the average group fills more than one CTA's tile.
-    const bool pair = p.M / p.E > 128 && p.N > 128;
+    const bool pair = take_pairs(p, sms);
     Maps maps;
     const cudaError_t e = make_maps(&maps, p, a, w, fmt, pair ? Shape<true>::kRowAtoms : Shape<false>::kRowAtoms);
     if (e != cudaSuccess) return e;
