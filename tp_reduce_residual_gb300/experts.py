@@ -13,7 +13,6 @@ in the library's kernels and there is no fallback.
 """
 from __future__ import annotations
 
-import ctypes
 from dataclasses import dataclass
 from typing import NamedTuple, Optional
 
