@@ -111,6 +111,42 @@ def test_route_scores_closer_than_32_bits(score):
     check_route(x, k, bias=bias, score=score, groups=8, top_groups=3, group_top=2)
 
 
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("k", [1, 2, 3])
+def test_route_a_third_key_crosses_two_equal_ones(score, k):
+    """Two experts of one logit and bias, and a third whose logit passes by them in steps of one unit in the
+    last place: 2^-26 of its score at a step."""
+    T = 1024
+    x = torch.full((T, 40), -3.0)
+    x[:, 17] = x[:, 30] = 0.25
+    x[:, 35] = 0.7 + torch.arange(-T // 2, T // 2) * 2.0 ** -24
+    s = ref.scores(x[T // 2].double(), score)
+    bias = torch.zeros(40)
+    bias[17] = bias[30] = float(s[35] - s[17])
+    check_route(x, k, bias=bias, score=score)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("copies,masked", [(2, 0.0), (3, 0.0), (1, 0.8), (2, 0.6)])
+@pytest.mark.parametrize("k,groups,top,gtop", [(1, 1, 1, 1), (5, 1, 1, 1), (8, 8, 3, 2), (6, 8, 2, 1), (3, 4, 1, 2), (8, 24, 8, 2)])
+def test_route_equal_and_close_scores_at_the_border(score, copies, masked, k, groups, top, gtop):
+    """Scores within 2^-25 of one another, each held by several experts: the k-th and the next may be equal and
+    a third between them and the bound on 32-bit errors; groups of nearly equal rank with few experts left."""
+    g = gen(100 * copies + k + groups)
+    E = 96
+    x = torch.randn(80, E // copies, generator=g).repeat_interleave(copies, 1)
+    x[:] = x[0, :, ].clone()
+    s = ref.scores(x[0].double(), score)
+    bias = (1.0 - s).float()
+    order = torch.stack([torch.randperm(E, generator=g) for _ in range(80)])
+    for t in range(80):
+        b, row = bias[order[t]], x[t][order[t]].clone()
+        if masked:
+            row[torch.rand(E, generator=g) < masked] = -math.inf
+        if t % 4 == 0:  # one token a call, each with a bias of its own
+            check_route(row[None], k, bias=b, score=score, groups=groups, top_groups=top, group_top=gtop)
+
+
 @pytest.mark.parametrize("score,renormalize", [("softmax", True), ("softmax", False), ("sigmoid", True), ("sigmoid", False)])
 @pytest.mark.parametrize("biased", [False, True])
 @pytest.mark.parametrize("groups", [1, 4])

@@ -25,7 +25,7 @@
 // take the largest of the 32 heads (redux.sync) and advance one lane.  What bounds
 // it is instruction issue: 1160 instructions a token at 256 experts in 8 groups with
 // a bias and k = 8 (ncu), of which the rounds are a third.  16384 such tokens take
-// 25.0 us (IPC 3.1; the bytes alone would take 1.4), one token 3.1.  Searching the
+// 27 us (IPC 3.1; the bytes alone would take 1.4), one token 3.1.  Searching the
 // lane's 8 keys again after each round, with indexes apart, took 1590 instructions
 // and 47 us, 20 of them a tail of rows that were selected whole in 64 bits.
 #include <cfloat>
@@ -513,19 +513,35 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
         const float atn = __shfl_down_sync(kAll, at, 1), xn = __shfl_down_sync(kAll, x, 1),
                     bn = __shfl_down_sync(kAll, b, 1);
         // equal logits and biases have equal keys: the index decides
-        const bool open = __any_sync(kAll, lane + 1 < n && !(at - atn > bound(fmaxf(fabsf(at), fabsf(atn))) ||
-                                                             (x == xn && b == bn)));
+        const bool apart = at - atn > bound(fmaxf(fabsf(at), fabsf(atn))), same = x == xn && b == bn;
+        bool open = __any_sync(kAll, lane + 1 < n && !(apart || same));
+        const float last = __shfl_sync(kAll, at, a.k - 1);
+        if (!open && __any_sync(kAll, lane == a.k - 1 && lane + 1 < n && !apart)) {
+            // the last and the next are equal: is one of another key behind them within the bound?
+            const float xl = __shfl_sync(kAll, x, a.k - 1), bl = __shfl_sync(kAll, b, a.k - 1);
+            if (head > -INFINITY) {
+#pragma unroll
+                for (int j = 0; j < VPT; ++j) {
+                    const float v = without_position<VPT>(key[j]);
+                    if (v > -INFINITY && last - v <= bound(fmaxf(fabsf(last), fabsf(v)))) {
+                        const int e = lane * VPT + position_of<VPT>(key[j]);
+                        open |= to_f32(row[e]) != xl || (a.bias && __ldg(a.bias + e) != bl);
+                    }
+                }
+            }
+            open = __any_sync(kAll, open);
+        }
         if (!sure || open) {
             // every expert that may belong among the k
-            const float last = __shfl_sync(kAll, at, a.k - 1);
             while (sure && n < 32 && m > -INFINITY && last - m <= bound(fmaxf(fabsf(last), fabsf(m)))) {
                 choose(m);
                 m = warp_max(head);
             }
             __syncwarp();
-            if (!sure || n == 32)
+            if (!sure || n == 32) {
                 id = select64<T, VPT, SUMS>(row, a, lane, slots[warp]);
-            else
+                n = 32;  // its ids say how many there are
+            } else
                 id = order64<T, SUMS>(row, a, lane, n, lane < n ? list[lane] : -1, top, sum_once(), list);
         }
     }
