@@ -387,7 +387,8 @@ BN_API size_t bn_quantize_fp4_workspace_bytes(int x_rows, int M, int K, bn_fp4 f
  *            when rows is given and it holds bn_quantize_fp4_workspace_bytes()
  *            (not 0), for two kernels on `stream` instead of one.  Nothing in it
  *            is kept.
- * K is a multiple of 32.  With v = x / tensor_scale, the scale of a block is the e4m3
+ * K is a multiple of 32.  With v = x / tensor_scale (in FP32, whose range it must
+ * not leave), the scale of a block is the e4m3
  * value next to max|v| / 6, at most 448 (BN_NVFP4), or
  * 2^(floor(log2 max|v|) - 2) (BN_MXFP4); codes are v / scale to the nearest,
  * half way to the even code, at most 6, all exactly decided.  A block with an

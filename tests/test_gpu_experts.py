@@ -112,6 +112,19 @@ def test_route_scores_closer_than_32_bits(score):
 
 
 @pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("levels", [1, 2, 3])
+@pytest.mark.parametrize("E,groups,top,gtop", [(256, 8, 4, 2), (256, 8, 3, 1), (96, 3, 2, 2), (60, 4, 2, 2)])
+def test_route_many_ties_in_groups(score, levels, E, groups, top, gtop):
+    """Logits and biases of one to three values: groups whose best are many equal experts."""
+    g = gen(E + levels)
+    x = torch.randint(0, levels, (24, E), generator=g).float() / 2
+    x[5, ::3] = -math.inf
+    bias = torch.randint(0, levels, (E,), generator=g).float() / 8
+    for b in (None, torch.zeros(E), bias):
+        check_route(x, 8, bias=b, score=score, groups=groups, top_groups=top, group_top=gtop)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
 @pytest.mark.parametrize("k", [1, 2, 3])
 def test_route_a_third_key_crosses_two_equal_ones(score, k):
     """Two experts of one logit and bias, and a third whose logit passes by them in steps of one unit in the

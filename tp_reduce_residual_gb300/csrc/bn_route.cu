@@ -289,7 +289,17 @@ __device__ __noinline__ bool groups64(const T *row, const RouteArgs &a, int lane
             v[4] = fmaxf(v[4], x);
         }
     const float need = a.group_top > 1 ? v[1] : v[0];  // a key this far below cannot count
-    const bool ok = !(need > -INFINITY) || need - v[4] > error;
+    bool ok = !(need > -INFINITY) || need - v[4] > error;
+    if (!ok) {
+        // Keys that equal both the third and the fourth (ties: same logit, same bias) add nothing to the four.
+        const float x3 = to_f32(row[e[3]]), b3 = a.bias ? __ldg(a.bias + e[3]) : 0.0f;
+        ok = to_f32(row[e[2]]) == x3 && (!a.bias || __ldg(a.bias + e[2]) == b3);
+        for (int i = 0; ok && i < size; ++i) {
+            const int at = lane * size + i;
+            if (need - slot[at] <= error && at != e[0] && at != e[1])
+                ok = to_f32(row[at]) == x3 && (!a.bias || __ldg(a.bias + at) == b3);
+        }
+    }
     double r1 = -INFINITY, r2 = -INFINITY, gap, largest;
 #pragma unroll
     for (int q = 0; q < 4; ++q)
