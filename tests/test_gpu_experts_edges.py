@@ -1,0 +1,54 @@
+"""The operators around the experts at the edges of their ranges, against the 64-bit definitions.
+
+Tolerances are those of ``test_gpu_experts`` except where a test states its own."""
+import math
+
+import pytest
+import torch
+
+from tests.test_gpu_experts import DTYPES, _gpu, check_route, gen  # noqa: F401
+
+pytestmark = pytest.mark.gpu
+
+LOWEST = torch.finfo(torch.float32).min
+
+
+# ---- routing: masks of the type's lowest value in small groups ---------------------------------------
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top,gtop", [(64, 32, 8, 1), (64, 32, 8, 2), (96, 32, 5, 1), (96, 32, 5, 2), (60, 20, 4, 2), (6, 3, 2, 1),
+                                               (24, 8, 3, 2), (40, 8, 2, 1), (256, 8, 4, 1), (256, 8, 4, 2)])
+@pytest.mark.parametrize("dtype", ["fp32", "bf16"])
+def test_route_groups_masked_by_the_lowest_value(score, E, groups, top, gtop, dtype):
+    """Experts masked by the type's lowest value, whole groups among them, with -inf beside them: a group may
+    have four keys or fewer left, and the sum of its two is past 32 bits."""
+    g = gen(E + groups)
+    x = torch.randn(24, E, generator=g).to(DTYPES[dtype])
+    low = torch.finfo(DTYPES[dtype]).min
+    x[torch.rand(24, E, generator=g) < 0.6] = low
+    x[torch.rand(24, E, generator=g) < 0.3] = -math.inf
+    x[0] = low
+    x[1, :E // groups] = low
+    x[2] = low
+    x[2, ::2] = -math.inf
+    x[3, E // groups:] = -math.inf
+    x[4] = -math.inf
+    check_route(x, min(3, top * (E // groups)), score=score, groups=groups, top_groups=top, group_top=gtop, renormalize=False)
+    check_route(x[:1], 2, score=score, groups=groups, top_groups=top, group_top=gtop, renormalize=False)
+
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("E,groups,top,gtop", [(64, 32, 8, 2), (96, 32, 5, 2), (60, 20, 4, 2), (6, 3, 2, 1), (256, 8, 4, 2)])
+@pytest.mark.parametrize("dtype", ["fp32", "fp16"])
+def test_route_groups_masked_by_the_bias(score, E, groups, top, gtop, dtype):
+    """The same masks held by the bias, and biases so high that sums of two pass 32 bits upwards."""
+    g = gen(E + top)
+    x = torch.randn(8, E, generator=g).to(DTYPES[dtype])
+    x[torch.rand(8, E, generator=g) < 0.3] = -math.inf
+    for value in (LOWEST, -LOWEST):
+        bias = 0.1 * torch.randn(E, generator=g)
+        bias[torch.rand(E, generator=g) < 0.5] = value
+        bias[:E // groups] = value
+        bias[E - 1] = -math.inf
+        check_route(x, min(3, top * (E // groups)), bias=bias, score=score, groups=groups, top_groups=top, group_top=gtop,
+                    renormalize=False)

@@ -166,7 +166,8 @@ __device__ __forceinline__ void push2(F v, F &a, F &b)
 // The groups that stay, as bits, from the two largest keys of group `lane` (lanes
 // past the groups hold -inf).  `gap`: how far the lowest rank that stays is above
 // the highest that goes (inf if none goes); `largest`: the largest sum of the sizes
-// of a group's two keys.
+// of the keys that rank a group.  In 32 bits it is inf for two keys of the type's
+// lowest value: no bound then tells anything, and the ranks are taken in 64 bits.
 template <typename F>
 __device__ __forceinline__ unsigned keep_groups(F r1, F r2, int lane, const RouteArgs &a, F &gap, F &largest)
 {
@@ -181,7 +182,7 @@ __device__ __forceinline__ unsigned keep_groups(F r1, F r2, int lane, const Rout
     const F low = -warp_max(keep && rank > (F)-INFINITY ? -rank : (F)-INFINITY);
     const F high = warp_max(!keep && lane < a.groups ? rank : (F)-INFINITY);
     const F size1 = r1 > (F)-INFINITY ? (r1 < 0 ? -r1 : r1) : (F)0, size2 = r2 > (F)-INFINITY ? (r2 < 0 ? -r2 : r2) : (F)0;
-    largest = warp_max(size1 + size2);
+    largest = warp_max(a.group_top > 1 ? size1 + size2 : size1);
     gap = high > (F)-INFINITY ? low - high : (F)INFINITY;
     return __ballot_sync(kAll, keep);
 }
@@ -289,14 +290,16 @@ __device__ __noinline__ bool groups64(const T *row, const RouteArgs &a, int lane
             v[4] = fmaxf(v[4], x);
         }
     const float need = a.group_top > 1 ? v[1] : v[0];  // a key this far below cannot count
-    bool ok = !(need > -INFINITY) || need - v[4] > error;
+    // With at most four keys they are all there, whatever the error (it may be inf);
+    // past this, e[0..3] are experts.
+    bool ok = !(v[4] > -INFINITY) || need - v[4] > error;
     if (!ok) {
         // Keys that equal both the third and the fourth (ties: same logit, same bias) add nothing to the four.
         const float x3 = to_f32(row[e[3]]), b3 = a.bias ? __ldg(a.bias + e[3]) : 0.0f;
         ok = to_f32(row[e[2]]) == x3 && (!a.bias || __ldg(a.bias + e[2]) == b3);
         for (int i = 0; ok && i < size; ++i) {
             const int at = lane * size + i;
-            if (need - slot[at] <= error && at != e[0] && at != e[1])
+            if (slot[at] > -INFINITY && need - slot[at] <= error && at != e[0] && at != e[1])
                 ok = to_f32(row[at]) == x3 && (!a.bias || __ldg(a.bias + at) == b3);
         }
     }
