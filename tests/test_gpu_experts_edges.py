@@ -6,6 +6,7 @@ import math
 import pytest
 import torch
 
+from tp_reduce_residual_gb300 import experts
 from tests.test_gpu_experts import DTYPES, _gpu, check_route, gen  # noqa: F401
 
 pytestmark = pytest.mark.gpu
@@ -52,3 +53,36 @@ def test_route_groups_masked_by_the_bias(score, E, groups, top, gtop, dtype):
         bias[E - 1] = -math.inf
         check_route(x, min(3, top * (E // groups)), bias=bias, score=score, groups=groups, top_groups=top, group_top=gtop,
                     renormalize=False)
+
+
+# ---- the product: what is in flight when a pair of CTAs leaves -----------------------------------------
+
+def test_products_back_to_back():
+    """Short products on pairs of CTAs, each followed at once by kernels that take over its shared memory (a
+    product on single CTAs and one on pairs): an arrival that came after its CTA had left would land on one
+    of their barriers.  Every output has the bits of the first, and no wait gave up."""
+    g = gen(40)
+
+    def operands(rows, N, K):
+        a = experts.quantize_fp4(torch.randn(rows, K, generator=g).bfloat16().cuda(), "nvfp4")
+        b = experts.quantize_fp4(torch.randn(N, K, generator=g).bfloat16().cuda(), "nvfp4")
+        return a, b
+
+    calls = [operands(2100, 2056, 32), operands(130, 264, 64), operands(900, 4360, 96)]
+    want = [experts.expert_product(a, b) for a, b in calls]
+    outs = [[torch.empty_like(w) for w in want] for _ in range(2)]
+    torch.cuda.synchronize()
+    off = torch.zeros((), dtype=torch.long, device="cuda")
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        for _ in range(100):
+            for set_ in outs:  # six products without another kernel between them
+                for (a, b), o in zip(calls, set_):
+                    experts.expert_product(a, b, out=o)
+            for set_ in outs:
+                for o, w in zip(set_, want):
+                    off += (o != w).sum()
+                    o.zero_()
+    side.synchronize()
+    assert off.item() == 0

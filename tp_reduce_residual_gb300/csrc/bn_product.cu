@@ -208,6 +208,15 @@ __device__ __forceinline__ void commit(uint32_t bar)
     else
         asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
 }
+// The same on this CTA's barrier alone.
+template <bool PAIR>
+__device__ __forceinline__ void commit_here(uint32_t bar)
+{
+    if constexpr (PAIR)
+        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
+    else
+        commit<false>(bar);
+}
 __device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
 __device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
 
@@ -454,8 +463,10 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     }
                 }
             }
+            // Every product has ended before tensor memory is freed.  Only this CTA waits, so
+            // only its barrier is told: an arrival at the other's could come after it left.
             if (elect_one()) {
-                commit<PAIR>(done);  // every product has ended before tensor memory is freed
+                commit_here<PAIR>(done);
                 wait_phase<false, kDrain>(done, 0, ctl);
             }
         }
