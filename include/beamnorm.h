@@ -325,7 +325,9 @@ typedef enum { BN_NVFP4 = 0, BN_MXFP4 = 1 } bn_fp4;
  *            equal groups) by rising index.  The order is that of exact
  *            arithmetic on the given logits and biases, up to 64-bit rounding.
  *   w        [R, T, k] FP32, the same for every shard: scale * s, or
- *            scale * s / (sum of the k chosen s) with renormalize
+ *            scale * s / (sum of the k chosen s) with renormalize, however small
+ *            the scores; chosen sigmoids that are all 0 in 64 bits (logits below
+ *            -709.78, such as masks of the type's lowest value) have weights 0
  * A logit or bias of -inf takes its expert out.  Slots without an expert left
  * get id -1 and weight 0.  A NaN takes its expert out and makes all k weights
  * of its row NaN.

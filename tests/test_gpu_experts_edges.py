@@ -6,8 +6,9 @@ import math
 import pytest
 import torch
 
-from tp_reduce_residual_gb300 import experts
+from tests import experts_reference as ref
 from tests.test_gpu_experts import DTYPES, _gpu, check_route, gen  # noqa: F401
+from tp_reduce_residual_gb300 import experts
 
 pytestmark = pytest.mark.gpu
 
@@ -86,3 +87,64 @@ def test_products_back_to_back():
                     o.zero_()
     side.synchronize()
     assert off.item() == 0
+
+
+# ---- normalised sigmoids of small scores ---------------------------------------------------------------
+
+def small_scores(dtype, seed):
+    """Rows whose largest chosen logit is far below 0, to where the scores leave 32 bits, and mixed ones."""
+    g = gen(seed)
+    x = torch.randn(12, 40, generator=g)
+    for t, shift in enumerate((-20, -60, -69, -75, -87, -90, -104, -200, -650)):
+        x[t] += shift
+    x[9] -= 75
+    x[9, ::3] -= 300
+    x[10] -= 90
+    x[10, 7] = 3.0
+    x[11] = -90.0
+    return x.to(DTYPES[dtype])
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_route_normalised_sigmoids_of_small_scores(dtype, groups):
+    """The weights are s over their sum however small the scores are."""
+    x = small_scores(dtype, 50)
+    _, w = check_route(x, 8, score="sigmoid", scale=2.5, groups=groups, top_groups=min(groups, 2))
+    assert ((w.sum(-1) - 2.5).abs() < 2.5 * 2.0 ** -18).all()
+
+
+def test_route_normalised_sigmoids_past_64_bits_are_zero():
+    """Rows whose chosen logits are all below -709.78, where exp(-x) passes 64 bits, count as masked; beside a
+    larger one such a logit has weight 0."""
+    x = torch.full((4, 32), -709.0)
+    x[1] = -710.0
+    x[2] = -65504.0
+    x[3] = LOWEST
+    x[3, 4] = -709.5
+    _, w = experts.route(x.cuda(), 8, score="sigmoid")
+    w = w[0].cpu()
+    assert ((w[0] - 0.125).abs() <= 2.0 ** -18).all()
+    assert (w[1] == 0).all() and (w[2] == 0).all()
+    assert w[3].tolist() == [1.0] + [0.0] * 7
+    dw = torch.randn(1, 4, 8, generator=gen(51)).cuda()
+    ids = torch.arange(8, dtype=torch.int32).repeat(4, 1).cuda()
+    d = experts.route_backward(x.cuda(), ids, dw, score="sigmoid").cpu()
+    assert torch.isfinite(d).all() and (d[1] == 0).all() and (d[2] == 0).all()
+
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp16", "fp32"])
+def test_route_backward_normalised_sigmoids_of_small_scores(dtype):
+    """dx_j = w_j (c_j - sum_i w_i c_i) (1 - s_j): each w within 2^-18 (32-bit exponentials of differences of at
+    most 8, or weights that are nothing beside the others), so 2^-16 of w_j (|c_j| + sum_i w_i |c_i|)."""
+    x = small_scores(dtype, 52)
+    ids, _ = ref.route(x, 8, score="sigmoid")
+    c = torch.randn(12, 8, generator=gen(53))
+    x64 = x.double().requires_grad_()
+    (ref.route_weights(x64, ids, "sigmoid", True, 1.0) * c.double()).sum().backward()
+    got = experts.route_backward(x.cuda(), ids.cuda(), c[None].cuda(), score="sigmoid").cpu().double()
+    w = ref.route_weights(x.double(), ids, "sigmoid", True, 1.0)
+    size = w * (c.double().abs() + (w * c.double().abs()).sum(-1, keepdim=True))
+    tol = torch.zeros_like(got).scatter_(1, ids.long(), 2.0 ** -16 * size)
+    tol += torch.finfo(DTYPES[dtype]).eps / 2 * x64.grad.abs() + (2.0 ** -25 if dtype == "fp16" else 1e-37)
+    assert ((got - x64.grad).abs() <= tol).all()

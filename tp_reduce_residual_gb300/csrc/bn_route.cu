@@ -7,7 +7,9 @@
 //   groups > 1: a group's rank is the sum of its `group_top` largest keys; the
 //     `top_groups` groups of the highest rank stay
 //   ids = the k largest keys left, equal keys by rising index
-//   w   = scale * s_id, or scale * s_id / sum over the k of s
+//   w   = scale * s_id, or scale * s_id / sum over the k of s; sigmoids over their
+//     sum are taken as s exp(-m) = 1 / (exp(m) + exp(m - x)), m the largest chosen
+//     logit but at most 0, so that small ones keep their digits
 // A logit or bias of -inf takes its expert out; slots for which no expert is
 // left get id -1 and weight 0.  A NaN logit or key takes its expert out and
 // makes the row's weights NaN.
@@ -123,6 +125,10 @@ __device__ __forceinline__ double sigmoid(double x) { return 1.0 / (1.0 + exp(-x
 // max(d exp(-d)) * 2^-24: under 2^-18 of the largest probability together.
 constexpr float kSigmoidError = 1.5f * 0x1p-22f;
 constexpr float kSoftmaxError = 0x1p-18f;
+
+// Where exp(-x) passes 64 bits, a sigmoid counts as 0: chosen logits that are all
+// below it (masks of the type's lowest value) have no weights.
+constexpr float kNoSigmoid = -709.7827f;
 
 __device__ __forceinline__ float rcp_approx(float v)
 {
@@ -564,7 +570,8 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
     const float x = on ? to_f32(row[id]) : -INFINITY;
     float w, sum = 1.0f;
     if (a.sigmoid) {
-        w = on ? rcp_approx(1.0f + expf(-x)) : 0.0f;
+        const float m = a.renormalize ? fminf(warp_max(x), 0.0f) : 0.0f;
+        w = on && m > kNoSigmoid ? rcp_approx(expf(m) + expf(m - x)) : 0.0f;
         if (a.renormalize) sum = warp_sum(w);
     } else if (a.renormalize) {
         const float most = warp_max(x);
@@ -575,7 +582,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
     }
     if (lane < a.k) {
         w *= a.scale;
-        if (a.renormalize) w /= fmaxf(sum, 1e-30f);
+        if (a.renormalize) w /= fmaxf(sum, FLT_MIN);  // 0, or a half and more
         if (nan) w = NAN;
         const long long at_out = (long long)t * a.k + lane, shard = (long long)a.T * a.k;
         a.ids[at_out] = id;
@@ -589,7 +596,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
 //   softmax, renormalised:  dx_j = w_j (c_j - sum_i w_i c_i),  w = softmax over the chosen
 //   softmax:                dx_e = p_e (c_e - sum_j p_j c_j)   for every e (c_e = 0 unless chosen)
 //   sigmoid:                dx_j = c_j s_j (1 - s_j)
-//   sigmoid, renormalised:  c_j is first replaced by (c_j - sum_i (s_i / S) c_i) / S, S = sum of s
+//   sigmoid, renormalised:  dx_j = w_j (c_j - sum_i w_i c_i) (1 - s_j),  w = s / sum of s as in the forward
 // 1 - s is computed as sigmoid(-x), which keeps its digits near s = 1.  One
 // warp per token: the chosen slots sit on lanes, are scattered into the warp's
 // row in shared memory, and the row is written once with 16-byte stores.  16384
@@ -647,10 +654,14 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const __gri
     } else {
         float d;
         if (a.sigmoid) {
-            const float s = on ? sigmoid(x) : 0.0f;
+            float s = on ? sigmoid(x) : 0.0f;
             if (a.renormalize) {
-                const float total = fmaxf(warp_sum(s), 1e-30f);
-                c = (c - warp_sum(s / total * c)) / total;
+                const float m = fminf(warp_max(x), 0.0f);
+                // a NaN is not below the limit: it shows
+                s = on && !(m < kNoSigmoid && x <= m) ? 1.0f / (expf(m) + expf(m - x)) : 0.0f;
+                const float total = warp_sum(s);
+                s = total == 0.0f ? 0.0f : s / total;
+                c -= warp_sum(s * c);
             }
             d = on ? c * s * sigmoid(-x) : 0.0f;
         } else {
