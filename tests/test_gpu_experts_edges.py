@@ -148,3 +148,49 @@ def test_route_backward_normalised_sigmoids_of_small_scores(dtype):
     tol = torch.zeros_like(got).scatter_(1, ids.long(), 2.0 ** -16 * size)
     tol += torch.finfo(DTYPES[dtype]).eps / 2 * x64.grad.abs() + (2.0 ** -25 if dtype == "fp16" else 1e-37)
     assert ((got - x64.grad).abs() <= tol).all()
+
+
+# ---- gradients of saturated rows -----------------------------------------------------------------------
+
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("score,renormalize", [("softmax", True), ("softmax", False), ("sigmoid", True)])
+@pytest.mark.parametrize("gap", [4, 8, 12, 20, 40, 80])
+def test_route_backward_of_a_dominant_expert(dtype, score, renormalize, gap):
+    """One expert (or two) far ahead: its gradient w_j sum_i w_i (c_j - c_i) is as exact as the others'.  Logits
+    are whole numbers, so exponentials are the only errors of w: 2^-18 with their sum.  With D the largest,
+    2^-16 of w_j (|c_j - c_D| + sum_i w_i |c_i - c_D|) and the rounding to the logits' type."""
+    g = gen(gap)
+    T, E, k = 10, 48, 6
+    x = torch.randint(-3, 1, (T, E), generator=g).float() - (gap if score == "sigmoid" else 0)
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32)
+    for t in range(T):
+        x[t, ids[t, t % k]] += gap
+    x[8, ids[8, 0]] = x[8, ids[8, 2]]  # two of them
+    x[9, (set(range(E)) - set(ids[9].tolist())).pop()] = gap + 5.0  # one that was not chosen
+    c = torch.randint(-8, 9, (T, k), generator=g).float()
+    c[0] = torch.tensor([1.0, 0, 0, 0, 0, 0])
+    ids[1, 3] = -1
+    ids[1, 2], ids[1, 4] = ids[1, 1], ids[1, 1]  # an expert chosen again
+    x, up = x.to(DTYPES[dtype]), torch.zeros(T, E, dtype=torch.float64)
+    got = experts.route_backward(x.cuda(), ids.cuda(), c[None].cuda(), score=score, renormalize=renormalize).cpu().double()
+    want, size = torch.zeros(T, E, dtype=torch.float64), torch.zeros(T, E, dtype=torch.float64)
+    for t in range(T):
+        on = [j for j in range(k) if ids[t, j] >= 0]
+        e = [int(ids[t, j]) for j in on]
+        cc = [float(c[t, j]) for j in on]
+        if not renormalize:  # every expert of the row, with the sum of its slots' c
+            cc = [sum(v for i, v in zip(e, cc) if i == n) for n in range(E)]
+            e = list(range(E))
+        z = x[t, e].double()
+        w = torch.softmax(z, 0) if score == "softmax" else torch.softmax(torch.nn.functional.logsigmoid(z), 0)
+        cc = torch.tensor(cc, dtype=torch.float64)
+        d = w * (w * (cc[:, None] - cc)).sum(1)
+        far = cc - cc[w.argmax()]
+        s = w * (far.abs() + (w * far.abs()).sum())
+        if score == "sigmoid":
+            d, s = d * torch.sigmoid(-z), s * torch.sigmoid(-z)
+        for i, n in enumerate(e):
+            want[t, n] += d[i]
+            size[t, n] += s[i]
+    tol = 2.0 ** -16 * size + torch.finfo(DTYPES[dtype]).eps / 2 * want.abs() + 1e-37
+    assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
