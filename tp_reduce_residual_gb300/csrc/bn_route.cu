@@ -655,29 +655,25 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const __gri
         const unsigned best = __ballot_sync(kAll, on && x == top);
         if (best) first = __shfl_sync(kAll, id, __ffs(best) - 1);
     } else {
-        const auto of_largest = [&](float w) {  // the c of the largest weight
-            const unsigned best = __ballot_sync(kAll, w == warp_max(w));
-            return best ? __shfl_sync(kAll, c, __ffs(best) - 1) : 0.0f;
-        };
+        const float top = warp_max(x);
+        if (!a.sigmoid || a.renormalize) {  // less the c of the largest logit
+            const unsigned best = __ballot_sync(kAll, x == top);
+            if (best) c -= __shfl_sync(kAll, c, __ffs(best) - 1);
+        }
         float d;
-        if (a.sigmoid) {
-            float s = on ? sigmoid(x) : 0.0f;
-            if (a.renormalize) {
-                const float m = fminf(warp_max(x), 0.0f);
-                // a NaN is not below the limit: it shows
-                s = on && !(m < kNoSigmoid && x <= m) ? 1.0f / (expf(m) + expf(m - x)) : 0.0f;
-                const float total = warp_sum(s);
-                s = total == 0.0f ? 0.0f : s / total;
-                c -= of_largest(s);
-                c -= warp_sum(s * c);
-            }
-            d = on ? c * s * sigmoid(-x) : 0.0f;
-        } else {
-            const float m = warp_max(x);
-            float w = on && x != -INFINITY ? expf(x - m) : 0.0f;
+        if (!a.sigmoid) {
+            float w = on && x != -INFINITY ? expf(x - top) : 0.0f;
             w = w / fmaxf(warp_sum(w), 1e-30f);
-            c -= of_largest(w);
             d = w * (c - warp_sum(w * c));
+        } else if (a.renormalize) {
+            const float m = fminf(top, 0.0f);
+            // a NaN is not below the limit: it shows
+            const float s = on && !(m < kNoSigmoid && x <= m) ? 1.0f / (expf(m) + expf(m - x)) : 0.0f;
+            const float total = warp_sum(s), w = total == 0.0f ? 0.0f : s / total;
+            c -= warp_sum(w * c);
+            d = w * c * (on ? sigmoid(-x) : 0.0f);
+        } else {
+            d = on ? c * sigmoid(x) * sigmoid(-x) : 0.0f;
         }
         if (on) atomicAdd(buf + id, d);
     }
