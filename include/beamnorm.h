@@ -330,7 +330,8 @@ typedef enum { BN_NVFP4 = 0, BN_MXFP4 = 1 } bn_fp4;
  *            -709.78, such as masks of the type's lowest value) have weights 0
  * A logit or bias of -inf takes its expert out.  Slots without an expert left
  * get id -1 and weight 0.  A NaN takes its expert out and makes all k weights
- * of its row NaN.
+ * of its row NaN.  A logit of +inf makes a softmax's k weights NaN (inf - inf),
+ * and with them its s + bias.
  * Source: none -- the pages describe no router; it has no counterpart there. */
 BN_API bn_status bn_route(const void *logits, bn_dtype dtype, long long ld, int T, int E, int k,
                           const float *bias, bn_score score, int groups, int top_groups,

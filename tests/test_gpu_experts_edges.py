@@ -89,6 +89,27 @@ def test_products_back_to_back():
     assert off.item() == 0
 
 
+# ---- routing: infinite logits --------------------------------------------------------------------------
+
+@pytest.mark.parametrize("renormalize", [True, False])
+@pytest.mark.parametrize("biased", [False, True])
+def test_route_infinite_logit(renormalize, biased):
+    """exp(inf - inf): a softmax with an infinite logit has no weights, as with a NaN; a sigmoid of it is 1."""
+    x = torch.randn(5, 64, generator=gen(60))
+    x[1, 7] = math.inf
+    x[3, 9] = x[3, 40] = math.inf
+    x[4, 8:] = -math.inf
+    x[4, 3] = math.inf
+    bias = torch.zeros(64, device="cuda") if biased else None
+    ids, w = experts.route(x.cuda(), 10, bias=bias, renormalize=renormalize)
+    clean = experts.route(x[[0, 2]].cuda(), 10, bias=bias, renormalize=renormalize)
+    assert torch.isnan(w[0, [1, 3, 4]]).all() and torch.equal(w[0, [0, 2]], clean[1][0])
+    assert torch.equal(ids[[0, 2]], clean[0])
+    ids, w = experts.route(x.cuda(), 10, bias=bias, score="sigmoid", renormalize=False)
+    assert ids[1, 0].item() == 7 and ids[3, :2].tolist() == [9, 40] and ids[4, 0].item() == 3
+    assert w[0, 1, 0].item() == 1.0 and torch.isfinite(w).all()
+
+
 # ---- normalised sigmoids of small scores ---------------------------------------------------------------
 
 def small_scores(dtype, seed):

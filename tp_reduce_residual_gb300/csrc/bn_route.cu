@@ -12,7 +12,7 @@
 //     logit but at most 0, so that small ones keep their digits
 // A logit or bias of -inf takes its expert out; slots for which no expert is
 // left get id -1 and weight 0.  A NaN logit or key takes its expert out and
-// makes the row's weights NaN.
+// makes the row's weights NaN; so does a logit of inf a softmax's (inf - inf).
 //
 // The order of keys is decided as in exact arithmetic.  Logits of 16 bits compare
 // exactly.  Sums s + bias are computed in 32 bits with a bound on their error, and
@@ -406,6 +406,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
 #pragma unroll
         for (int j = 0; j < VPT; ++j) top = fmaxf(top, key[j]);  // a NaN is passed over
         top = warp_max(top);
+        nan |= top == INFINITY;
         float sum = 0.0f;
 #pragma unroll
         for (int j = 0; j < VPT; ++j) sum += key[j] > -INFINITY ? expf(key[j] - top) : 0.0f;
@@ -575,6 +576,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
         if (a.renormalize) sum = warp_sum(w);
     } else if (a.renormalize) {
         const float most = warp_max(x);
+        nan |= most == INFINITY;
         w = on ? expf(x - most) : 0.0f;
         sum = warp_sum(w);
     } else {
