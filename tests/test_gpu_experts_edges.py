@@ -8,6 +8,7 @@ import torch
 
 from tests import experts_reference as ref
 from tests.test_gpu_experts import DTYPES, _gpu, check_route, gen  # noqa: F401
+from tp_reduce_residual_gb300 import beamnorm as bn
 from tp_reduce_residual_gb300 import experts
 
 pytestmark = pytest.mark.gpu
@@ -215,3 +216,116 @@ def test_route_backward_of_a_dominant_expert(dtype, score, renormalize, gap):
             size[t, n] += s[i]
     tol = 2.0 ** -16 * size + torch.finfo(DTYPES[dtype]).eps / 2 * want.abs() + 1e-37
     assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
+
+
+# ---- outputs on a caller's stream ----------------------------------------------------------------------
+
+def pool_of(t):
+    """The stream whose allocator pool a tensor's memory comes from."""
+    for s in torch.cuda.memory_snapshot():
+        if s["address"] <= t.data_ptr() < s["address"] + s["total_size"]:
+            return s["stream"]
+    raise AssertionError("not the allocator's memory")
+
+
+def calls():
+    """Every binding that allocates an output, by name."""
+    g = gen(70)
+    R, T, k, H, E, K = 2, 6, 2, 256, 4, 64
+    part = torch.randn(R, T, H, generator=g).bfloat16().cuda()
+    eo = torch.randn(R, T * k, H, generator=g).bfloat16().cuda()
+    perm = torch.arange(T * k, dtype=torch.int32).view(1, T, k).repeat(R, 1, 1).cuda()
+    w = torch.rand(R, T, k, generator=g).cuda()
+    sum_ = torch.randn(T, H, generator=g).cuda()
+    gamma = torch.ones(H, device="cuda")
+    logits = torch.randn(T, E, generator=g).cuda()
+    ids = torch.randint(0, E, (T, k), generator=g).to(torch.int32).cuda()
+    x = torch.randn(T, K, generator=g).bfloat16().cuda()
+    a = experts.quantize_fp4(x, "nvfp4")
+    b = experts.quantize_fp4(torch.randn(16, K, generator=g).bfloat16().cuda(), "nvfp4")
+    res = lambda: torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+    r = [res() for _ in range(8)]
+    return dict(
+        reduce_norm=lambda s: [bn.reduce_norm(part, r[0], gamma, gamma, 1e-6, stream=s)],
+        finalize_reduce_norm=lambda s: [bn.finalize_reduce_norm(eo, perm, w, None, r[1], gamma, gamma, 1e-6, stream=s)],
+        finalize_reduce_norm_noalloc=lambda s: [bn.finalize_reduce_norm_noalloc(eo, perm, w, None, r[2], gamma, gamma, 1e-6, stream=s)],
+        reduce_residual_norm=lambda s: [bn.reduce_residual_norm(part, r[3], gamma, 1e-6, stream=s)],
+        finalize_reduce_residual_norm=lambda s: [bn.finalize_reduce_residual_norm(eo, perm, w, None, r[4], gamma, 1e-6, stream=s)],
+        reduce_only=lambda s: [bn.reduce_only(part, stream=s)],
+        finalize_reduce_only=lambda s: [bn.finalize_reduce_only(eo, perm, w, None, stream=s)],
+        norm_only=lambda s: [bn.norm_only(sum_, r[5], gamma, gamma, 1e-6, stream=s)],
+        residual_norm_only=lambda s: [bn.residual_norm_only(sum_, r[6], gamma, 1e-6, stream=s)],
+        finalize_only=lambda s: [bn.finalize_only(eo, perm, w, None, stream=s)],
+        route=lambda s: list(experts.route(logits, 2, stream=s)),
+        route_backward=lambda s: [experts.route_backward(logits, ids, w[:1], stream=s)],
+        plan=lambda s: list(experts.plan(ids, E, stream=s)),
+        quantize_fp4=lambda s: (lambda q: [q.data, q.scales])(experts.quantize_fp4(x, "nvfp4", stream=s)),
+        dequantize_fp4=lambda s: [experts.dequantize_fp4(a, stream=s)],
+        expert_product=lambda s: [experts.expert_product(a, b, stream=s)])
+
+
+@pytest.mark.parametrize("form", ["stream", "address"])
+@pytest.mark.parametrize("name", ["reduce_norm", "finalize_reduce_norm", "finalize_reduce_norm_noalloc", "reduce_residual_norm",
+                                  "finalize_reduce_residual_norm", "reduce_only", "finalize_reduce_only", "norm_only",
+                                  "residual_norm_only", "finalize_only", "route", "route_backward", "plan", "quantize_fp4",
+                                  "dequantize_fp4", "expert_product"])
+def test_new_outputs_come_from_the_calls_stream(name, form):
+    """A block of the current stream's pool may still be in use there when another stream writes it."""
+    call = calls()[name]
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = call(side if form == "stream" else side.cuda_stream)
+    side.synchronize()
+    for t in got:
+        assert pool_of(t) == side.cuda_stream
+    for t in call(torch.cuda.current_stream().cuda_stream) + call(0):
+        assert pool_of(t) == torch.cuda.current_stream().cuda_stream
+    torch.cuda.synchronize()
+    if not name.endswith("norm") and "norm_" not in name:  # the others change their residual
+        for a, b in zip(got, want[:1] if name == "quantize_fp4" else want):  # scale places of no row are not written
+            assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("name", ["reduce_only", "route"])
+def test_new_outputs_are_not_the_current_streams_blocks(name):
+    """The current stream is busy and has freed blocks that it will still write: outputs of a call on another
+    stream keep their values."""
+    call = calls()[name]
+    want = [t.clone() for t in call(None)]
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    busy = torch.empty(1 << 28, dtype=torch.float32, device="cuda")
+    for _ in range(20):  # some milliseconds
+        busy.fill_(1.0)
+    for t in want:  # freed at once, filled after that
+        for _ in range(4):
+            torch.empty_like(t).fill_(7)
+    got = call(side)
+    torch.cuda.synchronize()
+    for a, b in zip(got, want):
+        assert torch.equal(a, b)
+
+
+def test_fallback_runs_on_an_address():
+    """The unfused pieces of a declined shape run on the stream whose address is given, copies included."""
+    R, T, H = 2, 2, 40960
+    g = gen(71)
+    part = torch.randn(R, T, H, generator=g).bfloat16().cuda()
+    gamma = torch.ones(H, device="cuda")
+    side = torch.cuda.Stream()
+    outs = []
+    for stream in (None, side.cuda_stream):
+        res = torch.zeros(T, H, dtype=torch.bfloat16, device="cuda")
+        debug = bn.Debug(sum=torch.zeros(T, H, device="cuda"))
+        torch.cuda.synchronize()
+        if stream is not None:  # the current stream is busy: what went there would come late
+            busy = torch.empty(1 << 28, dtype=torch.float32, device="cuda")
+            for _ in range(20):
+                busy.fill_(1.0)
+        out = bn.reduce_norm(part, res, gamma, gamma, 1e-6, debug=debug, stream=stream, on_decline="fallback")
+        (side if stream is not None else torch.cuda.current_stream()).synchronize()
+        with torch.cuda.stream(side):
+            outs.append((out.clone(), debug.sum.clone()))
+        torch.cuda.synchronize()
+    assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])

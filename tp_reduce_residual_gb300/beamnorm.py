@@ -9,6 +9,10 @@ BF16 tensors are ``torch.bfloat16``; perm is ``torch.int32``; w, gammas and
 FP32 sums are ``torch.float32``.  Shapes: partials [R,T,H], expert_out
 [R,T*k,H], perm and w [R,T,k], shared [R,T,H] (or None), residual and out
 [T,H], gammas [H].  The residual is updated in place.
+
+``stream`` (a stream object or its address) is where a call's kernels go; by
+default the current stream.  Inputs have to be ready there.  Outputs that are not
+given are allocated as that stream's; whoever reads them elsewhere waits for it.
 """
 from __future__ import annotations
 
@@ -160,7 +164,35 @@ def _check(status: int):
 def _stream(t: torch.Tensor, stream) -> int:
     if stream is None:
         stream = torch.cuda.current_stream(t.device)
+    return _address(stream)
+
+
+def _address(stream) -> int:
     return int(stream.cuda_stream) if hasattr(stream, "cuda_stream") else int(stream)
+
+
+def _on(stream, dev):
+    """A context in which ``stream`` (a stream object or its address) is torch's current one."""
+    if isinstance(stream, torch.cuda.Stream):
+        return torch.cuda.stream(stream)
+    address = _address(stream)
+    # 0, 1 and 2 are CUDA's names of the default streams, which wait for one another
+    return torch.cuda.stream(torch.cuda.default_stream(dev) if address <= 2
+                             else torch.cuda.ExternalStream(address, device=dev))
+
+
+def _empty(shape, dtype, dev, stream) -> torch.Tensor:
+    """A new output, from the allocator's pool of the stream that writes it: a block of
+    the current stream's pool may still be in use there.  The current stream, where the
+    caller may read it, is recorded with it."""
+    if stream is not None and dev.type == "cuda":
+        current = torch.cuda.current_stream(dev)
+        if _address(stream) != current.cuda_stream:
+            with _on(stream, dev):
+                t = torch.empty(shape, dtype=dtype, device=dev)
+            t.record_stream(current)
+            return t
+    return torch.empty(shape, dtype=dtype, device=dev)
 
 
 def _need(t: Optional[torch.Tensor], name: str, dtype, shape, device) -> int:
@@ -217,8 +249,7 @@ def _fallback_allowed(err: "BeamNormError", on_decline: str) -> bool:
 
 def _fallback(partials, z_inputs, residual, gamma_post, gamma_pre, eps, out, debug, stream,
               single: bool):
-    ctx = torch.cuda.stream(stream) if hasattr(stream, "cuda_stream") else _nullctx()
-    with ctx:
+    with _nullctx() if stream is None else _on(stream, out.device):
         if z_inputs is not None:
             expert_out, perm, w, shared = z_inputs
             partials = finalize_only(expert_out, perm, w, shared, stream=stream)
@@ -253,7 +284,7 @@ def reduce_norm(partials, residual, gamma_post, gamma_pre, eps: float, out=None,
     R, T, H = partials.shape
     dev = partials.device
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, H), torch.bfloat16, dev, stream)
     args = (_need(partials, "partials", torch.bfloat16, (R, T, H), dev), R, T, H,
             _need(residual, "residual", torch.bfloat16, (T, H), dev),
             _need(gamma_post, "gamma_post", torch.float32, (H,), dev),
@@ -311,7 +342,7 @@ def finalize_reduce_norm(expert_out, perm, w, shared, residual, gamma_post, gamm
     H = expert_out.shape[-1]
     dev = expert_out.device
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, H), torch.bfloat16, dev, stream)
     args = (_need(expert_out, "expert_out", torch.bfloat16, (R, T * k, H), dev),
             _need(perm, "perm", torch.int32, (R, T, k), dev),
             _need(w, "w", torch.float32, (R, T, k), dev),
@@ -357,7 +388,7 @@ def finalize_reduce_norm_noalloc(expert_out, perm, w, shared, residual, gamma_po
     H = expert_out.shape[-1]
     dev = expert_out.device
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, H), torch.bfloat16, dev, stream)
     args = (_need(expert_out, "expert_out", torch.bfloat16, (R, T * k, H), dev),
             _need(perm, "perm", torch.int32, (R, T, k), dev),
             _need(w, "w", torch.float32, (R, T, k), dev),
@@ -382,7 +413,7 @@ def reduce_residual_norm(partials, residual, gamma, eps: float, out=None,
     R, T, H = partials.shape
     dev = partials.device
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, H), torch.bfloat16, dev, stream)
     args = (_need(partials, "partials", torch.bfloat16, (R, T, H), dev), R, T, H,
             _need(residual, "residual", torch.bfloat16, (T, H), dev),
             _need(gamma, "gamma", torch.float32, (H,), dev), float(eps),
@@ -411,7 +442,7 @@ def finalize_reduce_residual_norm(expert_out, perm, w, shared, residual, gamma, 
     H = expert_out.shape[-1]
     dev = expert_out.device
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, H), torch.bfloat16, dev, stream)
     args = (_need(expert_out, "expert_out", torch.bfloat16, (R, T * k, H), dev),
             _need(perm, "perm", torch.int32, (R, T, k), dev),
             _need(w, "w", torch.float32, (R, T, k), dev),
@@ -443,7 +474,7 @@ def reduce_only(partials, sum_out=None, stream=None) -> torch.Tensor:
     R, T, H = partials.shape
     dev = partials.device
     if sum_out is None:
-        sum_out = torch.empty((T, H), dtype=torch.float32, device=dev)
+        sum_out = _empty((T, H), torch.float32, dev, stream)
     with _with_device(partials):
         _check(L.bn_reduce_only(_need(partials, "partials", torch.bfloat16, (R, T, H), dev), R, T, H,
                                 _need(sum_out, "sum_out", torch.float32, (T, H), dev),
@@ -458,7 +489,7 @@ def finalize_reduce_only(expert_out, perm, w, shared, sum_out=None, stream=None)
     H = expert_out.shape[-1]
     dev = expert_out.device
     if sum_out is None:
-        sum_out = torch.empty((T, H), dtype=torch.float32, device=dev)
+        sum_out = _empty((T, H), torch.float32, dev, stream)
     with _with_device(expert_out):
         _check(L.bn_finalize_reduce_only(
             _need(expert_out, "expert_out", torch.bfloat16, (R, T * k, H), dev),
@@ -476,7 +507,7 @@ def norm_only(sum_, residual, gamma_post, gamma_pre, eps: float, out=None,
     T, H = sum_.shape
     dev = sum_.device
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, H), torch.bfloat16, dev, stream)
     args = (_need(sum_, "sum", torch.float32, (T, H), dev), T, H,
             _need(residual, "residual", torch.bfloat16, (T, H), dev),
             _need(gamma_post, "gamma_post", torch.float32, (H,), dev),
@@ -496,7 +527,7 @@ def residual_norm_only(sum_, residual, gamma, eps: float, out=None,
     T, H = sum_.shape
     dev = sum_.device
     if out is None:
-        out = torch.empty((T, H), dtype=torch.bfloat16, device=dev)
+        out = _empty((T, H), torch.bfloat16, dev, stream)
     args = (_need(sum_, "sum", torch.float32, (T, H), dev), T, H,
             _need(residual, "residual", torch.bfloat16, (T, H), dev),
             _need(gamma, "gamma", torch.float32, (H,), dev), float(eps),
@@ -514,7 +545,7 @@ def finalize_only(expert_out, perm, w, shared, z_out=None, stream=None) -> torch
     H = expert_out.shape[-1]
     dev = expert_out.device
     if z_out is None:
-        z_out = torch.empty((R, T, H), dtype=torch.bfloat16, device=dev)
+        z_out = _empty((R, T, H), torch.bfloat16, dev, stream)
     with _with_device(expert_out):
         _check(L.bn_finalize_only(
             _need(expert_out, "expert_out", torch.bfloat16, (R, T * k, H), dev),

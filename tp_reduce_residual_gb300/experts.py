@@ -88,10 +88,10 @@ def _ptr(t, name, dtype, shape, dev):
     return _bn._need(t, name, dtype, tuple(shape), dev)
 
 
-def _out(t, name, dtype, shape, dev):
+def _out(t, name, dtype, shape, dev, stream):
     """An output and its address: the caller's, checked, or a new one."""
     if t is None:
-        t = torch.empty(shape, dtype=dtype, device=dev)
+        t = torch.empty(shape, dtype=dtype, device=dev) if stream is None else _bn._empty(shape, dtype, dev, stream)
         return t, t.data_ptr()
     return t, _ptr(t, name, dtype, shape, dev)
 
@@ -146,8 +146,8 @@ def route(logits, k: int, bias=None, score: str = "softmax", groups: int = 1, to
     dev = logits.device
     dtype = _dtype(logits, "logits")
     bp = None if bias is None else _ptr(bias, "bias", _FLOAT32, (E,), dev)
-    ids, ip = _out(ids, "ids", _INT32, (T, k), dev)
-    w, wp = _out(w, "w", _FLOAT32, (shards, T, k), dev)
+    ids, ip = _out(ids, "ids", _INT32, (T, k), dev, stream)
+    w, wp = _out(w, "w", _FLOAT32, (shards, T, k), dev, stream)
     _call("bn_route", (logits.data_ptr(), dtype, ld, T, E, k, bp, _name(SCORES, score, "score"), groups, top_groups,
                        group_top, 1 if renormalize else 0, scale, shards, ip, wp), dev.index, stream)
     return ids, w
@@ -166,7 +166,7 @@ def route_backward(logits, ids, dw, score: str = "softmax", renormalize: bool = 
     R, _, k = dw.shape
     ip = _ptr(ids, "ids", _INT32, (T, k), dev)
     dp = _ptr(dw, "dw", _FLOAT32, (R, T, k), dev)
-    dlogits, op = _out(dlogits, "dlogits", logits.dtype, (T, E), dev)
+    dlogits, op = _out(dlogits, "dlogits", logits.dtype, (T, E), dev, stream)
     _call("bn_route_backward", (logits.data_ptr(), dtype, ld, T, E, k, ip, dp, R, _name(SCORES, score, "score"),
                                 1 if renormalize else 0, scale, op), dev.index, stream)
     return dlogits
@@ -180,9 +180,9 @@ def plan(ids, experts: int, shards: int = 1, perm=None, offsets=None, rows=None,
     T, k = ids.shape
     dev = ids.device
     ip = _ptr(ids, "ids", _INT32, (T, k), dev)
-    perm, pp = _out(perm, "perm", _INT32, (shards, T, k), dev)
-    offsets, op = _out(offsets, "offsets", _INT32, (experts + 1,), dev)
-    rows, rp = _out(rows, "rows", _INT32, (T * k,), dev)
+    perm, pp = _out(perm, "perm", _INT32, (shards, T, k), dev, stream)
+    offsets, op = _out(offsets, "offsets", _INT32, (experts + 1,), dev, stream)
+    rows, rp = _out(rows, "rows", _INT32, (T * k,), dev, stream)
     _call("bn_expert_plan", (ip, T, k, experts, shards, pp, op, rp), dev.index, stream)
     return Plan(perm, offsets, rows)
 
@@ -263,8 +263,8 @@ def quantize_fp4(x, format: str, rows=None, offsets=None, tensor_scale: float = 
         raise ValueError("offsets must have 2 entries or more")
     dshape = (*lead, K // 2) if lead is not None else (M, K // 2)
     groups = max(groups, 1)
-    data, dp = _out(data, "data", _UINT8, dshape, dev)
-    scales, sp = _out(scales, "scales", _UINT8, fp4_scales_shape(M, K, format, groups, op is not None), dev)
+    data, dp = _out(data, "data", _UINT8, dshape, dev, stream)
+    scales, sp = _out(scales, "scales", _UINT8, fp4_scales_shape(M, K, format, groups, op is not None), dev, stream)
     wp, wn = None, 0
     if workspace is not None:
         wp, wn = _bn._workspace(workspace, dev)
@@ -282,7 +282,7 @@ def dequantize_fp4(q: FP4, dtype=torch.bfloat16, out=None, stream=None) -> torch
     """The values of quantised rows ([..., K]) in BF16, FP16 or FP32."""
     M, K, groups, op, dp, sp = _layout(q, "q")
     dev = q.data.device
-    out, yp = _out(out, "out", dtype if out is None else out.dtype, q.shape, dev)
+    out, yp = _out(out, "out", dtype if out is None else out.dtype, q.shape, dev, stream)
     _call("bn_dequantize_fp4", (dp, sp, M, K, op, max(groups, 1), FORMATS[q.format], q.tensor_scale, yp, _dtype(out, "out")),
           dev.index, stream)
     return out
@@ -306,7 +306,7 @@ def expert_product(a: FP4, w: FP4, scale: float = 1.0, out=None, stream=None) ->
     if w.data.device != dev:
         raise ValueError(f"w is on {w.data.device}, expected {dev}")
     N = w.data.shape[-2]
-    out, yp = _out(out, "out", torch.bfloat16, (M, N), dev)
+    out, yp = _out(out, "out", torch.bfloat16, (M, N), dev, stream)
     _call("bn_expert_product", (ap, sp, M, wp, wsp, E, N, K, op, FORMATS[a.format], scale * a.tensor_scale * w.tensor_scale, yp),
           dev.index, stream)
     return out
