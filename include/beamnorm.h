@@ -381,7 +381,9 @@ BN_API size_t bn_quantize_fp4_workspace_bytes(int x_rows, int M, int K, bn_fp4 f
  *   rows     [M] int32 or NULL; values outside [0, x_rows) set
  *            BN_DEVERR_PERM_RANGE and read row 0
  *   offsets  [groups + 1] int32 (groups <= 1024; rows past the last offset are a
- *            group of their own) or NULL: equal groups of M / groups rows
+ *            group of their own; rows before the first, where the offsets are a
+ *            part of a longer list, are in no group and have no scales) or NULL:
+ *            equal groups of M / groups rows
  *   tensor_scale  a power of two in [2^-64, 2^64]; a value is
  *            code * block scale * tensor_scale
  *   data     [M, K / 2]: element 2i in the low half of byte i
@@ -404,7 +406,8 @@ BN_API bn_status bn_quantize_fp4(const void *x, bn_dtype dtype, long long ld, in
                                  void *stream);
 
 /* The values [M, K] of quantised rows, in BF16, FP16 or FP32 (BF16 and FP32
- * hold every value exactly within their range).
+ * hold every value exactly within their range).  Rows before the first offset
+ * are zeros.
  * Source: none -- it has no counterpart on the pages. */
 BN_API bn_status bn_dequantize_fp4(const uint8_t *data, const uint8_t *scales, int M, int K,
                                    const int32_t *offsets, int groups, bn_fp4 format,
@@ -416,7 +419,7 @@ BN_API bn_status bn_dequantize_fp4(const uint8_t *data, const uint8_t *scales, i
  *   w, w_scales  [E, N, K] quantised as E equal groups of N rows
  *   offsets      [E + 1] int32, or NULL when E == 1 (every row)
  *   alpha        the product of the operands' tensor scales, and any factor
- *   out          [M, N] BF16; rows past the last offset are zeros
+ *   out          [M, N] BF16; rows before the first offset and past the last are zeros
  * N is a multiple of 8, K of 32.  Offsets that fall or leave [0, M] set
  * BN_DEVERR_OFFSETS; they are clamped.
  * Source: none -- the pages take the experts' rows as given; it has no counterpart there. */

@@ -329,3 +329,61 @@ def test_fallback_runs_on_an_address():
             outs.append((out.clone(), debug.sum.clone()))
         torch.cuda.synchronize()
     assert torch.equal(outs[0][0], outs[1][0]) and torch.equal(outs[0][1], outs[1][1])
+
+
+# ---- groups that are a part of a longer list ------------------------------------------------------------
+
+@pytest.mark.parametrize("fmt", ["nvfp4", "mxfp4"])
+@pytest.mark.parametrize("first", [1, 50, 128, 300])
+@pytest.mark.parametrize("counts,tail", [([3, 0, 130, 1], 5), ([0, 257], 0), ([0, 0], 40)])
+@pytest.mark.parametrize("repeated", [False, True])
+def test_rows_before_the_first_group(fmt, first, counts, tail, repeated):
+    """Offsets that do not begin at 0, as one of several holders of the experts has them: its groups' rows are
+    what they are without the rows before them, and those are zeros."""
+    g = gen(first + tail)
+    K, n = (8192, 20) if repeated else (96, 40)
+    scale = 4 if repeated else 1  # enough work that rows are quantised once into the workspace
+    counts, first, tail = [c * scale for c in counts], first * scale, tail * scale
+    first = max(first, 2048 - sum(counts) - tail) if repeated else first
+    M, E, N = first + sum(counts) + tail, len(counts), 40
+    offsets = (first + torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist())).to(torch.int32)
+    x = torch.randn(n, K, generator=g).bfloat16().cuda()
+    rows = torch.randint(0, n, (M,), generator=g).to(torch.int32).cuda()
+    assert (experts.quantize_workspace_bytes(n, M, K, fmt) > 0) == repeated
+    part = experts.quantize_fp4(x, fmt, rows=rows[first:], offsets=(offsets - first).cuda())
+    shape = experts.fp4_scales_shape(M, K, fmt, E, True)
+    got = []
+    for work in (None, torch.empty(16, dtype=torch.uint8, device="cuda")):
+        scales = torch.full(shape, 85, dtype=torch.uint8, device="cuda")
+        q = experts.quantize_fp4(x, fmt, rows=rows, offsets=offsets.cuda(), scales=scales, workspace=work)
+        assert torch.equal(q.data[first:], part.data)
+        assert (scales[:first // 128] == 85).all()  # no row's places
+        got.append(scales)
+        v = experts.dequantize_fp4(q, dtype=torch.float32)
+        assert (v[:first] == 0).all() and torch.equal(v[first:], experts.dequantize_fp4(part, dtype=torch.float32))
+    assert torch.equal(got[0], got[1])
+    w = experts.quantize_fp4((torch.randn(E, N, K, generator=g) / 8).bfloat16().cuda(), fmt)
+    out = torch.full((M, N), math.nan, dtype=torch.bfloat16, device="cuda")
+    experts.expert_product(q, w, out=out)
+    assert bn.check_device_error() == 0
+    assert (out[:first] == 0).all() and torch.equal(out[first:], experts.expert_product(part, w))
+    assert (out[M - tail:] == 0).all()
+
+
+def test_rows_before_the_first_group_on_pairs_of_ctas():
+    """The same where the product runs on pairs of CTAs."""
+    g = gen(81)
+    first, counts, tail, N, K = 300, [900, 1300], 70, 2312, 96
+    M = first + sum(counts) + tail
+    offsets = torch.tensor([300, 1200, 2500], dtype=torch.int32, device="cuda")
+    x = torch.randn(M, K, generator=g).bfloat16().cuda()
+    w = experts.quantize_fp4((torch.randn(2, N, K, generator=g) / 8).bfloat16().cuda(), "nvfp4")
+    out = torch.full((M, N), math.nan, dtype=torch.bfloat16, device="cuda")
+    experts.expert_product(experts.quantize_fp4(x, "nvfp4", offsets=offsets), w, out=out)
+    part = experts.expert_product(experts.quantize_fp4(x[first:], "nvfp4", offsets=offsets - first), w)
+    assert bn.check_device_error() == 0
+    assert (out[:first] == 0).all() and torch.equal(out[first:], part) and (out[2500:] == 0).all()
+    experts.expert_product(experts.quantize_fp4(x, "nvfp4", offsets=offsets[:2]),
+                           experts.FP4(w.data[:1], w.scales[:19], "nvfp4"), out=out.fill_(math.nan))
+    assert bn.check_device_error() == 0
+    assert (out[:first] == 0).all() and torch.equal(out[first:1200], part[:900]) and (out[1200:] == 0).all()

@@ -61,9 +61,11 @@ template <> struct Half2<__half> {
 };
 
 // The row's place among the scale tiles.  The group is the number of group ends
-// at or below m (a warp-wide count, in bounds whatever the offsets hold).
+// at or below m (a warp-wide count, in bounds whatever the offsets hold).  A row
+// before its group's start (one before the first offset) is in no group and has none.
 struct Place {
     int tile, r;
+    bool in;
 };
 __device__ __forceinline__ Place place_of(const QuantArgs &a, int m, int lane)
 {
@@ -72,13 +74,14 @@ __device__ __forceinline__ Place place_of(const QuantArgs &a, int m, int lane)
         int n = 0;
         for (int i = lane; i < a.groups; i += 32) n += __ldg(a.offsets + 1 + i) <= m ? 1 : 0;
         g = __reduce_add_sync(kAll, n);
-        start = min(max(__ldg(a.offsets + g), 0), m);
+        start = max(__ldg(a.offsets + g), 0);
+        if (start > m) return {0, 0, false};
         const int r = m - start;
-        return {(start >> 7) + g + (r >> 7), r & 127};
+        return {(start >> 7) + g + (r >> 7), r & 127, true};
     }
     g = m / a.per;
     const int r = m - g * a.per;
-    return {g * a.tiles_per + (r >> 7), r & 127};
+    return {g * a.tiles_per + (r >> 7), r & 127, true};
 }
 
 // Eight codes, the first in the lowest four bits.
@@ -184,7 +187,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) quantize_kernel(const __grid_c
             src = 0;
         }
     }
-    const Place p = WORK ? Place{0, 0} : place_of(a, m, lane);
+    const Place p = WORK ? Place{0, 0, true} : place_of(a, m, lane);
     const T *x = static_cast<const T *>(a.x) + src * a.ld;
     uint8_t *data = a.data + (long long)m * (a.K / 2);
     // scales of this row: 4 bytes of every 512-byte tile
@@ -219,7 +222,7 @@ __global__ void __launch_bounds__(kRowWarps * 32) quantize_kernel(const __grid_c
             // four scales of one tile row: of lanes 0..3 of four (NVFP4) or of every second of eight (MXFP4)
             uint32_t word = code | (__shfl_down_sync(kAll, code, MX ? 2 : 1) << 8);
             word |= __shfl_down_sync(kAll, word, MX ? 4 : 2) << 16;
-            if ((lane & (MX ? 7 : 3)) == 0 && (FULL || at < k1))
+            if ((lane & (MX ? 7 : 3)) == 0 && p.in && (FULL || at < k1))
                 *reinterpret_cast<uint32_t *>(scales + (size_t)(at / kChunk) * (WORK ? 4 : 512)) = word;
         }
         k += 512 * kAhead;
@@ -247,15 +250,16 @@ place_rows_kernel(const __grid_constant__ QuantArgs a, const uint8_t *work, cons
             int n = 0;
             for (int i = lane + 1; i <= a.groups; i += 32) n += (min(max(__ldg(a.offsets + i), 0), a.M) >> 7) + i <= tile ? 1 : 0;
             const int g = __reduce_add_sync(kAll, n);
-            const int start = min(max(__ldg(a.offsets + g), 0), a.M);
-            row0 = start + ((long long)tile - (start >> 7) - g) * 128;
+            const int start = min(max(__ldg(a.offsets + g), 0), a.M), local = tile - (start >> 7) - g;
+            if (local < 0) return;  // before the first group: no row's place
+            row0 = start + local * 128LL;
             end = g < a.groups ? min(max(__ldg(a.offsets + g + 1), 0), a.M) : a.M;
         } else {
             const int g = tile / a.tiles_per;
             row0 = (long long)g * a.per + (long long)(tile - g * a.tiles_per) * 128;
             end = (long long)(g + 1) * a.per;
         }
-        if (row0 < 0 || row0 >= end) return;
+        if (row0 >= end) return;
         const uint32_t *from[4];
         bool in[4];
 #pragma unroll
@@ -348,6 +352,11 @@ __global__ void __launch_bounds__(kRowWarps * 32) dequantize_kernel(const __grid
     constexpr unsigned kAhead = 4;  // steps of 256 values, 8 a lane, whose loads are in flight together
     const unsigned k1 = min((unsigned)a.K, (blockIdx.y + 1) * (unsigned)share);
     unsigned k = blockIdx.y * (unsigned)share + lane * 8u;
+    if (!p.in) {  // no group, no scales
+        const f2 zeros[4] = {};
+        for (; k < k1; k += 256) store8<T>(out + k, zeros);
+        return;
+    }
     const auto steps = [&](auto full) {
         constexpr bool FULL = decltype(full)::value;
         uint32_t q[kAhead], b[kAhead];

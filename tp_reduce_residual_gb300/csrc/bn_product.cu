@@ -3,7 +3,7 @@
 // For the rows m of group e (offsets[e] <= m < offsets[e + 1]) and n in [0, N):
 //   out[m, n] = bf16(alpha * sum_k a[m, k] * w[e, n, k])
 // with a and w codes times block scales (bn_fp4.cu), summed in 32 bits by the
-// tensor core.  Rows past the last group are written as zeros.
+// tensor core.  Rows of no group (before the first, past the last) are written as zeros.
 //
 // Weights are the tensor core's M operand and rows its N operand, so that the few
 // rows an expert has in a decode batch cost a narrow product (N = 16 upwards)
@@ -518,11 +518,15 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                 }
             }
         }
-        // rows of no group
-        const long long first = (long long)start[p.E] * p.N / 8, last = (long long)p.M * p.N / 8;
-        for (long long i = first + (long long)blockIdx.x * (S::kThreads - 64) + (threadIdx.x - 64); i < last;
-             i += (long long)gridDim.x * (S::kThreads - 64))
-            reinterpret_cast<uint4 *>(p.out)[i] = make_uint4(0, 0, 0, 0);
+        // rows of no group: before the first, and past the last
+        const long long step = (long long)gridDim.x * (S::kThreads - 64);
+        const auto zeros = [&](long long row, long long end) {
+            const long long last = end * p.N / 8;
+            for (long long i = row * p.N / 8 + (long long)blockIdx.x * (S::kThreads - 64) + (threadIdx.x - 64); i < last; i += step)
+                reinterpret_cast<uint4 *>(p.out)[i] = make_uint4(0, 0, 0, 0);
+        };
+        zeros(0, start[0]);
+        zeros(start[p.E], p.M);
     }
     fence_before();
     __syncthreads();

@@ -44,8 +44,9 @@ class FP4:
     """Quantised rows: ``data`` uint8 [..., K/2] (element 2i in the low half of
     byte i) and ``scales`` uint8 [tiles, chunks, 512] in the layout that
     ``include/beamnorm.h`` describes at bn_fp4_scale_bytes.  ``offsets`` are the
-    ragged groups' first rows (int32 [groups+1]) or None: one group per leading
-    index of a 3-D ``data``, one group for a 2-D one."""
+    ragged groups' first rows (int32 [groups+1]; of a longer list a part, then the
+    rows before its first are in no group) or None: one group per leading index of
+    a 3-D ``data``, one group for a 2-D one."""
     data: torch.Tensor
     scales: torch.Tensor
     format: str
@@ -291,7 +292,7 @@ def dequantize_fp4(q: FP4, dtype=torch.bfloat16, out=None, stream=None) -> torch
 def expert_product(a: FP4, w: FP4, scale: float = 1.0, out=None, stream=None) -> torch.Tensor:
     """out [M,N] BF16: each row of ``a`` ([M,K], grouped by ``a.offsets``) times
     its group's weights of ``w`` ([E,N,K]; [N,K] is one expert), times ``scale``
-    and both tensor scales.  Rows past the last group are zeros."""
+    and both tensor scales.  Rows before the first group and past the last are zeros."""
     M, K, groups, op, ap, sp = _layout(a, "a")
     _, wK, E, wo, wp, wsp = _layout(w, "w")
     if wo is not None:
