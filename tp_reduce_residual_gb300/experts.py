@@ -62,13 +62,12 @@ class FP4:
 # below are written for the host's time: an argument that is as it should be passes
 # in one expression, and only one that is not goes through beamnorm's checks for
 # the message.
-_raw_stream = torch._C._cuda_getCurrentRawStream
 
 
 def _call(name, args, index, stream):
     """One C call with device ``index`` current, on ``stream`` or the current one."""
     if stream is None:
-        stream = _raw_stream(index)
+        stream = torch._C._cuda_getCurrentRawStream(index)
     else:
         stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
     fn = getattr(_bn._lib or _bn.load(), name)
