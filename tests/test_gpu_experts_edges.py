@@ -90,6 +90,27 @@ def test_products_back_to_back():
     assert off.item() == 0
 
 
+# ---- routing: 16-bit floats with sums ------------------------------------------------------------------
+
+@pytest.mark.parametrize("score", ["softmax", "sigmoid"])
+@pytest.mark.parametrize("T,E,k,groups,top,gtop", [
+    (40, 256, 8, 8, 4, 2), (17, 256, 8, 8, 3, 1), (9, 160, 6, 8, 3, 2), (11, 56, 5, 8, 5, 2), (5, 24, 4, 24, 7, 2),
+    (3, 1024, 16, 32, 4, 2), (8, 512, 10, 2, 1, 1), (4, 40, 2, 1, 1, 1), (6, 513, 16, 1, 1, 1)])
+@pytest.mark.parametrize("biased", [False, True])
+@pytest.mark.parametrize("strided", [False, True])
+def test_route_fp16_sums(score, T, E, k, groups, top, gtop, biased, strided):
+    """FP16 logits with a bias, with sums of group scores, and rows with masks, subnormals and the type's
+    extremes among them."""
+    g = gen(E + k + 1)
+    x = torch.randn(T, E, generator=g)
+    x[1] *= 2.0 ** -20
+    x[2, torch.rand(E, generator=g) < 0.5] = -math.inf
+    x = x.half()
+    x[0, 3], x[0, E - 1] = torch.finfo(torch.float16).min, -0.0
+    bias = 0.1 * torch.randn(E, generator=g) if biased else None
+    check_route(x, k, bias=bias, score=score, groups=groups, top_groups=top, group_top=gtop, shards=2, strided=strided)
+
+
 # ---- routing: infinite logits --------------------------------------------------------------------------
 
 @pytest.mark.parametrize("renormalize", [True, False])
