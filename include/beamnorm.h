@@ -370,9 +370,10 @@ BN_API size_t bn_fp4_scale_bytes(int M, int K, int groups, int ragged, bn_fp4 fo
 
 /* Bytes of workspace with which bn_quantize_fp4 quantises the x_rows rows of x once
  * and copies them to the M places that take them, or 0 where that does not pay:
- * it needs places four times the rows and work for the whole device
- * (M * K >= 2^24; measured: 32768 places of 4096 rows of 5120 in 30 us against
- * 45, 50 places of 5 rows slower by a launch).  Pure host logic.
+ * it needs 9000 places more than rows, and M * K >= 2^24 with 8 places a row or
+ * M * K >= 2^25 with 4 (measured: 32768 places of 4096 rows of 5120 in 28 us against
+ * 39 (MXFP4) and 34 against 54 (NVFP4); 8192 of 2048 rows of 8192 31 against 24).
+ * Pure host logic.
  * Source: no passage: library utility. */
 BN_API size_t bn_quantize_fp4_workspace_bytes(int x_rows, int M, int K, bn_fp4 format);
 

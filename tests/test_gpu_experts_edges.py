@@ -362,10 +362,10 @@ def test_rows_before_the_first_group(fmt, first, counts, tail, repeated):
     """Offsets that do not begin at 0, as one of several holders of the experts has them: its groups' rows are
     what they are without the rows before them, and those are zeros."""
     g = gen(first + tail)
-    K, n = (8192, 20) if repeated else (96, 40)
-    scale = 4 if repeated else 1  # enough work that rows are quantised once into the workspace
-    counts, first, tail = [c * scale for c in counts], first * scale, tail * scale
-    first = max(first, 2048 - sum(counts) - tail) if repeated else first
+    K, n = (608, 20) if repeated else (96, 40)
+    scale = 40 if repeated else 1  # enough work that rows are quantised once into the workspace
+    counts, tail = [c * scale for c in counts], tail * scale
+    first += max(0, 29000 - sum(counts) - tail) if repeated else 0
     M, E, N = first + sum(counts) + tail, len(counts), 40
     offsets = (first + torch.tensor([0] + torch.tensor(counts).cumsum(0).tolist())).to(torch.int32)
     x = torch.randn(n, K, generator=g).bfloat16().cuda()

@@ -13,6 +13,7 @@ in the library's kernels and there is no fallback.
 """
 from __future__ import annotations
 
+import functools
 from dataclasses import dataclass
 from typing import NamedTuple, Optional
 
@@ -215,6 +216,7 @@ def _layout(q: FP4, name: str):
     return M, K, groups, op, dp, sp
 
 
+@functools.lru_cache(maxsize=256)
 def quantize_workspace_bytes(n: int, M: int, K: int, format: str) -> int:
     """Workspace bytes with which ``quantize_fp4`` quantises n rows once for M
     places, or 0 where that does not pay."""
@@ -268,7 +270,7 @@ def quantize_fp4(x, format: str, rows=None, offsets=None, tensor_scale: float = 
     wp, wn = None, 0
     if workspace is not None:
         wp, wn = _bn._workspace(workspace, dev)
-    elif rp is not None and M >= 4 * n and M * K >= 1 << 24 and stream is None:
+    elif rp is not None and stream is None:
         wn = quantize_workspace_bytes(n, M, K, format)
         if wn:
             workspace = torch.empty(wn, dtype=_UINT8, device=dev)
