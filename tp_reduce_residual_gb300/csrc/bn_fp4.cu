@@ -22,11 +22,12 @@
 // a sum over the groups.  Scales past the end of a row are 0.
 //
 // One warp per row (or per share of a row): a lane takes 16 values, the four
-// lanes of a scale tile row join their scale bytes into one 4-byte store.  About 7
-// instructions a value bound the quantisation, so rows that are repeated (a token's
-// for each of its experts) are quantised once into a workspace and copied from there:
-// 32768 rows of 5120 from 4096 BF16 rows take 11 us and 18, where quantising each
-// place took 45.  The way back is bounded by memory: 92 MB in, 336 MB out in 65 us.
+// lanes of a scale tile row join their scale bytes into one 4-byte store.  Memory
+// bounds rows in their places (32768 rows of 5120, MXFP4: 63 us, 6.7 TB/s) and the
+// way back (67).  Where rows are repeated (a token's for each of its experts) they
+// come from L2, and about 7 instructions a value bound it, so enough of them are
+// quantised once into a workspace and copied from there: 32768 places of 4096 such
+// rows take 11 us and 18, where quantising each place takes 39.
 #include <type_traits>
 
 #include <cuda_bf16.h>

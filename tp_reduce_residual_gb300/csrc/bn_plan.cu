@@ -13,7 +13,7 @@
 // pass over the run hands them out.  Within 32 slots __match_any_sync finds
 // equal ids.  Latency bounds it (the bytes are a few hundred KB), so loads are
 // issued several at a time: ids eight steps ahead, the other CTAs' totals together
-// (131072 slots 13.6 us; one at a time 22).  610 slots take 3.8 us.
+// (131072 slots 14.1 us; one at a time 22).  610 slots take 3.9 us.
 #include "../../include/beamnorm.h"
 #include "bn_device.cuh"
 #include "bn_experts.h"

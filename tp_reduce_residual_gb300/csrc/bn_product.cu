@@ -17,11 +17,13 @@
 // pair of CTAs (cta_group::2): tiles of 256 features by 256 rows, of which each
 // CTA loads half the weights and half the rows; twice the products for the same
 // bytes, because what bounds large groups is the filling of shared memory by TMA
-// (about 60 bytes a cycle and SM here and in a loop of copies alone).
+// (60 bytes a cycle and SM here, 59.7 in a loop of copies from L2 alone, whatever the
+// number in flight).
 //
 // Measured.  Few rows: the stream of weights bounds it; 100 tokens with 8 of 256
 // experts (192 of them reached, 1.28 GB) 187 us, 6.9 TB/s; one token with 10 experts
-// (94 MB) 20 us, of which 12 stream, 2 find the tiles, 3 are the last tiles' tail.
+// (94 MB, not in L2) 20 us, 4.7 TB/s: its 640 tiles are a little over four rounds of
+// the device, so the fifth leaves most of it idle.
 // Large groups: 4096 tokens with 8 of 64 experts, N = 4096, K = 5120: 247 us in a
 // burst (5.6 PFLOP/s, tensor pipe 64 % active), 282 under the power cap at
 // 1.5 GHz.  In SM cycles: products alone 362 thousand, with scale copies 377, with

@@ -25,11 +25,11 @@
 // keys once (an odd-even merge sorting network; the position in the lane rides in
 // the keys' lowest bits, so that a comparison is one instruction), then k rounds
 // take the largest of the 32 heads (redux.sync) and advance one lane.  What bounds
-// it is instruction issue: 1160 instructions a token at 256 experts in 8 groups with
-// a bias and k = 8 (ncu), of which the rounds are a third.  16384 such tokens take
-// 27 us (IPC 3.1; the bytes alone would take 1.4), one token 3.1.  Searching the
-// lane's 8 keys again after each round, with indexes apart, took 1590 instructions
-// and 47 us, 20 of them a tail of rows that were selected whole in 64 bits.
+// it is instruction issue: 1390 instructions a token at 256 experts in 8 groups with
+// a bias and k = 8 (ncu).  16384 such tokens take 27 us (IPC 3.1; the bytes alone
+// would take 1.4), one token 3.6.  Searching the lane's 8 keys again after each round,
+// with indexes apart, took 47 us, 20 of them a tail of rows that were selected whole
+// in 64 bits.
 #include <cfloat>
 #include <cmath>
 
@@ -604,7 +604,7 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
 // largest weight is taken off first: its own c_j - sum_i w_i c_i is then a sum of the
 // others' terms and not what is left of two equal numbers.  One warp per token: the chosen slots sit on lanes, are scattered into the warp's
 // row in shared memory, and the row is written once with 16-byte stores.  16384
-// tokens of 128 FP32 logits, dense: 6.1 us for 18 MB; 4096 of 256 BF16, sparse: 3.3.
+// tokens of 128 FP32 logits, dense: 6.1 us for 18 MB; 4096 of 256 BF16, sparse: 3.5.
 template <typename T, int VPT, bool DENSE>
 __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const __grid_constant__ RouteBackwardArgs a)
 {
