@@ -239,6 +239,37 @@ def test_route_backward_of_a_dominant_expert(dtype, score, renormalize, gap):
     assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
 
 
+@pytest.mark.parametrize("dtype", ["bf16", "fp32"])
+@pytest.mark.parametrize("E", [8, 100, 1024])
+@pytest.mark.parametrize("spread", [0, 1, 3])
+def test_route_backward_of_light_experts(dtype, E, spread):
+    """No expert has much of the weight, the largest is chosen and its c is far above the others': the others'
+    gradients p_e (c_e - sum_i p_i c_i) are as exact as without it.  Whole logits, so 2^-16 of
+    p_e (|c_e| + sum_i p_i |c_i|), and with an expert D of more than a quarter of p (at 8 experts) of
+    4 p_e (|c_e - c_D| + sum_i p_i |c_i - c_D|)."""
+    g = gen(E + spread)
+    T, k = 12, 4
+    x = torch.randint(-spread, 1, (T, E), generator=g).float()
+    ids = torch.stack([torch.randperm(E, generator=g)[:k] for _ in range(T)]).to(torch.int32)
+    x[torch.arange(T), ids[:, 0].long()] = 0.0
+    c = torch.randint(-4, 5, (T, k), generator=g).float()
+    c[:, 0] = 4096.0
+    c[::2, 0] = 1.0
+    c[1::4, 1:] = 0.0
+    x = x.to(DTYPES[dtype])
+    got = experts.route_backward(x.cuda(), ids.cuda(), c[None].cuda(), renormalize=False).cpu().double()
+    p = torch.softmax(x.double(), 1)
+    u = torch.zeros(T, E, dtype=torch.float64).scatter_(1, ids.long(), c.double())
+    want = p * (p[:, None, :] * (u[:, :, None] - u[:, None, :])).sum(-1)
+    heavy, at = p.max(1)
+    off = torch.where(heavy > 0.25 - 2.0 ** -20, u.gather(1, at[:, None])[:, 0], 0.0)[:, None]
+    plain = p * (u.abs() + (p * u.abs()).sum(1, keepdim=True))
+    less = 4 * p * ((u - off).abs() + (p * (u - off).abs()).sum(1, keepdim=True))
+    size = torch.where(heavy[:, None] > 0.25 - 2.0 ** -20, torch.maximum(plain, less), plain)
+    tol = 2.0 ** -16 * size + torch.finfo(DTYPES[dtype]).eps / 2 * want.abs() + 1e-37
+    assert ((got - want).abs() <= tol).all(), ((got - want).abs() / tol).max()
+
+
 # ---- outputs on a caller's stream ----------------------------------------------------------------------
 
 def pool_of(t):

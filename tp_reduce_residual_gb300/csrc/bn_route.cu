@@ -600,9 +600,11 @@ __global__ void __launch_bounds__(kWarps * 32, VPT <= 8 ? 10 : 1) route_kernel(c
 //   sigmoid:                dx_j = c_j s_j (1 - s_j)
 //   sigmoid, renormalised:  dx_j = w_j (c_j - sum_i w_i c_i) (1 - s_j),  w = s / sum of s as in the forward
 // 1 - s is computed as sigmoid(-x), which keeps its digits near s = 1.  A constant
-// added to every c changes nothing but the plain sigmoid's gradient, so the c of the
-// largest weight is taken off first: its own c_j - sum_i w_i c_i is then a sum of the
-// others' terms and not what is left of two equal numbers.  One warp per token: the chosen slots sit on lanes, are scattered into the warp's
+// added to every c changes nothing but the plain sigmoid's gradient, so the c of an
+// expert with more than a quarter of the weight is taken off first: its own
+// c_j - sum_i w_i c_i is then a sum of the others' terms and not what is left of two
+// equal numbers.  (With less weight nothing cancels, and to take it off would add an
+// error of its size to all others.)  One warp per token: the chosen slots sit on lanes, are scattered into the warp's
 // row in shared memory, and the row is written once with 16-byte stores.  16384
 // tokens of 128 FP32 logits, dense: 6.1 us for 18 MB; 4096 of 256 BF16, sparse: 3.5.
 template <typename T, int VPT, bool DENSE>
@@ -636,7 +638,7 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const __gri
     const float x = on ? to_f32(row[id]) : -INFINITY;
     __syncwarp();
     float p[DENSE ? VPT : 1];
-    int first = -1;  // the row's largest logit, if it was chosen
+    int first = -1;  // the row's largest logit, if it was chosen and has much of the weight
     if constexpr (DENSE) {
         load_row<T, VPT>(row, a.E, lane, a.vec, -INFINITY, p);
         float top = -INFINITY;
@@ -654,24 +656,26 @@ __global__ void __launch_bounds__(kWarps * 32) route_backward_kernel(const __gri
 #pragma unroll
         for (int j = 0; j < VPT; ++j) p[j] *= inv;
         if (on) atomicAdd(buf + id, c);
-        const unsigned best = __ballot_sync(kAll, on && x == top);
+        const unsigned best = __ballot_sync(kAll, on && x == top && inv > 0.25f);  // its p is inv
         if (best) first = __shfl_sync(kAll, id, __ffs(best) - 1);
     } else {
+        const auto less_heaviest = [&](float w) {  // c less that of an expert of much weight
+            const unsigned heavy = __ballot_sync(kAll, w > 0.25f);
+            return heavy ? c - __shfl_sync(kAll, c, __ffs(heavy) - 1) : c;
+        };
         const float top = warp_max(x);
-        if (!a.sigmoid || a.renormalize) {  // less the c of the largest logit
-            const unsigned best = __ballot_sync(kAll, x == top);
-            if (best) c -= __shfl_sync(kAll, c, __ffs(best) - 1);
-        }
         float d;
         if (!a.sigmoid) {
             float w = on && x != -INFINITY ? expf(x - top) : 0.0f;
             w = w / fmaxf(warp_sum(w), 1e-30f);
+            c = less_heaviest(w);
             d = w * (c - warp_sum(w * c));
         } else if (a.renormalize) {
             const float m = fminf(top, 0.0f);
             // a NaN is not below the limit: it shows
             const float s = on && !(m < kNoSigmoid && x <= m) ? 1.0f / (expf(m) + expf(m - x)) : 0.0f;
             const float total = warp_sum(s), w = total == 0.0f ? 0.0f : s / total;
+            c = less_heaviest(w);
             c -= warp_sum(w * c);
             d = w * c * (on ? sigmoid(-x) : 0.0f);
         } else {
