@@ -429,6 +429,43 @@ BN_API bn_status bn_expert_product(const uint8_t *a, const uint8_t *a_scales, in
                                    const int32_t *offsets, bn_fp4 format, float alpha,
                                    uint16_t *out, void *stream);
 
+/* The experts' linear layers in 16 bits, for training and for weights that are not
+ * quantised: the rows m of group e (offsets[e] <= m < offsets[e + 1]) with its weights.
+ *   bn_expert_linear     y[m, n]     = sum over k of x[rows[m], k] * w[e, n, k]
+ *   bn_expert_linear_dx  dx[m, k]    = sum over n of dy[m, n] * w[e, n, k]
+ *   bn_expert_linear_dw  dw[e, n, k] = sum over the group's m of dy[m, n] * x[rows[m], k]
+ * summed in FP32 on the tensor core and rounded once.
+ *   dtype    BN_BF16 or BN_FP16: of every matrix (dw may be FP32)
+ *   x        [x_rows, K], dy [M, N]: rows ld (ld_dy) elements apart, a multiple of 8
+ *   rows     [M] int32 or NULL (then x_rows == M): the row of x at each place; values
+ *            outside [0, x_rows) set BN_DEVERR_PERM_RANGE and read row 0
+ *   w        [E, N, K] dense
+ *   offsets  [E + 1] int32, or NULL when E == 1 (every row).  Offsets that fall or
+ *            leave [0, M] set BN_DEVERR_OFFSETS; they are clamped
+ * Rows of y and dx before the first offset and past the last are zeros; such rows of
+ * x and dy are not read into any result.  dw of an empty group is zeros.  N and K are
+ * multiples of 8.
+ * Source: none -- the pages take the experts' rows as given; it has no counterpart there. */
+BN_API bn_status bn_expert_linear(const void *x, bn_dtype dtype, long long ld, int x_rows,
+                                  const int32_t *rows, int M, const void *w, int E, int N, int K,
+                                  const int32_t *offsets, void *y, void *stream);
+
+/* dx of bn_expert_linear, a row for every place (of rows that several places take, the
+ * gradients are the sum: bn_finalize_only with weights of 1 adds them up).
+ * Source: none -- it has no counterpart on the pages. */
+BN_API bn_status bn_expert_linear_dx(const void *dy, bn_dtype dtype, long long ld_dy, int M,
+                                     const void *w, int E, int N, int K, const int32_t *offsets,
+                                     void *dx, void *stream);
+
+/* dw of bn_expert_linear, in `dtype` or BN_FP32 (dw_dtype).  With accumulate != 0
+ * (BN_FP32 only) the sums are added to what dw holds, and dw of an empty group stays.
+ * Every sum has one order: equal calls give equal bits.
+ * Source: none -- it has no counterpart on the pages. */
+BN_API bn_status bn_expert_linear_dw(const void *dy, bn_dtype dtype, long long ld_dy, int M,
+                                     const void *x, long long ld, int x_rows, const int32_t *rows,
+                                     int E, int N, int K, const int32_t *offsets, void *dw,
+                                     bn_dtype dw_dtype, int accumulate, void *stream);
+
 /* ---- queries and errors ------------------------------------------------ */
 
 /* 1 if the fused entry points serve this shape (k = 0 for the reduce-only

@@ -139,6 +139,9 @@ def load() -> ctypes.CDLL:
             "bn_quantize_fp4_workspace_bytes": [_I, _I, _I, _I],
             "bn_dequantize_fp4": [_P, _P, _I, _I, _P, _I, _I, _F, _P, _I, _P],
             "bn_expert_product": [_P, _P, _I, _P, _P, _I, _I, _I, _P, _I, _F, _P, _P],
+            "bn_expert_linear": [_P, _I, _L, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P],
+            "bn_expert_linear_dx": [_P, _I, _L, _I, _P, _I, _I, _I, _P, _P, _P],
+            "bn_expert_linear_dw": [_P, _I, _L, _I, _P, _L, _I, _P, _I, _I, _I, _P, _P, _I, _I, _P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)

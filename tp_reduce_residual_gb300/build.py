@@ -48,11 +48,11 @@ MODES = {
 }
 
 # the operators around the experts, one object each
-EXPERTS = ["bn_experts_abi", "bn_route", "bn_plan", "bn_fp4", "bn_product"]
+EXPERTS = ["bn_experts_abi", "bn_route", "bn_plan", "bn_fp4", "bn_product", "bn_linear"]
 
 SOURCES = ["bn_device.cuh", "bn_internal.h", "bn_kernels.cu", "bn_abi.cu", "bn_wide.h",
            "bn_wide.cu", "bn_noalloc.cu", "bn_cluster.h", "bn_cluster.cu", "bn_host.h",
-           "bn_experts.h", *(f"{n}.cu" for n in EXPERTS)]
+           "bn_experts.h", "bn_tensor.cuh", *(f"{n}.cu" for n in EXPERTS)]
 
 
 def nvcc() -> str:

@@ -1,6 +1,6 @@
 // bn_experts.h -- the operators around the experts: launch arguments shared by
 // the ABI (bn_experts_abi.cu) and the kernels (bn_route.cu, bn_plan.cu,
-// bn_fp4.cu, bn_product.cu).  Not part of the ABI.
+// bn_fp4.cu, bn_product.cu, bn_linear.cu).  Not part of the ABI.
 #pragma once
 
 #include <atomic>
@@ -80,6 +80,21 @@ struct ProductArgs {
     unsigned *err;
 };
 
+// One product of an expert's linear layer.  Forward: out [M, F] = x [M, D] of rows of a
+// group times w [E, F, D]; input gradient: out [M, F] = dy [M, D] times w [E, D, F];
+// weight gradient: out [E, N, F] = dy [M, N] transposed times x [M, F], group by group.
+struct LinearArgs {
+    int M, E, F, D, N;
+    const int32_t *offsets;   // [E + 1] or null (E = 1, all rows)
+    const int32_t *rows;      // [M] or null: the row of x at each place
+    int x_rows;
+    void *out;
+    int dtype;                // of the operands: 0 BF16, 1 FP16
+    int out_fp32, accumulate; // weight gradient
+    unsigned *err;
+};
+enum LinearMode { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
+
 // dtype: 0 BF16, 1 FP16, 2 FP32.  fmt: 0 NVFP4, 1 MXFP4.
 cudaError_t launch_route(const RouteArgs &, int dtype, bool pdl, cudaStream_t);
 cudaError_t launch_route_backward(const RouteBackwardArgs &, int dtype, bool pdl, cudaStream_t);
@@ -88,6 +103,11 @@ cudaError_t launch_quantize(const QuantArgs &, int dtype, int fmt, int sms, bool
 cudaError_t launch_dequantize(const QuantArgs &, int dtype, int fmt, int sms, bool pdl, cudaStream_t);
 cudaError_t launch_product(const ProductArgs &, const uint8_t *a, const uint8_t *w, int fmt, int sms,
                            bool pdl, cudaStream_t);
+
+// x: the rows operand (x, or dy), ld elements between rows; w: the weights, or for the
+// weight gradient dy, w_ld elements between rows.
+cudaError_t launch_linear(const LinearArgs &, LinearMode mode, const void *x, long long ld, const void *w, long long w_ld,
+                          int sms, bool pdl, cudaStream_t);
 
 // A kernel's attributes, set once per device: dynamic shared memory of up to
 // `bytes`, and clusters of more than 8 CTAs if `wide`.

@@ -94,6 +94,45 @@ bn_status check_fp4(int fmt, int M, int K, int groups, const int32_t *offsets)
     return BN_OK;
 }
 
+// What the three products of a linear layer share.
+bn_status check_linear(int dtype, int M, int E, int N, int K, const int32_t *offsets)
+{
+    BN_TRY(check_dtype(dtype, false));
+    BN_REQUIRE(M >= 0, "M=%d is negative", M);
+    BN_REQUIRE(E >= 1, "E=%d is not positive", E);
+    BN_REQUIRE(N >= 8 && N % 8 == 0, "N=%d is not a positive multiple of 8", N);
+    BN_REQUIRE(K >= 8 && K % 8 == 0, "K=%d is not a positive multiple of 8", K);
+    BN_REQUIRE(offsets || E == 1, "offsets is NULL with E=%d experts", E);
+    BN_REQUIRE(aligned(offsets, 4), "offsets is not 4-byte aligned");
+    if (E > kMaxExperts) return fail(BN_ERR_UNSUPPORTED, "E=%d above the served maximum %d", E, kMaxExperts);
+    if (M > kMaxRows) return fail(BN_ERR_UNSUPPORTED, "M=%d above the served maximum %lld", M, kMaxRows);
+    if (N > (1 << 20) || K > (1 << 20))
+        return fail(BN_ERR_UNSUPPORTED, "N=%d, K=%d: above the served maximum %d", N, K, 1 << 20);
+    return BN_OK;
+}
+
+bn_status check_rows(const void *p, const char *name, long long ld, int width)
+{
+    BN_REQUIRE(ld >= width && ld % 8 == 0, "%s: ld=%lld is not a multiple of 8 of at least %d", name, ld, width);
+    if (ld > (1LL << 36)) return fail(BN_ERR_UNSUPPORTED, "%s: ld=%lld above the served maximum", name, ld);
+    return check_ptr16(p, name);
+}
+
+LinearArgs linear_args(int dtype, int M, int E, int F, int D, int N, const int32_t *offsets, void *out, unsigned *err)
+{
+    LinearArgs a = {};
+    a.M = M;
+    a.E = E;
+    a.F = F;
+    a.D = D;
+    a.N = N;
+    a.offsets = offsets;
+    a.out = out;
+    a.dtype = dtype;
+    a.err = err;
+    return a;
+}
+
 bn_status launched(cudaError_t e, const char *what)
 {
     if (e == cudaSuccess) return BN_OK;
@@ -379,6 +418,92 @@ bn_status bn_expert_product(const uint8_t *a, const uint8_t *a_scales, int M, co
     p.err = d->err;
     return launched(launch_product(p, a, w, format, d->sms, dependent_launch(), (cudaStream_t)stream),
                     "launching expert_product");
+}
+
+bn_status bn_expert_linear(const void *x, bn_dtype dtype, long long ld, int x_rows, const int32_t *rows, int M,
+                           const void *w, int E, int N, int K, const int32_t *offsets, void *y, void *stream)
+{
+    clear_message();
+    BN_TRY(check_linear(dtype, M, E, N, K, offsets));
+    BN_REQUIRE(x_rows >= 0, "x_rows=%d is negative", x_rows);
+    BN_REQUIRE(rows || x_rows == M, "x has %d rows, M=%d are wanted and no rows are given", x_rows, M);
+    if (M == 0) return BN_OK;
+    BN_REQUIRE(x_rows > 0, "x has no rows");
+    BN_REQUIRE(aligned(rows, 4), "rows is not 4-byte aligned");
+    BN_TRY(check_rows(x, "x", ld, K));
+    BN_TRY(check_ptr16(w, "w"));
+    BN_TRY(check_ptr16(y, "y"));
+    const Range writes[] = {{y, (size_t)M * N * 2, "y"}};
+    const Range reads[] = {{x, span(x_rows, ld, K, 2), "x"},
+                           {rows, (size_t)M * 4, "rows"},
+                           {w, (size_t)E * N * K * 2, "w"},
+                           {offsets, (size_t)(E + 1) * 4, "offsets"}};
+    BN_TRY(check_overlaps(writes, 1, reads, 4));
+    const DeviceInfo *d = nullptr;
+    BN_TRY(device_info(&d));
+    LinearArgs a = linear_args(dtype, M, E, N, K, 0, offsets, y, d->err);
+    a.rows = rows;
+    a.x_rows = x_rows;
+    return launched(launch_linear(a, kForward, x, ld, w, 0, d->sms, dependent_launch(), (cudaStream_t)stream),
+                    "launching expert_linear");
+}
+
+bn_status bn_expert_linear_dx(const void *dy, bn_dtype dtype, long long ld_dy, int M, const void *w, int E, int N, int K,
+                              const int32_t *offsets, void *dx, void *stream)
+{
+    clear_message();
+    BN_TRY(check_linear(dtype, M, E, N, K, offsets));
+    if (M == 0) return BN_OK;
+    BN_TRY(check_rows(dy, "dy", ld_dy, N));
+    BN_TRY(check_ptr16(w, "w"));
+    BN_TRY(check_ptr16(dx, "dx"));
+    const Range writes[] = {{dx, (size_t)M * K * 2, "dx"}};
+    const Range reads[] = {{dy, span(M, ld_dy, N, 2), "dy"},
+                           {w, (size_t)E * N * K * 2, "w"},
+                           {offsets, (size_t)(E + 1) * 4, "offsets"}};
+    BN_TRY(check_overlaps(writes, 1, reads, 3));
+    const DeviceInfo *d = nullptr;
+    BN_TRY(device_info(&d));
+    const LinearArgs a = linear_args(dtype, M, E, K, N, 0, offsets, dx, d->err);
+    return launched(launch_linear(a, kInputGrad, dy, ld_dy, w, 0, d->sms, dependent_launch(), (cudaStream_t)stream),
+                    "launching expert_linear_dx");
+}
+
+bn_status bn_expert_linear_dw(const void *dy, bn_dtype dtype, long long ld_dy, int M, const void *x, long long ld,
+                              int x_rows, const int32_t *rows, int E, int N, int K, const int32_t *offsets, void *dw,
+                              bn_dtype dw_dtype, int accumulate, void *stream)
+{
+    clear_message();
+    BN_TRY(check_linear(dtype, M, E, N, K, offsets));
+    BN_REQUIRE(dw_dtype == dtype || dw_dtype == BN_FP32, "dw_dtype %d is neither dtype nor BN_FP32", (int)dw_dtype);
+    BN_REQUIRE(!accumulate || dw_dtype == BN_FP32, "accumulate takes BN_FP32 gradients");
+    BN_REQUIRE(x_rows >= 0, "x_rows=%d is negative", x_rows);
+    BN_REQUIRE(rows || x_rows == M, "x has %d rows, M=%d are wanted and no rows are given", x_rows, M);
+    BN_TRY(check_ptr16(dw, "dw"));
+    const size_t bytes = (size_t)E * N * K * dtype_size(dw_dtype);
+    if (M == 0) {  // every group is empty
+        if (accumulate) return BN_OK;
+        return launched(cudaMemsetAsync(dw, 0, bytes, (cudaStream_t)stream), "clearing dw");
+    }
+    BN_REQUIRE(x_rows > 0, "x has no rows");
+    BN_REQUIRE(aligned(rows, 4), "rows is not 4-byte aligned");
+    BN_TRY(check_rows(dy, "dy", ld_dy, N));
+    BN_TRY(check_rows(x, "x", ld, K));
+    const Range writes[] = {{dw, bytes, "dw"}};
+    const Range reads[] = {{dy, span(M, ld_dy, N, 2), "dy"},
+                           {x, span(x_rows, ld, K, 2), "x"},
+                           {rows, (size_t)M * 4, "rows"},
+                           {offsets, (size_t)(E + 1) * 4, "offsets"}};
+    BN_TRY(check_overlaps(writes, 1, reads, 4));
+    const DeviceInfo *d = nullptr;
+    BN_TRY(device_info(&d));
+    LinearArgs a = linear_args(dtype, M, E, K, 0, N, offsets, dw, d->err);
+    a.rows = rows;
+    a.x_rows = x_rows;
+    a.out_fp32 = dw_dtype == BN_FP32;
+    a.accumulate = accumulate != 0;
+    return launched(launch_linear(a, kWeightGrad, x, ld, dy, ld_dy, d->sms, dependent_launch(), (cudaStream_t)stream),
+                    "launching expert_linear_dw");
 }
 
 }  // extern "C"

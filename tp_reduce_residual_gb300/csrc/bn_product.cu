@@ -28,13 +28,10 @@
 // burst (5.6 PFLOP/s, tensor pipe 64 % active), 282 under the power cap at
 // 1.5 GHz.  In SM cycles: products alone 362 thousand, with scale copies 377, with
 // loads 428; tiles of 384 rows and weights prefetched into L2 were not faster.
-#include <mutex>
-
-#include <cuda.h>
-
 #include "../../include/beamnorm.h"
 #include "bn_device.cuh"
 #include "bn_experts.h"
+#include "bn_tensor.cuh"
 
 namespace bn {
 
@@ -42,7 +39,6 @@ using namespace dev;
 
 namespace {
 
-constexpr unsigned kAll = 0xffffffffu;
 constexpr int kHalf = 128;              // features, and at most rows, that one CTA loads for a tile
 constexpr int kTileBytes = 128;         // codes of a stage: 256 values of K
 constexpr int kBoxRows = 32;            // rows of the smaller TMA box of the row operand
@@ -66,106 +62,13 @@ struct Shape {
     static constexpr int kScaleStride = 16 + 16 * kRowAtoms;  // tensor memory columns of a stage's scales
 };
 
-// One thread of a converged warp.  The product's and the copies' operands live in
-// uniform registers; behind elect.sync the compiler knows that one thread runs.
-__device__ __forceinline__ bool elect_one()
-{
-    uint32_t e;
-    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(e));
-    return e != 0;
-}
-
 struct Maps {
     CUtensorMap a, a_small, w;   // codes: boxes of 128 (a_small: 32) rows by 128 bytes
     CUtensorMap a_scales, w_scales;  // scale tiles: boxes of a stage's chunks of 512 bytes of so many row tiles
 };
 
-struct Tile {
-    int e, f, row0, rows, stile;
-};
-
-// The output tiles in order: experts one after another; of one expert, the row
-// tiles of a feature tile next to each other, so that CTAs that run together
-// share its weights in L2.  Every unit (a CTA or a pair) takes every step-th
-// tile.  Called by whole warps: a warp keeps its place among the experts and the
-// lanes look at the next 32 together, because the issuing warp has nothing in
-// flight while it looks for its next tile.
-template <int TILE>
-class Tiles {
-public:
-    __device__ Tiles(const int *start, const int *cum, int E, unsigned tiles_f, unsigned first, unsigned step)
-        : start_(start), cum_(cum), E_(E), e_(0), tiles_f_(tiles_f), step_(step), id_(first),
-          total_((unsigned long long)(unsigned)cum[E] * tiles_f)
-    {
-    }
-    // The next tile, or false past the last one.
-    __device__ __forceinline__ bool next(Tile &t, int lane)
-    {
-        if (id_ >= total_) return false;
-        // row tiles before this tile: 32-bit arithmetic where the tile numbers fit
-        const unsigned tt = total_ >> 32 ? (unsigned)(id_ / tiles_f_) : (unsigned)id_ / tiles_f_;
-        unsigned past;
-        do {  // experts that end at or before it
-            const int e = e_ + 1 + lane;
-            past = __popc(__ballot_sync(kAll, e <= E_ && (unsigned)cum_[min(e, E_)] <= tt));
-            e_ += (int)past;
-        } while (past == 32);
-        const unsigned c = (unsigned)cum_[e_], nt = (unsigned)cum_[e_ + 1] - c;
-        const unsigned local = (unsigned)(id_ - (unsigned long long)c * tiles_f_);
-        const int s0 = start_[e_], s1 = start_[e_ + 1];
-        t.e = e_;
-        t.f = nt == 1 ? (int)local : (int)(local / nt);
-        const int r = (int)(local - (unsigned)t.f * nt);
-        t.row0 = s0 + r * TILE;
-        t.rows = min(TILE, s1 - t.row0);
-        t.stile = (s0 >> 7) + e_ + r * (TILE / 128);
-        id_ += step_;
-        return true;
-    }
-
-private:
-    const int *start_, *cum_;
-    int E_, e_;
-    unsigned tiles_f_, step_;
-    unsigned long long id_, total_;
-};
-
-// A box into this CTA's shared memory; its bytes count on `bar`, which for a
-// pair is the first CTA's.
-template <bool PAIR>
-__device__ __forceinline__ void tma_2d(uint32_t dst, const CUtensorMap *map, int x, int y, uint32_t bar)
-{
-    if constexpr (PAIR)
-        asm volatile(
-            "cp.async.bulk.tensor.2d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3}], [%4];" ::"r"(dst), "l"(map), "r"(x), "r"(y), "r"(bar) : "memory");
-}
-
-// The same of three dimensions, from (0, y, z).
-template <bool PAIR>
-__device__ __forceinline__ void tma_3d(uint32_t dst, const CUtensorMap *map, int y, int z, uint32_t bar)
-{
-    if constexpr (PAIR)
-        asm volatile(
-            "cp.async.bulk.tensor.3d.cta_group::2.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar) : "memory");
-    else
-        asm volatile(
-            "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes "
-            "[%0], [%1, {%2, %3, %4}], [%5];" ::"r"(dst), "l"(map), "r"(0), "r"(y), "r"(z), "r"(bar) : "memory");
-}
-
-// Shared-memory operand descriptors.  Codes: rows of 128 bytes, 128-byte
-// swizzle, 8 rows apart by 1024 bytes.  Scales: 32 rows of 16 bytes, no
-// swizzle, 8 rows apart by 128 bytes.
-__device__ __forceinline__ uint64_t codes_desc(uint32_t addr)
-{
-    return (uint64_t)((addr & 0x3ffffu) >> 4) | (1ull << 16) | (64ull << 32) | (1ull << 46) | (2ull << 61);
-}
+// Shared-memory operand descriptor of scales: 32 rows of 16 bytes, no swizzle, 8
+// rows apart by 128 bytes.
 __device__ __forceinline__ uint64_t scales_desc(uint32_t addr)
 {
     return (uint64_t)((addr & 0x3ffffu) >> 4) | (1ull << 16) | (8ull << 32) | (1ull << 46);
@@ -198,71 +101,6 @@ __device__ __forceinline__ void product(uint32_t d, uint64_t a, uint64_t b, uint
     else BN_PRODUCT("1", "4X");
 }
 #undef BN_PRODUCT
-
-// Arrive on `bar` (of both CTAs of a pair) when every product so far has ended.
-template <bool PAIR>
-__device__ __forceinline__ void commit(uint32_t bar)
-{
-    if constexpr (PAIR)
-        asm volatile(
-            "tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(bar),
-            "h"((uint16_t)3) : "memory");
-    else
-        asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-}
-// The same on this CTA's barrier alone.
-template <bool PAIR>
-__device__ __forceinline__ void commit_here(uint32_t bar)
-{
-    if constexpr (PAIR)
-        asm volatile("tcgen05.commit.cta_group::2.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(bar) : "memory");
-    else
-        commit<false>(bar);
-}
-__device__ __forceinline__ void fence_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
-__device__ __forceinline__ void fence_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
-
-// Arrive on a barrier of the pair's first CTA.  What it orders are reads of tensor
-// memory, which the tcgen05 fences cover; a release at cluster scope would wait for
-// the CTA's stores in flight (1350 cycles measured).
-__device__ __forceinline__ void arrive_first(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.shared::cluster.b64 _, [%0];" ::"r"(mapa(bar, 0)) : "memory");
-}
-
-__device__ __forceinline__ void read16(uint32_t tmem, uint32_t *v)
-{
-    asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-        "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
-        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
-          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15])
-        : "r"(tmem) : "memory");
-}
-
-// Each lane of eight holds eight rows of its own feature (two a word); after it,
-// lane i holds the eight features of row i.
-__device__ __forceinline__ uint4 transpose8(const uint32_t *w, int lane)
-{
-    uint32_t a[4];
-#pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const uint32_t o = __shfl_xor_sync(kAll, w[i], 1);
-        a[i] = lane & 1 ? __byte_perm(o, w[i], 0x7632) : __byte_perm(w[i], o, 0x5410);
-    }
-    uint32_t b[2][2];
-#pragma unroll
-    for (int i = 0; i < 2; ++i) {
-        const uint32_t keep = lane & 2 ? a[2 * i + 1] : a[2 * i];
-        const uint32_t o = __shfl_xor_sync(kAll, lane & 2 ? a[2 * i] : a[2 * i + 1], 2);
-        b[i][0] = lane & 2 ? o : keep;
-        b[i][1] = lane & 2 ? keep : o;
-    }
-    const uint32_t o0 = __shfl_xor_sync(kAll, lane & 4 ? b[0][0] : b[1][0], 4);
-    const uint32_t o1 = __shfl_xor_sync(kAll, lane & 4 ? b[0][1] : b[1][1], 4);
-    return lane & 4 ? make_uint4(o0, o1, b[1][0], b[1][1]) : make_uint4(b[0][0], b[0][1], o0, o1);
-}
 
 template <bool MX, bool PAIR>
 __global__ void __launch_bounds__(Shape<PAIR>::kThreads, 1)
@@ -304,47 +142,10 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
         fence_mbarrier_init();
     }
     if (warp == 2) {
-        if constexpr (PAIR) {
-            asm volatile("tcgen05.alloc.cta_group::2.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
-                         "r"(kTmemColumns) : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::2.sync.aligned;");
-        } else {
-            asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], %1;" ::"r"(smem_addr(&tmem_slot)),
-                         "r"(kTmemColumns) : "memory");
-            asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
-        }
+        tmem_alloc<PAIR>(smem_addr(&tmem_slot), kTmemColumns);
     }
     griddep_wait();
-    // the groups' first rows and the row tiles before each group
-    for (int e = threadIdx.x; e <= p.E; e += S::kThreads) {
-        const int o = p.offsets ? __ldg(p.offsets + e) : e * p.M;
-        if (o < 0 || o > p.M) atomicOr(p.err, BN_DEVERR_OFFSETS);
-        start[e] = min(max(o, 0), p.M);
-    }
-    __syncthreads();
-    if (warp == 0) {  // a lane takes its share of consecutive groups
-        const int share = (p.E + 31) / 32, e0 = min(lane * share, p.E), e1 = min(e0 + share, p.E);
-        const auto tiles_of = [&](int e) { return (max(start[e + 1] - start[e], 0) + kTile - 1) / kTile; };
-        int n = 0;
-        bool falls = false;  // a falling offset: an empty group
-        for (int e = e0; e < e1; ++e) {
-            n += tiles_of(e);
-            falls |= start[e + 1] < start[e];
-        }
-        if (falls) atomicOr(p.err, BN_DEVERR_OFFSETS);
-        int before = n;
-#pragma unroll
-        for (int o = 1; o < 32; o <<= 1) {
-            const int v = __shfl_up_sync(kAll, before, o);
-            if (lane >= o) before += v;
-        }
-        before -= n;
-        for (int e = e0; e < e1; ++e) {
-            cum[e] = before;
-            before += tiles_of(e);
-        }
-        if (lane == 31) cum[p.E] = before;
-    }
+    group_tiles<kTile>(p.offsets, p.M, p.E, S::kThreads, start, cum, p.err);
     fence_before();
     __syncthreads();
     if constexpr (PAIR) cluster_sync_all();  // the pair's barriers are ready
@@ -392,9 +193,9 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                         tma_2d<PAIR>(at + S::kOffB, &maps.a, x, b0, bar);
                     for (int b = 0; b < boxes; ++b)
                         tma_2d<PAIR>(at + S::kOffB + b * kBoxRows * kTileBytes, &maps.a_small, x, b0 + b * kBoxRows, bar);
-                    tma_3d<PAIR>(at + S::kOffSA, &maps.w_scales, c, sw, bar);
+                    tma_3d<PAIR>(at + S::kOffSA, &maps.w_scales, 0, c, sw, bar);
                     // scale tiles past the group's rows are fetched too and not used
-                    tma_3d<PAIR>(at + S::kOffSB, &maps.a_scales, c, t.stile, bar);
+                    tma_3d<PAIR>(at + S::kOffSB, &maps.a_scales, 0, c, t.stile, bar);
                 }
             }
         }
@@ -431,7 +232,7 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
                     fence_after();
                     const uint32_t at = base + s * S::kStageBytes;
                     const uint32_t sa = tmem + kScaleColumn + (it & 1u) * S::kScaleStride, sb = sa + 16u;
-                    const uint64_t da = codes_desc(at), db = codes_desc(at + S::kOffB);
+                    const uint64_t da = rows_desc(at), db = rows_desc(at + S::kOffB);
                     const uint64_t dsa = scales_desc(at + S::kOffSA), dsb = scales_desc(at + S::kOffSB);
                     auto scales = [&](int c) {
                         copy_scales<PAIR>(sa + 4 * c, dsa + 32 * c);
@@ -535,37 +336,8 @@ product_kernel(const __grid_constant__ Maps maps, const __grid_constant__ Produc
     if constexpr (PAIR) cluster_sync_all();  // the pair's products read both CTAs' shared memory
     if (warp == 2) {
         fence_after();
-        if constexpr (PAIR)
-            asm volatile("tcgen05.dealloc.cta_group::2.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns));
-        else
-            asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, %1;" ::"r"(tmem), "r"(kTmemColumns));
+        tmem_free<PAIR>(tmem, kTmemColumns);
     }
-}
-
-using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,
-                              const cuuint64_t *, const cuuint32_t *, const cuuint32_t *, CUtensorMapInterleave,
-                              CUtensorMapSwizzle, CUtensorMapL2promotion, CUtensorMapFloatOOBfill);
-
-EncodeFn g_encode;
-cudaError_t g_encode_status = cudaErrorUnknown;
-std::once_flag g_encode_once;
-
-// `dims` elements of `size` bytes, densely, in boxes.
-template <int RANK>
-cudaError_t make_map(CUtensorMap *map, CUtensorMapDataType type, int size, const void *data, const cuuint64_t (&dims)[RANK],
-                     const cuuint32_t (&box)[RANK], CUtensorMapSwizzle swizzle)
-{
-    cuuint64_t strides[RANK - 1], bytes = (cuuint64_t)size;
-    cuuint32_t ones[RANK];
-    for (int i = 0; i < RANK; ++i) {
-        bytes *= dims[i];
-        if (i < RANK - 1) strides[i] = bytes;
-        ones[i] = 1;
-    }
-    const CUresult r = g_encode(map, type, RANK, const_cast<void *>(data), dims, strides, box, ones,
-                                CU_TENSOR_MAP_INTERLEAVE_NONE, swizzle, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                                CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
 }
 
 cudaError_t make_maps(Maps *m, const ProductArgs &p, const uint8_t *a, const uint8_t *w, int fmt, int row_atoms)
@@ -624,15 +396,8 @@ bool take_pairs(const ProductArgs &p, int sms)
 cudaError_t launch_product(const ProductArgs &p, const uint8_t *a, const uint8_t *w, int fmt, int sms, bool pdl,
                            cudaStream_t st)
 {
-    std::call_once(g_encode_once, []() {
-        void *fn = nullptr;
-        cudaDriverEntryPointQueryResult q = cudaDriverEntryPointSymbolNotFound;
-        g_encode_status = cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &fn, 12000, cudaEnableDefault, &q);
-        if (g_encode_status == cudaSuccess && (q != cudaDriverEntryPointSuccess || !fn))
-            g_encode_status = cudaErrorNotSupported;
-        g_encode = reinterpret_cast<EncodeFn>(fn);
-    });
-    if (g_encode_status != cudaSuccess) return g_encode_status;
+    const cudaError_t ready = tensor_maps_ready();
+    if (ready != cudaSuccess) return ready;
     const bool pair = take_pairs(p, sms);
     Maps maps;
     const cudaError_t e = make_maps(&maps, p, a, w, fmt, pair ? Shape<true>::kRowAtoms : Shape<false>::kRowAtoms);

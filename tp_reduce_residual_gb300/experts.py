@@ -312,3 +312,100 @@ def expert_product(a: FP4, w: FP4, scale: float = 1.0, out=None, stream=None) ->
     _call("bn_expert_product", (ap, sp, M, wp, wsp, E, N, K, op, FORMATS[a.format], scale * a.tensor_scale * w.tensor_scale, yp),
           dev.index, stream)
     return out
+
+
+def _groups(offsets, E, dev):
+    """The address of the groups' offsets of E experts, or None where one expert has every row."""
+    if offsets is None:
+        if E != 1:
+            raise ValueError(f"offsets are required with {E} experts")
+        return None
+    return _ptr(offsets, "offsets", _INT32, (E + 1,), dev)
+
+
+def _weights(w, dtype, dev):
+    """(E, N, K) and the address of the experts' weights [E,N,K], or [N,K]: one expert."""
+    if not isinstance(w, torch.Tensor) or w.dim() not in (2, 3):
+        raise ValueError("w must be a tensor [experts, N, K] or [N, K]")
+    shape = w.shape
+    E, N, K = shape if len(shape) == 3 else (1, *shape)
+    return E, N, K, _ptr(w, "w", dtype, shape, dev)
+
+
+def _places(x, rows):
+    """M and the address of ``rows``: the rows of x, or one for every entry of ``rows``."""
+    if rows is None:
+        return x.shape[0], None
+    return rows.numel(), _ptr(rows, "rows", _INT32, (rows.numel(),), x.device)
+
+
+def _stride(t, name):
+    """The row stride of a 2-D tensor for the kernels that copy rows in 16-byte pieces."""
+    ld = _rows2d(t, name)
+    return ld if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+
+
+def expert_linear(x, w, offsets=None, rows=None, out=None, stream=None) -> torch.Tensor:
+    """The experts' linear layer in 16 bits: out [M,N], each row of ``x`` ([n,K] BF16 or
+    FP16, any row stride that is a multiple of 8) times its group's weights of ``w``
+    ([E,N,K]; [N,K] is one expert), summed in FP32.  ``offsets`` (int32 [E+1]) are the
+    groups, ``rows`` (int32 [M]) the row of x at each place, as ``plan`` gives them;
+    without ``rows`` x is grouped already.  Rows of no group are zeros."""
+    ld = _stride(x, "x")
+    dev = x.device
+    dtype = _dtype(x, "x", fp32=False)
+    M, rp = _places(x, rows)
+    E, N, K, wp = _weights(w, x.dtype, dev)
+    if x.shape[1] != K:
+        raise ValueError(f"x has rows of {x.shape[1]} values, w of {K}")
+    op = _groups(offsets, E, dev)
+    out, yp = _out(out, "out", x.dtype, (M, N), dev, stream)
+    _call("bn_expert_linear", (x.data_ptr(), dtype, ld, x.shape[0], rp, M, wp, E, N, K, op, yp), dev.index, stream)
+    return out
+
+
+def expert_linear_dx(dy, w, offsets=None, dx=None, stream=None) -> torch.Tensor:
+    """Gradient of ``expert_linear`` with respect to the grouped rows: dx [M,K] from ``dy``
+    [M,N].  Where ``rows`` took a row several times, its gradient is the sum over its
+    places: ``beamnorm.finalize_only`` with the plan's perm and weights of 1."""
+    ld = _stride(dy, "dy")
+    dev = dy.device
+    dtype = _dtype(dy, "dy", fp32=False)
+    M = dy.shape[0]
+    E, N, K, wp = _weights(w, dy.dtype, dev)
+    if dy.shape[1] != N:
+        raise ValueError(f"dy has rows of {dy.shape[1]} values, w has {N} rows")
+    op = _groups(offsets, E, dev)
+    dx, xp = _out(dx, "dx", dy.dtype, (M, K), dev, stream)
+    _call("bn_expert_linear_dx", (dy.data_ptr(), dtype, ld, M, wp, E, N, K, op, xp), dev.index, stream)
+    return dx
+
+
+def expert_linear_dw(dy, x, offsets=None, rows=None, dtype=None, dw=None, accumulate: bool = False, stream=None) -> torch.Tensor:
+    """Gradient of ``expert_linear`` with respect to the weights: dw [E,N,K] from ``dy``
+    [M,N] and the layer's ``x`` and ``rows``, in x's dtype or FP32 (``dtype``, or that of
+    ``dw``).  ``accumulate`` adds to what an FP32 ``dw`` holds.  Without ``offsets`` there
+    is one expert and dw is [N,K]."""
+    ld_dy = _stride(dy, "dy")
+    ld = _stride(x, "x")
+    dev = dy.device
+    d = _dtype(dy, "dy", fp32=False)
+    if x.device != dev or x.dtype is not dy.dtype:
+        raise ValueError(f"x ({x.dtype} on {x.device}) must be as dy ({dy.dtype} on {dev})")
+    M, rp = _places(x, rows)
+    if dy.shape[0] != M:
+        raise ValueError(f"dy has {dy.shape[0]} rows, expected {M}")
+    E = 1 if offsets is None else offsets.numel() - 1
+    if E < 1:
+        raise ValueError("offsets must have 2 entries or more")
+    op = _groups(offsets, E, dev)
+    N, K = dy.shape[1], x.shape[1]
+    if accumulate and dw is None:
+        raise ValueError("accumulate adds to a dw that is given")
+    want = dw.dtype if isinstance(dw, torch.Tensor) else x.dtype if dtype is None else dtype
+    if want not in (x.dtype, _FLOAT32) or (dtype is not None and dtype is not want):
+        raise TypeError(f"dw must be {x.dtype} or torch.float32 (got {dtype or want})")
+    dw, wp = _out(dw, "dw", want, (N, K) if offsets is None else (E, N, K), dev, stream)
+    _call("bn_expert_linear_dw", (dy.data_ptr(), d, ld_dy, M, x.data_ptr(), ld, x.shape[0], rp, E, N, K, op, wp, _DTYPES[want],
+                                  1 if accumulate else 0), dev.index, stream)
+    return dw
