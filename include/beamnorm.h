@@ -429,6 +429,12 @@ BN_API bn_status bn_expert_product(const uint8_t *a, const uint8_t *a_scales, in
                                    const int32_t *offsets, bn_fp4 format, float alpha,
                                    uint16_t *out, void *stream);
 
+/* Bytes of workspace with which bn_expert_linear and bn_expert_linear_dw bring the rows
+ * of x to their M places before the product, or 0 where the product fetches them as
+ * fast itself (M <= 32).  Pure host logic.
+ * Source: no passage: library utility. */
+BN_API size_t bn_expert_linear_workspace_bytes(int M, int K);
+
 /* The experts' linear layers in 16 bits, for training and for weights that are not
  * quantised: the rows m of group e (offsets[e] <= m < offsets[e + 1]) with its weights.
  *   bn_expert_linear     y[m, n]     = sum over k of x[rows[m], k] * w[e, n, k]
@@ -445,10 +451,15 @@ BN_API bn_status bn_expert_product(const uint8_t *a, const uint8_t *a_scales, in
  * Rows of y and dx before the first offset and past the last are zeros; such rows of
  * x and dy are not read into any result.  dw of an empty group is zeros.  N and K are
  * multiples of 8.
+ *   workspace  device memory of workspace_bytes, 16-byte aligned, or NULL; used when rows
+ *            is given and it holds bn_expert_linear_workspace_bytes() (not 0), for two
+ *            kernels on `stream` instead of one: rows go to their places there first.
+ *            Nothing in it is kept; the results are the same, several times slower without
  * Source: none -- the pages take the experts' rows as given; it has no counterpart there. */
 BN_API bn_status bn_expert_linear(const void *x, bn_dtype dtype, long long ld, int x_rows,
                                   const int32_t *rows, int M, const void *w, int E, int N, int K,
-                                  const int32_t *offsets, void *y, void *stream);
+                                  const int32_t *offsets, void *y, void *workspace,
+                                  size_t workspace_bytes, void *stream);
 
 /* dx of bn_expert_linear, a row for every place (of rows that several places take, the
  * gradients are the sum: bn_finalize_only with weights of 1 adds them up).
@@ -464,7 +475,8 @@ BN_API bn_status bn_expert_linear_dx(const void *dy, bn_dtype dtype, long long l
 BN_API bn_status bn_expert_linear_dw(const void *dy, bn_dtype dtype, long long ld_dy, int M,
                                      const void *x, long long ld, int x_rows, const int32_t *rows,
                                      int E, int N, int K, const int32_t *offsets, void *dw,
-                                     bn_dtype dw_dtype, int accumulate, void *stream);
+                                     bn_dtype dw_dtype, int accumulate, void *workspace,
+                                     size_t workspace_bytes, void *stream);
 
 /* ---- queries and errors ------------------------------------------------ */
 

@@ -202,3 +202,30 @@ def test_no_rows():
     dw = torch.full((3, 16, 24), 2.0, device="cuda")
     experts.expert_linear_dw(dy, x, o, dw=dw, accumulate=True)
     assert (dw == 2).all()
+
+
+@pytest.mark.parametrize("M", [32, 33, 300])
+def test_rows_with_and_without_a_workspace(M):
+    """The product fetches rows itself where it gets no workspace, or one that is too small."""
+    d = make([M // 3, 0, M - M // 3], 136, 264, "bf16", gather=True, before=2)
+    y, _, dw = exact(d)
+    n = experts.linear_workspace_bytes(M + 2, 264)
+    assert n == (0 if M + 2 <= 32 else (M + 2) * 264 * 2)
+    for size in (16, n, n + 160):
+        ws = torch.full((max(size, 16),), 255, dtype=torch.uint8, device="cuda")
+        assert torch.equal(experts.expert_linear(d["x"], d["w"], d["offsets"], rows=d["rows"], workspace=ws), y.bfloat16())
+        assert torch.equal(experts.expert_linear_dw(d["dy"], d["x"], d["offsets"], rows=d["rows"], workspace=ws), dw.bfloat16())
+        if size == 16:
+            assert (ws == 255).all()
+
+
+@pytest.mark.parametrize("gather", [False, True])
+@pytest.mark.parametrize("sizes,N,K", [([1], 64, 8192), ([0, 7, 0, 9], 512, 4096), ([16], 2048, 3000), ([40], 128, 2056), ([64], 4096, 2048),
+                                       ([1, 1, 1, 1, 1, 1, 1, 1, 1, 1], 512, 2048), ([70], 128, 4104)])
+def test_split_sums(sizes, N, K, gather):
+    """Few tiles and a long sum: clusters of CTAs that each sum a part, by 2 to 8."""
+    d = make(sizes, N, K, "bf16", gather=gather, seed=3, after=1)
+    check(d, whole=True)
+    t = dict(d, w=d["w"].transpose(1, 2).contiguous(), x=d["dy"], dy=d["x"] if not gather else d["x"][d["rows"].long()], rows=None)
+    check(t, whole=True)
+    check(make(sizes, N, K, "fp16", whole=False, gather=gather), whole=False)

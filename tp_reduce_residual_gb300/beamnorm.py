@@ -42,6 +42,8 @@ EXPORTS = (
     "bn_route", "bn_route_backward", "bn_expert_plan", "bn_fp4_scale_bytes", "bn_quantize_fp4",
     "bn_quantize_fp4_workspace_bytes",
     "bn_dequantize_fp4", "bn_expert_product",
+    "bn_expert_linear_workspace_bytes", "bn_expert_linear", "bn_expert_linear_dx",
+    "bn_expert_linear_dw",
 )
 
 # bn_op values of the entry points, for launch_info()
@@ -139,9 +141,11 @@ def load() -> ctypes.CDLL:
             "bn_quantize_fp4_workspace_bytes": [_I, _I, _I, _I],
             "bn_dequantize_fp4": [_P, _P, _I, _I, _P, _I, _I, _F, _P, _I, _P],
             "bn_expert_product": [_P, _P, _I, _P, _P, _I, _I, _I, _P, _I, _F, _P, _P],
-            "bn_expert_linear": [_P, _I, _L, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P],
+            "bn_expert_linear_workspace_bytes": [_I, _I],
+            "bn_expert_linear": [_P, _I, _L, _I, _P, _I, _P, _I, _I, _I, _P, _P, _P, ctypes.c_size_t, _P],
             "bn_expert_linear_dx": [_P, _I, _L, _I, _P, _I, _I, _I, _P, _P, _P],
-            "bn_expert_linear_dw": [_P, _I, _L, _I, _P, _L, _I, _P, _I, _I, _I, _P, _P, _I, _I, _P],
+            "bn_expert_linear_dw": [_P, _I, _L, _I, _P, _L, _I, _P, _I, _I, _I, _P, _P, _I, _I, _P, ctypes.c_size_t,
+                                    _P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -152,6 +156,7 @@ def load() -> ctypes.CDLL:
         L.bn_finalize_workspace_bytes.restype = ctypes.c_size_t
         L.bn_fp4_scale_bytes.restype = ctypes.c_size_t
         L.bn_quantize_fp4_workspace_bytes.restype = ctypes.c_size_t
+        L.bn_expert_linear_workspace_bytes.restype = ctypes.c_size_t
         L.bn_last_error.restype = ctypes.c_char_p
         L.bn_status_string.restype = ctypes.c_char_p
         _lib = L

@@ -91,6 +91,7 @@ struct LinearArgs {
     void *out;
     int dtype;                // of the operands: 0 BF16, 1 FP16
     int out_fp32, accumulate; // weight gradient
+    int split;                // CTAs that share a tile's sum
     unsigned *err;
 };
 enum LinearMode { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
@@ -108,6 +109,10 @@ cudaError_t launch_product(const ProductArgs &, const uint8_t *a, const uint8_t 
 // weight gradient dy, w_ld elements between rows.
 cudaError_t launch_linear(const LinearArgs &, LinearMode mode, const void *x, long long ld, const void *w, long long w_ld,
                           int sms, bool pdl, cudaStream_t);
+
+// out [M, K] dense: row rows[m] of x at place m (16-bit values).
+cudaError_t launch_place_rows(const void *x, long long ld, int x_rows, const int32_t *rows, int M, int K, void *out, unsigned *err,
+                              int sms, bool pdl, cudaStream_t);
 
 // A kernel's attributes, set once per device: dynamic shared memory of up to
 // `bytes`, and clusters of more than 8 CTAs if `wide`.

@@ -1,7 +1,7 @@
 // bn_experts_abi.cu -- the C entry points around the experts: host-side
 // validation and launches.  Like the rest of the ABI, arguments are checked
 // before any CUDA call, and each call enqueues one kernel (two for a quantisation
-// with a workspace) or nothing.
+// or a linear layer with a workspace) or nothing.
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -94,6 +94,13 @@ bn_status check_fp4(int fmt, int M, int K, int groups, const int32_t *offsets)
     return BN_OK;
 }
 
+bn_status launched(cudaError_t e, const char *what)
+{
+    if (e == cudaSuccess) return BN_OK;
+    (void)cudaGetLastError();  // a failed launch leaves no error behind for the caller's next call
+    return cuda_fail(e, what);
+}
+
 // What the three products of a linear layer share.
 bn_status check_linear(int dtype, int M, int E, int N, int K, const int32_t *offsets)
 {
@@ -118,6 +125,22 @@ bn_status check_rows(const void *p, const char *name, long long ld, int width)
     return check_ptr16(p, name);
 }
 
+// With a workspace of enough bytes, rows by index go to their places there first; x, ld and the
+// arguments' rows are then those of the workspace.
+bn_status place_rows(LinearArgs &a, const void *&x, long long &ld, int K, void *workspace, size_t bytes, const DeviceInfo &d,
+                     void *stream)
+{
+    const size_t need = a.rows ? bn_expert_linear_workspace_bytes(a.M, K) : 0;
+    if (need == 0 || !workspace || bytes < need) return BN_OK;
+    BN_TRY(launched(launch_place_rows(x, ld, a.x_rows, a.rows, a.M, K, workspace, d.err, d.sms, dependent_launch(), (cudaStream_t)stream),
+                    "launching place_rows"));
+    x = workspace;
+    ld = K;
+    a.rows = nullptr;
+    a.x_rows = a.M;
+    return BN_OK;
+}
+
 LinearArgs linear_args(int dtype, int M, int E, int F, int D, int N, const int32_t *offsets, void *out, unsigned *err)
 {
     LinearArgs a = {};
@@ -131,13 +154,6 @@ LinearArgs linear_args(int dtype, int M, int E, int F, int D, int N, const int32
     a.dtype = dtype;
     a.err = err;
     return a;
-}
-
-bn_status launched(cudaError_t e, const char *what)
-{
-    if (e == cudaSuccess) return BN_OK;
-    (void)cudaGetLastError();  // a failed launch leaves no error behind for the caller's next call
-    return cuda_fail(e, what);
 }
 
 }  // namespace
@@ -420,8 +436,17 @@ bn_status bn_expert_product(const uint8_t *a, const uint8_t *a_scales, int M, co
                     "launching expert_product");
 }
 
+size_t bn_expert_linear_workspace_bytes(int M, int K)
+{
+    // Fetching a row by its index costs the copying thread about 25 cycles for every 64 values, which
+    // the stream of weights hides up to about 30 rows of a group: with no more rows than that in
+    // all, none go through the workspace.
+    return M > 32 && K >= 8 && K % 8 == 0 ? (size_t)M * K * 2 : 0;
+}
+
 bn_status bn_expert_linear(const void *x, bn_dtype dtype, long long ld, int x_rows, const int32_t *rows, int M,
-                           const void *w, int E, int N, int K, const int32_t *offsets, void *y, void *stream)
+                           const void *w, int E, int N, int K, const int32_t *offsets, void *y, void *workspace,
+                           size_t workspace_bytes, void *stream)
 {
     clear_message();
     BN_TRY(check_linear(dtype, M, E, N, K, offsets));
@@ -433,17 +458,19 @@ bn_status bn_expert_linear(const void *x, bn_dtype dtype, long long ld, int x_ro
     BN_TRY(check_rows(x, "x", ld, K));
     BN_TRY(check_ptr16(w, "w"));
     BN_TRY(check_ptr16(y, "y"));
-    const Range writes[] = {{y, (size_t)M * N * 2, "y"}};
+    BN_TRY(check_ptr16(workspace, "workspace", false));
+    const Range writes[] = {{y, (size_t)M * N * 2, "y"}, {workspace, workspace_bytes, "workspace"}};
     const Range reads[] = {{x, span(x_rows, ld, K, 2), "x"},
                            {rows, (size_t)M * 4, "rows"},
                            {w, (size_t)E * N * K * 2, "w"},
                            {offsets, (size_t)(E + 1) * 4, "offsets"}};
-    BN_TRY(check_overlaps(writes, 1, reads, 4));
+    BN_TRY(check_overlaps(writes, 2, reads, 4));
     const DeviceInfo *d = nullptr;
     BN_TRY(device_info(&d));
     LinearArgs a = linear_args(dtype, M, E, N, K, 0, offsets, y, d->err);
     a.rows = rows;
     a.x_rows = x_rows;
+    BN_TRY(place_rows(a, x, ld, K, workspace, workspace_bytes, *d, stream));
     return launched(launch_linear(a, kForward, x, ld, w, 0, d->sms, dependent_launch(), (cudaStream_t)stream),
                     "launching expert_linear");
 }
@@ -471,7 +498,7 @@ bn_status bn_expert_linear_dx(const void *dy, bn_dtype dtype, long long ld_dy, i
 
 bn_status bn_expert_linear_dw(const void *dy, bn_dtype dtype, long long ld_dy, int M, const void *x, long long ld,
                               int x_rows, const int32_t *rows, int E, int N, int K, const int32_t *offsets, void *dw,
-                              bn_dtype dw_dtype, int accumulate, void *stream)
+                              bn_dtype dw_dtype, int accumulate, void *workspace, size_t workspace_bytes, void *stream)
 {
     clear_message();
     BN_TRY(check_linear(dtype, M, E, N, K, offsets));
@@ -489,12 +516,13 @@ bn_status bn_expert_linear_dw(const void *dy, bn_dtype dtype, long long ld_dy, i
     BN_REQUIRE(aligned(rows, 4), "rows is not 4-byte aligned");
     BN_TRY(check_rows(dy, "dy", ld_dy, N));
     BN_TRY(check_rows(x, "x", ld, K));
-    const Range writes[] = {{dw, bytes, "dw"}};
+    BN_TRY(check_ptr16(workspace, "workspace", false));
+    const Range writes[] = {{dw, bytes, "dw"}, {workspace, workspace_bytes, "workspace"}};
     const Range reads[] = {{dy, span(M, ld_dy, N, 2), "dy"},
                            {x, span(x_rows, ld, K, 2), "x"},
                            {rows, (size_t)M * 4, "rows"},
                            {offsets, (size_t)(E + 1) * 4, "offsets"}};
-    BN_TRY(check_overlaps(writes, 1, reads, 4));
+    BN_TRY(check_overlaps(writes, 2, reads, 4));
     const DeviceInfo *d = nullptr;
     BN_TRY(device_info(&d));
     LinearArgs a = linear_args(dtype, M, E, K, 0, N, offsets, dw, d->err);
@@ -502,6 +530,7 @@ bn_status bn_expert_linear_dw(const void *dy, bn_dtype dtype, long long ld_dy, i
     a.x_rows = x_rows;
     a.out_fp32 = dw_dtype == BN_FP32;
     a.accumulate = accumulate != 0;
+    BN_TRY(place_rows(a, x, ld, K, workspace, workspace_bytes, *d, stream));
     return launched(launch_linear(a, kWeightGrad, x, ld, dy, ld_dy, d->sms, dependent_launch(), (cudaStream_t)stream),
                     "launching expert_linear_dw");
 }

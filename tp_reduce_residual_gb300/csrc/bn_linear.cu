@@ -34,25 +34,32 @@ namespace {
 constexpr int kHalf = 128;      // features, and at most rows, that one CTA loads for a tile
 constexpr int kDepth = 64;      // summed values of a stage: 128 bytes
 constexpr int kBoxRows = 32;    // rows of the smaller box
+constexpr int kMaxSplit = 8;    // CTAs that share a tile's sum
 constexpr int kAtom = 64 * 128; // bytes of 64 features or rows by 64 values, where the sum runs across rows
 
-template <bool PAIR>
+enum Shape { kOne = 0, kPair = 1, kSplit = 2 };
+
+template <int SHAPE>
 struct LinearShape {
-    static constexpr int kCtas = PAIR ? 2 : 1;
-    static constexpr int kTile = PAIR ? 256 : 128;  // features, and rows, of an output tile
-    static constexpr int kStep = PAIR ? 32 : 16;    // rows of a product are rounded up to this
-    static constexpr int kStages = 6;
+    static constexpr int kCtas = SHAPE == kPair ? 2 : 1;       // CTAs of one product
+    static constexpr int kTile = SHAPE == kPair ? 256 : 128;   // features of an output tile
+    static constexpr int kRows = SHAPE == kSplit ? 64 : kTile; // its rows
+    static constexpr int kStep = SHAPE == kPair ? 32 : 16;     // rows of a product are rounded up to this
+    static constexpr int kStages = SHAPE == kSplit ? 7 : 6;
     static constexpr int kOffQ = kHalf * 128;
-    static constexpr int kStageBytes = 2 * kOffQ;
-    static constexpr int kColumns = 2 * kTile;      // tensor memory: two accumulators
-    static constexpr int kOutWarps = PAIR ? 8 : 4;
+    static constexpr int kStageBytes = kOffQ + kRows / kCtas * 128;
+    static constexpr int kColumns = 2 * kRows;      // tensor memory: two accumulators
+    static constexpr int kJoinBytes = SHAPE == kSplit ? (kRows + kMaxSplit) * kHalf * 4 : 0;  // parts of a split sum
+    static constexpr int kOutWarps = SHAPE == kPair ? 8 : 4;
     static constexpr int kThreads = 64 + 32 * kOutWarps;  // copies, products, output
+    static constexpr size_t smem(int E) { return 1024 + (size_t)kStages * kStageBytes + kJoinBytes + 2 * sizeof(int) * (size_t)(E + 1); }
 };
 
 struct LinearMaps {
     CUtensorMap p;                 // the features' operand: w, or x
     CUtensorMap q, q_small;        // the rows' operand: x or dy, in boxes of 128 (64) and 32 rows
     CUtensorMap p_rows, q_rows;    // row by row: x (and dy) of the weight gradient, x of the forward
+    CUtensorMap p16, p4, q16, q4;  // the weight gradient's in boxes of 16 and 4 rows
 };
 
 // The weight gradient's tiles: experts one after another, of one expert the row tiles
@@ -115,27 +122,46 @@ __device__ __forceinline__ uint32_t round16(float a, float b, bool fp16)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <int MODE, bool PAIR, bool GATHER>
-__global__ void __launch_bounds__(LinearShape<PAIR>::kThreads, 1)
+// A value into the shared memory of a CTA of the cluster, counted on its barrier there.
+__device__ __forceinline__ void send_cluster(uint32_t addr, uint32_t v, uint32_t bar)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+template <int MODE, int SHAPE, bool GATHER>
+__global__ void __launch_bounds__(LinearShape<SHAPE>::kThreads, 1)
 linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearArgs p)
 {
-    using S = LinearShape<PAIR>;
-    constexpr int kStages = S::kStages, kTile = S::kTile;
+    using S = LinearShape<SHAPE>;
+    constexpr bool PAIR = SHAPE == kPair, SPLIT = SHAPE == kSplit;
+    constexpr int kStages = S::kStages, kTile = S::kTile, kRows = S::kRows;
     constexpr bool kWeights = MODE == kWeightGrad;
     constexpr bool kAcrossP = MODE != kForward, kAcrossQ = kWeights;
     extern __shared__ __align__(1024) uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-    __shared__ __align__(8) uint64_t bars[2 * kStages + 5];
+    __shared__ __align__(8) uint64_t bars[2 * kStages + 7];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
-    int *start = reinterpret_cast<int *>(raw + (base - smem_addr(raw)) + kStages * S::kStageBytes);
+    __shared__ int4 quads[32];  // row indexes of the copying warp
+    float *parts = reinterpret_cast<float *>(raw + (base - smem_addr(raw)) + kStages * S::kStageBytes);
+    int *start = reinterpret_cast<int *>(parts) + S::kJoinBytes / 4;
     int *cum = start + p.E + 1;
     const int warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
     // full: the copies of a stage have landed (a pair's on the first CTA's barrier);
     // empty: the products have read it
     const uint32_t full = smem_addr(bars), empty = full + 8 * kStages, acc_full = empty + 8 * kStages, acc_empty = acc_full + 16, done = acc_empty + 16;
+    // a split sum: the parts of this CTA's rows have come; the other CTAs have read theirs
+    const uint32_t joined = done + 8, joinable = joined + 8;
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
-    const int unit = (int)blockIdx.x / S::kCtas, units = (int)gridDim.x / S::kCtas;
+    // a unit: a CTA, a pair, or a cluster whose CTAs each sum a part
+    const uint32_t parts_n = SPLIT ? (uint32_t)p.split : 1u, part = SPLIT ? cluster_ctarank() : 0u;
+    const int ctas = SPLIT ? p.split : S::kCtas;
+    const int unit = (int)blockIdx.x / ctas, units = (int)gridDim.x / ctas;
 
     griddep_launch_dependents();
     if (warp == 1 && elect_one()) {
@@ -153,14 +179,18 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
             mbar_init(acc_empty + 8 * i, S::kCtas * S::kOutWarps);
         }
         mbar_init(done, 1);
+        if (SPLIT) {
+            mbar_init(joined, 1);
+            mbar_init(joinable, parts_n * S::kOutWarps);
+        }
         fence_mbarrier_init();
     }
     if (warp == 2) tmem_alloc<PAIR>(smem_addr(&tmem_slot), S::kColumns);
     griddep_wait();
-    group_tiles<kTile>(p.offsets, p.M, p.E, S::kThreads, start, cum, p.err);
+    group_tiles<kRows>(p.offsets, p.M, p.E, S::kThreads, start, cum, p.err);
     fence_before();
     __syncthreads();
-    if constexpr (PAIR) cluster_sync_all();  // the pair's barriers are ready
+    if constexpr (PAIR || SPLIT) cluster_sync_all();  // the cluster's barriers are ready
     fence_after();
     const uint32_t tmem = tmem_slot;
 
@@ -173,11 +203,17 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
         if constexpr (kWeights)
             return WeightTiles<kTile>(p.E, p.N, p.F, (unsigned)unit, (unsigned)units);
         else
-            return Tiles<kTile>(start, cum, p.E, (unsigned)((p.F + kTile - 1) / kTile), (unsigned)unit, (unsigned)units);
+            return Tiles<kRows>(start, cum, p.E, (unsigned)((p.F + kTile - 1) / kTile), (unsigned)unit, (unsigned)units);
     }();
     Tile t = {};
     // the length of a tile's sum
     const auto depth = [&]() { return kWeights ? max(start[t.e + 1] - start[t.e], 0) : p.D; };
+    // the stages of it that this CTA sums
+    const auto stages = [&](int d, int &k0, int &k1) {
+        const int nk = (d + kDepth - 1) / kDepth;
+        k0 = SPLIT ? (int)(part * (uint32_t)nk / parts_n) : 0;
+        k1 = SPLIT ? (int)((part + 1) * (uint32_t)nk / parts_n) : nk;
+    };
     const auto columns_of = [&]() { return (t.rows + S::kStep - 1) / S::kStep * S::kStep; };
 
     // The copying and the issuing warp run their loops as a whole, so that loop
@@ -191,10 +227,11 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
             // this CTA's rows of the product's N operand: all, or half of the rounded count
             const int columns = columns_of();
             const int nb = PAIR ? columns / 2 : columns, b0 = t.row0 + (PAIR ? (int)rank * nb : 0);
-            const int d = depth(), nk = (d + kDepth - 1) / kDepth;
+            const int d = depth();
+            int k0, k1;
+            stages(d, k0, k1);
             const int boxes = nb > kHalf / 2 ? 0 : (nb + kBoxRows - 1) / kBoxRows;  // 0: one of kHalf rows
             const int q_atoms = nb > 64 ? 2 : 1;
-            int4 index = {};
             if constexpr (GATHER && !kWeights) {  // four rows a lane; places past the tile read zeros
                 int v[4];
 #pragma unroll
@@ -209,9 +246,11 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                         }
                     }
                 }
-                index = make_int4(v[0], v[1], v[2], v[3]);
+                __syncwarp();
+                quads[lane] = make_int4(v[0], v[1], v[2], v[3]);
+                __syncwarp();
             }
-            for (int k = 0; k < nk; ++k, ++it) {
+            for (int k = k0; k < k1; ++k, ++it) {
                 const uint32_t s = it % kStages;
                 if constexpr (GATHER && kWeights) {  // 16 places a quad: the same indexes for both atoms
                     int v[4];
@@ -227,7 +266,9 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                             }
                         }
                     }
-                    index = make_int4(v[0], v[1], v[2], v[3]);
+                    __syncwarp();
+                    quads[lane] = make_int4(v[0], v[1], v[2], v[3]);
+                    __syncwarp();
                 }
                 ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(empty + 8 * s, ((it / kStages) & 1u) ^ 1u, ctl));
                 if (!ok) break;
@@ -248,11 +289,10 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                             if (boxes == 0) tma_2d<PAIR>(q, &maps.q, r0, b0, bar);
                             for (int b = 0; b < boxes; ++b)
                                 tma_2d<PAIR>(q + b * kBoxRows * 128, &maps.q_small, r0, b0 + b * kBoxRows, bar);
+                        } else {
+#pragma unroll 4
+                            for (int i = 0; i < nb / 4; ++i) tma_rows<PAIR>(q + i * 512, &maps.q_rows, r0, quads[i], bar);
                         }
-                    }
-                    if constexpr (GATHER) {
-                        __syncwarp();
-                        if (4 * lane < nb) tma_rows<PAIR>(q + lane * 512, &maps.q_rows, r0, index, bar);
                     }
                 } else {
                     const bool tail = r0 + kDepth > d;
@@ -269,18 +309,41 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                             tma_2d<PAIR>(q, &maps.q, b0, m0, bar);
                             if (q_atoms == 2) tma_2d<PAIR>(q + kAtom, &maps.q, b0 + 64, m0, bar);
                         }
-                    }
-                    __syncwarp();
-                    const int quad = lane & 15, atom = lane >> 4, m = 4 * quad;
-                    if (m < live && (GATHER || tail)) {
-                        int4 own;  // the places themselves
-                        own.x = r0 + m < d ? m0 + m : p.M;
-                        own.y = r0 + m + 1 < d ? m0 + m + 1 : p.M;
-                        own.z = r0 + m + 2 < d ? m0 + m + 2 : p.M;
-                        own.w = r0 + m + 3 < d ? m0 + m + 3 : p.M;
-                        tma_rows<PAIR>(at + atom * kAtom + quad * 512, &maps.p_rows, f0 + 64 * atom, GATHER ? index : own, bar);
-                        if (tail && atom < q_atoms)
-                            tma_rows<PAIR>(q + atom * kAtom + quad * 512, &maps.q_rows, b0 + 64 * atom, own, bar);
+                        if constexpr (GATHER) {
+#pragma unroll 4
+                            for (int i = 0; i < live / 4; ++i) {
+                                const int4 y = quads[i];
+                                tma_rows<PAIR>(at + i * 512, &maps.p_rows, f0, y, bar);
+                                tma_rows<PAIR>(at + kAtom + i * 512, &maps.p_rows, f0 + 64, y, bar);
+                            }
+                        }
+                        if (tail) {
+                            // 16 rows at a time while all are the group's, then 4 (past it: boxes
+                            // outside the map, zeros); four that the group's end cuts, by index
+                            const auto box = [&](const CUtensorMap *mp, const CUtensorMap *mq, int i, int y) {
+                                if (!GATHER) {
+                                    tma_2d<PAIR>(at + i * 128, mp, f0, y, bar);
+                                    tma_2d<PAIR>(at + kAtom + i * 128, mp, f0 + 64, y, bar);
+                                }
+                                tma_2d<PAIR>(q + i * 128, mq, b0, y, bar);
+                                if (q_atoms == 2) tma_2d<PAIR>(q + kAtom + i * 128, mq, b0 + 64, y, bar);
+                            };
+                            const int left = d - r0;
+                            int i = 0;
+                            for (; i + 16 <= left; i += 16) box(&maps.p16, &maps.q16, i, m0 + i);
+                            for (; i + 4 <= left; i += 4) box(&maps.p4, &maps.q4, i, m0 + i);
+                            if (i < left) {
+                                const int4 y = {m0 + i, i + 1 < left ? m0 + i + 1 : p.M, i + 2 < left ? m0 + i + 2 : p.M, p.M};
+                                if (!GATHER) {
+                                    tma_rows<PAIR>(at + i * 128, &maps.p_rows, f0, y, bar);
+                                    tma_rows<PAIR>(at + kAtom + i * 128, &maps.p_rows, f0 + 64, y, bar);
+                                }
+                                tma_rows<PAIR>(q + i * 128, &maps.q_rows, b0, y, bar);
+                                if (q_atoms == 2) tma_rows<PAIR>(q + kAtom + i * 128, &maps.q_rows, b0 + 64, y, bar);
+                                i += 4;
+                            }
+                            for (; i < live; i += 4) box(&maps.p4, &maps.q4, i, p.M);
+                        }
                     }
                 }
             }
@@ -309,9 +372,11 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 const uint32_t type = p.dtype == BN_BF16 ? 1u : 0u;
                 const uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | ((kAcrossP ? 1u : 0u) << 15) |
                                        ((kAcrossQ ? 1u : 0u) << 16) | (((uint32_t)columns_of() >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
-                const uint32_t acc = tmem + buf * kTile;
-                const int d = depth(), nk = (d + kDepth - 1) / kDepth;
-                for (int k = 0; k < nk; ++k, ++it) {
+                const uint32_t acc = tmem + buf * kRows;
+                const int d = depth();
+                int k0, k1;
+                stages(d, k0, k1);
+                for (int k = k0; k < k1; ++k, ++it) {
                     const uint32_t s = it % kStages;
                     ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(full + 8 * s, (it / kStages) & 1u, ctl));
                     if (!ok) break;
@@ -325,17 +390,17 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                         if (k * kDepth + kDepth <= d) {  // unrolled: the issuing thread sets the pace
 #pragma unroll
                             for (int j = 0; j < 4; ++j)
-                                product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, k > 0 || j > 0);
+                                product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, k > k0 || j > 0);
                         } else {
                             const int steps = (d - k * kDepth + 15) / 16;
                             for (int j = 0; j < steps; ++j)
-                                product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, k > 0 || j > 0);
+                                product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, k > k0 || j > 0);
                         }
                         commit<PAIR>(empty + 8 * s);
-                        if (k == nk - 1) commit<PAIR>(acc_full + 8 * buf);
+                        if (k == k1 - 1) commit<PAIR>(acc_full + 8 * buf);
                     }
                 }
-                if (kWeights && ok && nk == 0 && elect_one()) commit<PAIR>(acc_full + 8 * buf);
+                if (kWeights && ok && k0 == k1 && elect_one()) commit<PAIR>(acc_full + 8 * buf);
             }
             // Every product has ended before tensor memory is freed.  Only this CTA waits, so
             // only its barrier is told: an arrival at the other's could come after it left.
@@ -358,7 +423,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
             const bool none = kWeights && depth() == 0;  // an empty group
             if (!__all_sync(kAll, wait_phase<PAIR, kPipe>(acc_full + 8 * buf, (n >> 1) & 1u, ctl))) break;
             fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + buf * kTile;
+            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + buf * kRows;
             const long long row0 = kWeights ? (long long)t.e * p.N + t.row0 : t.row0;
             const int f0 = t.f * kTile + (int)rank * kHalf + quad * 32;
             const auto release = [&]() {
@@ -369,6 +434,46 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                     else mbar_arrive(acc_empty + 8 * buf);
                 }
             };
+            if constexpr (SPLIT) {
+                // Every CTA of the cluster finishes its share of the rows: the parts of a row
+                // come to it from all of them and are added in the order of the sum.
+                const int share = (columns_of() + (int)parts_n - 1) / (int)parts_n;
+                if (!__all_sync(kAll, wait_phase<true, kPipe>(joinable, (n & 1u) ^ 1u, ctl))) break;
+                const int r0 = (int)part * share, r1 = min(r0 + share, t.rows);
+                if (quad == 0 && lane == 0) mbar_arrive_expect_tx(joined, parts_n * (uint32_t)max(r1 - r0, 0) * 512u);
+                const uint32_t mine = smem_addr(parts) + 4u * (uint32_t)(quad * 32 + lane) + part * (uint32_t)share * 512u;
+                int owner = 0, at = 0;  // the CTA that takes a row, and the row's place there
+                uint32_t to = mapa(mine, 0), bar = mapa(joined, 0);
+#pragma unroll
+                for (int b = 0; b < kRows / 16; ++b) {
+                    if (16 * b < t.rows) {
+                        uint32_t v[16];
+                        read16(acc + 16 * b, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            if (16 * b + i < t.rows) send_cluster(to + (uint32_t)at * 512u, v[i], bar);
+                            if (++at == share) {
+                                at = 0;
+                                owner = min(owner + 1, (int)parts_n - 1);
+                                to = mapa(mine, (uint32_t)owner);
+                                bar = mapa(joined, (uint32_t)owner);
+                            }
+                        }
+                    }
+                }
+                release();
+                if (!__all_sync(kAll, wait_phase<true, kPipe>(joined, n & 1u, ctl))) break;
+                uint16_t *out = static_cast<uint16_t *>(p.out) + (row0 + r0) * p.F + f0 + lane;
+                const float *from = parts + quad * 32 + lane;
+                for (int r = r0; r < r1; ++r, out += p.F, from += 128) {
+                    float sum = 0.0f;
+                    for (int i = 0; i < (int)parts_n; ++i) sum += from[i * share * 128];
+                    if (f0 + lane < p.F) *out = (uint16_t)round16(sum, 0.0f, fp16);
+                }
+                __syncwarp();
+                if (lane < (int)parts_n) arrive_cluster(mapa(joinable, (uint32_t)lane));
+                continue;
+            }
             if (kWeights && p.out_fp32) {  // a lane's feature, row by row: 128 bytes a warp
                 float *out = static_cast<float *>(p.out) + row0 * p.F + f0 + lane;
                 const bool mine = f0 + lane < p.F;
@@ -432,7 +537,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
     }
     fence_before();
     __syncthreads();
-    if constexpr (PAIR) cluster_sync_all();  // the pair's products read both CTAs' shared memory
+    if constexpr (PAIR || SPLIT) cluster_sync_all();  // the others' products, or stores, reach this CTA's shared memory
     if (warp == 2) {
         fence_after();
         tmem_free<PAIR>(tmem, S::kColumns);
@@ -454,6 +559,10 @@ cudaError_t make_linear_maps(LinearMaps *m, const LinearArgs &p, LinearMode mode
         if (e == cudaSuccess) e = matrix(&m->p_rows, x, n, p.F, ld, 1);
         if (e == cudaSuccess) e = matrix(&m->q, w, p.M, p.N, w_ld, kDepth);
         if (e == cudaSuccess) e = matrix(&m->q_rows, w, p.M, p.N, w_ld, 1);
+        if (e == cudaSuccess) e = matrix(&m->p16, x, n, p.F, ld, 16);
+        if (e == cudaSuccess) e = matrix(&m->p4, x, n, p.F, ld, 4);
+        if (e == cudaSuccess) e = matrix(&m->q16, w, p.M, p.N, w_ld, 16);
+        if (e == cudaSuccess) e = matrix(&m->q4, w, p.M, p.N, w_ld, 4);
         m->q_small = m->q;
         return e;
     }
@@ -462,55 +571,153 @@ cudaError_t make_linear_maps(LinearMaps *m, const LinearArgs &p, LinearMode mode
                     CU_TENSOR_MAP_SWIZZLE_128B);
     if (p.rows) {
         if (e == cudaSuccess) e = matrix(&m->q_rows, x, p.x_rows, p.D, ld, 1);
-        m->q = m->q_small = m->p_rows = m->q_rows;
+        m->q = m->q_small = m->p_rows = m->p16 = m->p4 = m->q16 = m->q4 = m->q_rows;
         return e;
     }
     if (e == cudaSuccess) e = matrix(&m->q, x, p.M, p.D, ld, kHalf);
     if (e == cudaSuccess) e = matrix(&m->q_small, x, p.M, p.D, ld, kBoxRows);
-    m->p_rows = m->q_rows = m->q_small;
+    m->p_rows = m->q_rows = m->p16 = m->p4 = m->q16 = m->q4 = m->q_small;
     return e;
 }
 
-template <int MODE, bool PAIR, bool GATHER>
-cudaError_t launch_mode(const LinearArgs &p, const LinearMaps &maps, int sms, bool pdl, cudaStream_t st)
+// Clusters of `split` CTAs that the device holds at once, looked up once per device.
+template <typename... P>
+int resident_clusters(void (*kernel)(P...), int split, int threads, size_t smem, int sms)
 {
-    using S = LinearShape<PAIR>;
-    const auto smem = [](int E) { return 1024 + (size_t)S::kStages * S::kStageBytes + 2 * sizeof(int) * (size_t)(E + 1); };
-    static KernelSetup setup;
-    auto *k = linear_kernel<MODE, PAIR, GATHER>;
-    const cudaError_t e = setup(k, (int)smem(kMaxExperts));
-    if (e != cudaSuccess) return e;
-    const long long row_tiles = MODE == kWeightGrad ? (long long)p.E * ((p.N + S::kTile - 1) / S::kTile)
-                                                    : (long long)p.M / S::kTile + (p.E < p.M ? p.E : p.M);
-    const long long most = row_tiles * ((p.F + S::kTile - 1) / S::kTile);
-    const long long units = sms / S::kCtas;
-    const int grid = (int)(most < units ? most : units) * S::kCtas;
-    return launch_kernel(k, dim3((unsigned)grid), dim3(S::kThreads), smem(p.E), pdl, S::kCtas, st, maps, p);
+    static std::atomic<int> known[64][kMaxSplit + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return sms / split;
+    const int at = split;
+    int n = dev < 64 ? known[dev][at].load(std::memory_order_relaxed) : 0;
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms / split * split));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = (unsigned)split;
+    a.val.clusterDim.y = a.val.clusterDim.z = 1;
+    cfg.attrs = &a;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        n = sms / split;
+    }
+    if (dev < 64) known[dev][at].store(n, std::memory_order_relaxed);
+    return n;
 }
 
-// Which shape: rounds of tiles over the device, a pair's tile costing about twice a
-// CTA's for four times the products.
-bool take_pairs(const LinearArgs &p, LinearMode mode, int sms)
+// Output tiles, at most: the groups' sizes are on the device, and as many groups as rows
+// allow may be in use.
+template <int SHAPE>
+long long most_tiles(const LinearArgs &p, int mode)
 {
+    using S = LinearShape<SHAPE>;
+    const long long groups = p.E < p.M ? p.E : p.M;
+    const long long rows = mode == kWeightGrad ? (long long)p.E * ((p.N + S::kRows - 1) / S::kRows)
+                                               : ((long long)p.M + groups * (S::kRows - 1)) / S::kRows;
+    return rows * ((p.F + S::kTile - 1) / S::kTile);
+}
+
+template <int MODE, int SHAPE, bool GATHER>
+cudaError_t launch_shape(const LinearArgs &p, const LinearMaps &maps, int sms, bool pdl, cudaStream_t st)
+{
+    using S = LinearShape<SHAPE>;
+    static KernelSetup setup;
+    auto *k = linear_kernel<MODE, SHAPE, GATHER>;
+    const cudaError_t e = setup(k, (int)S::smem(kMaxExperts));
+    if (e != cudaSuccess) return e;
+    const int ctas = SHAPE == kSplit ? p.split : S::kCtas;
+    const long long most = most_tiles<SHAPE>(p, MODE);
+    const long long units = SHAPE == kSplit ? resident_clusters(k, ctas, S::kThreads, S::smem(kMaxExperts), sms) : sms / ctas;
+    const int grid = (int)(most < units ? most : units) * ctas;
+    return launch_kernel(k, dim3((unsigned)grid), dim3(S::kThreads), S::smem(p.E), pdl, ctas, st, maps, p);
+}
+
+// Which shape.  A sum is split where one round leaves CTAs idle and is long enough to
+// pay for joining its parts (about 2 us a tile).  Measured, whole / split (us, bytes at
+// the copy rate first): 10 experts with one row, 512 x 8192 12.6: 29.3 / 19.6 (by 3); one
+// expert, 16 rows, 4096 x 8192 10.0: 28.4 / 16.8 (4); 8 rows, 2048 x 8192 5.0: 28.3 / 13.8
+// (8); 512 x 512 5.5 / 6.4 (2): too short.
+// Pairs go by rounds of tiles over the device (groups are taken to leave half a tile
+// each).  A pair's tile fills shared memory as long as a CTA's does, but has more to
+// lose at a group's end: 1.5 of it.  Measured, one CTA / pairs (us): 4096 tokens with 8 of 64
+// experts of 4096 x 5120 1096 / 918, dx 1104 / 909; 2000 with 8 of 32, 1024 x 4096 141 /
+// 117; one expert, 8192 x 8192 and as many rows 870 / 620; 1024 with 2 of 8, 2048 x 2048
+// 34.8 / 38.9.  A weight gradient's tiles are all whole: 333 with 4 of 16, 1024 x 2048
+// 47 / 37; 4096 with 8 of 64, 5120 x 2048 913 / 612.
+int choose_shape(LinearArgs &p, int mode, int sms)
+{
+    const long long groups = p.E < p.M ? p.E : p.M;
     const auto rounds = [&](int tile, int units) {
-        const long long groups = p.E < p.M ? p.E : p.M, even = p.M / tile + groups / 2;
+        const long long even = p.M / tile + groups / 2;
         const long long rows = mode == kWeightGrad ? (long long)p.E * ((p.N + tile - 1) / tile) : even > groups ? even : groups;
         return (rows * ((p.F + tile - 1) / tile) + units - 1) / units;
     };
-    return 2 * rounds(256, sms / 2) < rounds(128, sms);
+    p.split = 1;
+    if (mode == kWeightGrad) return rounds(256, sms / 2) < rounds(128, sms) ? kPair : kOne;
+    const long long fit = sms / most_tiles<kSplit>(p, mode), nk = (p.D + kDepth - 1) / kDepth;
+    const int split = (int)(fit < kMaxSplit ? fit : kMaxSplit);
+    if (split >= 2 && nk * (split - 1) >= 16 * split) {
+        p.split = split;
+        return kSplit;
+    }
+    return 3 * rounds(256, sms / 2) < 2 * rounds(128, sms) ? kPair : kOne;
 }
 
 template <int MODE>
-cudaError_t launch_shapes(const LinearArgs &p, const LinearMaps &maps, int sms, bool pdl, cudaStream_t st)
+cudaError_t launch_mode(LinearArgs p, const LinearMaps &maps, int sms, bool pdl, cudaStream_t st)
 {
-    const bool pair = take_pairs(p, (LinearMode)MODE, sms);
-    if constexpr (MODE != kInputGrad) {
-        if (p.rows) return pair ? launch_mode<MODE, true, true>(p, maps, sms, pdl, st) : launch_mode<MODE, false, true>(p, maps, sms, pdl, st);
+    const int shape = choose_shape(p, MODE, sms);
+    if constexpr (MODE == kForward) {
+        if (p.rows && shape == kSplit) return launch_shape<MODE, kSplit, true>(p, maps, sms, pdl, st);
     }
-    return pair ? launch_mode<MODE, true, false>(p, maps, sms, pdl, st) : launch_mode<MODE, false, false>(p, maps, sms, pdl, st);
+    if constexpr (MODE != kInputGrad) {
+        if (p.rows) return launch_shape<MODE, kOne, true>(p, maps, sms, pdl, st);
+    }
+    if constexpr (MODE != kWeightGrad) {
+        if (shape == kSplit) return launch_shape<MODE, kSplit, false>(p, maps, sms, pdl, st);
+    }
+    return shape == kPair ? launch_shape<MODE, kPair, false>(p, maps, sms, pdl, st) : launch_shape<MODE, kOne, false>(p, maps, sms, pdl, st);
+}
+
+// Rows of x at their places, densely.  A warp a row at a time.
+__global__ void __launch_bounds__(256) place_rows_kernel(const uint4 *x, long long ld, int x_rows, const int32_t *rows, int M,
+                                                         int vectors, uint4 *out, unsigned *err)
+{
+    griddep_launch_dependents();
+    griddep_wait();
+    const int lane = threadIdx.x & 31, warps = (int)gridDim.x * 8;
+    for (int m = (int)blockIdx.x * 8 + ((int)threadIdx.x >> 5); m < M; m += warps) {
+        int r = __ldg(rows + m);
+        if ((unsigned)r >= (unsigned)x_rows) {
+            if (lane == 0) atomicOr(err, BN_DEVERR_PERM_RANGE);
+            r = 0;
+        }
+        const uint4 *from = x + (long long)r * ld;
+        uint4 *to = out + (long long)m * vectors;
+        int i = lane;
+        for (; i + 96 < vectors; i += 128) {
+            uint4 v[4];
+#pragma unroll
+            for (int j = 0; j < 4; ++j) v[j] = __ldg(from + i + 32 * j);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) to[i + 32 * j] = v[j];
+        }
+        for (; i < vectors; i += 32) to[i] = __ldg(from + i);
+    }
 }
 
 }  // namespace
+
+cudaError_t launch_place_rows(const void *x, long long ld, int x_rows, const int32_t *rows, int M, int K, void *out, unsigned *err,
+                              int sms, bool pdl, cudaStream_t st)
+{
+    const long long blocks = ((long long)M + 7) / 8, most = 8LL * sms;
+    return launch_kernel(place_rows_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, pdl, 1, st,
+                         static_cast<const uint4 *>(x), ld / 8, x_rows, rows, M, K / 8, static_cast<uint4 *>(out), err);
+}
 
 cudaError_t launch_linear(const LinearArgs &p, LinearMode mode, const void *x, long long ld, const void *w, long long w_ld, int sms,
                           bool pdl, cudaStream_t st)
@@ -521,9 +728,9 @@ cudaError_t launch_linear(const LinearArgs &p, LinearMode mode, const void *x, l
     const cudaError_t e = make_linear_maps(&maps, p, mode, x, ld, w, w_ld);
     if (e != cudaSuccess) return e;
     switch (mode) {
-    case kForward: return launch_shapes<kForward>(p, maps, sms, pdl, st);
-    case kInputGrad: return launch_shapes<kInputGrad>(p, maps, sms, pdl, st);
-    default: return launch_shapes<kWeightGrad>(p, maps, sms, pdl, st);
+    case kForward: return launch_mode<kForward>(p, maps, sms, pdl, st);
+    case kInputGrad: return launch_mode<kInputGrad>(p, maps, sms, pdl, st);
+    default: return launch_mode<kWeightGrad>(p, maps, sms, pdl, st);
     }
 }
 

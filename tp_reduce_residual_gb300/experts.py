@@ -345,12 +345,31 @@ def _stride(t, name):
     return ld if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
 
 
-def expert_linear(x, w, offsets=None, rows=None, out=None, stream=None) -> torch.Tensor:
+def linear_workspace_bytes(M: int, K: int) -> int:
+    """Workspace bytes with which ``expert_linear`` and ``expert_linear_dw`` bring rows of
+    K values to M places by index, or 0 where they need none."""
+    return (_bn._lib or _bn.load()).bn_expert_linear_workspace_bytes(M, K)
+
+
+def _place_workspace(workspace, rp, M, K, dev, stream):
+    """The caller's workspace, or one for the call from its stream's pool: address, bytes, and the tensor to keep."""
+    if workspace is not None:
+        return (*_bn._workspace(workspace, dev), workspace)
+    n = linear_workspace_bytes(M, K) if rp is not None else 0
+    if n == 0:
+        return None, 0, None
+    workspace = torch.empty(n, dtype=_UINT8, device=dev) if stream is None else _bn._empty((n,), _UINT8, dev, stream)
+    return workspace.data_ptr(), n, workspace
+
+
+def expert_linear(x, w, offsets=None, rows=None, out=None, workspace=None, stream=None) -> torch.Tensor:
     """The experts' linear layer in 16 bits: out [M,N], each row of ``x`` ([n,K] BF16 or
     FP16, any row stride that is a multiple of 8) times its group's weights of ``w``
     ([E,N,K]; [N,K] is one expert), summed in FP32.  ``offsets`` (int32 [E+1]) are the
     groups, ``rows`` (int32 [M]) the row of x at each place, as ``plan`` gives them;
-    without ``rows`` x is grouped already.  Rows of no group are zeros."""
+    without ``rows`` x is grouped already.  Rows of no group are zeros.  More than a few
+    rows by index go through a ``workspace`` (a 1-D uint8 tensor of
+    ``linear_workspace_bytes``; by default one is allocated for the call)."""
     ld = _stride(x, "x")
     dev = x.device
     dtype = _dtype(x, "x", fp32=False)
@@ -360,7 +379,8 @@ def expert_linear(x, w, offsets=None, rows=None, out=None, stream=None) -> torch
         raise ValueError(f"x has rows of {x.shape[1]} values, w of {K}")
     op = _groups(offsets, E, dev)
     out, yp = _out(out, "out", x.dtype, (M, N), dev, stream)
-    _call("bn_expert_linear", (x.data_ptr(), dtype, ld, x.shape[0], rp, M, wp, E, N, K, op, yp), dev.index, stream)
+    sp, n, workspace = _place_workspace(workspace, rp, M, K, dev, stream)
+    _call("bn_expert_linear", (x.data_ptr(), dtype, ld, x.shape[0], rp, M, wp, E, N, K, op, yp, sp, n), dev.index, stream)
     return out
 
 
@@ -381,11 +401,12 @@ def expert_linear_dx(dy, w, offsets=None, dx=None, stream=None) -> torch.Tensor:
     return dx
 
 
-def expert_linear_dw(dy, x, offsets=None, rows=None, dtype=None, dw=None, accumulate: bool = False, stream=None) -> torch.Tensor:
+def expert_linear_dw(dy, x, offsets=None, rows=None, dtype=None, dw=None, accumulate: bool = False, workspace=None,
+                     stream=None) -> torch.Tensor:
     """Gradient of ``expert_linear`` with respect to the weights: dw [E,N,K] from ``dy``
     [M,N] and the layer's ``x`` and ``rows``, in x's dtype or FP32 (``dtype``, or that of
     ``dw``).  ``accumulate`` adds to what an FP32 ``dw`` holds.  Without ``offsets`` there
-    is one expert and dw is [N,K]."""
+    is one expert and dw is [N,K].  ``workspace`` as in ``expert_linear``."""
     ld_dy = _stride(dy, "dy")
     ld = _stride(x, "x")
     dev = dy.device
@@ -406,6 +427,7 @@ def expert_linear_dw(dy, x, offsets=None, rows=None, dtype=None, dw=None, accumu
     if want not in (x.dtype, _FLOAT32) or (dtype is not None and dtype is not want):
         raise TypeError(f"dw must be {x.dtype} or torch.float32 (got {dtype or want})")
     dw, wp = _out(dw, "dw", want, (N, K) if offsets is None else (E, N, K), dev, stream)
+    sp, n, workspace = _place_workspace(workspace, rp, M, K, dev, stream)
     _call("bn_expert_linear_dw", (dy.data_ptr(), d, ld_dy, M, x.data_ptr(), ld, x.shape[0], rp, E, N, K, op, wp, _DTYPES[want],
-                                  1 if accumulate else 0), dev.index, stream)
+                                  1 if accumulate else 0, sp, n), dev.index, stream)
     return dw
