@@ -478,6 +478,39 @@ BN_API bn_status bn_expert_linear_dw(const void *dy, bn_dtype dtype, long long l
                                      bn_dtype dw_dtype, int accumulate, void *workspace,
                                      size_t workspace_bytes, void *stream);
 
+/* The gated activation between an expert's two layers: a row of x holds gate and up side
+ * by side (F values each, rows `ld` elements apart),
+ *   y [M, F] = gate / (1 + exp(-gate)) * up
+ * in FP32, rounded once to `dtype` (BF16, FP16 or FP32).  An infinite gate gives NaN
+ * where the formula has inf - inf or 0 * inf.
+ * Source: none -- it has no counterpart on the pages. */
+BN_API bn_status bn_swiglu(const void *x, bn_dtype dtype, long long ld, int M, int F, void *y,
+                           void *stream);
+
+/* Gradient of bn_swiglu: dx [M, 2 F] from dy [M, F] (rows ld_dy elements apart).
+ * Source: none -- it has no counterpart on the pages. */
+BN_API bn_status bn_swiglu_backward(const void *x, bn_dtype dtype, long long ld, int M, int F,
+                                    const void *dy, long long ld_dy, void *dx, void *stream);
+
+/* Rows in 8-bit integers with a scale a row: row m is row rows[m] (or m) of x.
+ *   x        [x_rows, K] BF16, FP16 or FP32, rows of 16-byte pieces `ld` elements apart
+ *   rows     [M] int32 or NULL; values outside [0, x_rows) set
+ *            BN_DEVERR_PERM_RANGE and read row 0
+ *   data     [M, K]: codes in [-127, 127]
+ *   scales   [M] FP32: max|x| of the row / 127, rounded; a value is code * scale
+ * K is a multiple of 16, at most 131056.  Codes are x / scale to the nearest whole
+ * number, half way to the even one, exactly decided.  A row with an infinity or a NaN
+ * gets a NaN scale and codes 0.
+ * Source: none -- it has no counterpart on the pages. */
+BN_API bn_status bn_quantize_int8(const void *x, bn_dtype dtype, long long ld, int x_rows,
+                                  const int32_t *rows, int M, int K, int8_t *data, float *scales,
+                                  void *stream);
+
+/* The values [M, K] of such rows in BF16, FP16 or FP32: code * scale in FP32, rounded.
+ * Source: none -- it has no counterpart on the pages. */
+BN_API bn_status bn_dequantize_int8(const int8_t *data, const float *scales, int M, int K,
+                                    void *out, bn_dtype dtype, void *stream);
+
 /* ---- queries and errors ------------------------------------------------ */
 
 /* 1 if the fused entry points serve this shape (k = 0 for the reduce-only

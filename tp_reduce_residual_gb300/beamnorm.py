@@ -43,7 +43,7 @@ EXPORTS = (
     "bn_quantize_fp4_workspace_bytes",
     "bn_dequantize_fp4", "bn_expert_product",
     "bn_expert_linear_workspace_bytes", "bn_expert_linear", "bn_expert_linear_dx",
-    "bn_expert_linear_dw",
+    "bn_expert_linear_dw", "bn_swiglu", "bn_swiglu_backward", "bn_quantize_int8", "bn_dequantize_int8",
 )
 
 # bn_op values of the entry points, for launch_info()
@@ -146,6 +146,10 @@ def load() -> ctypes.CDLL:
             "bn_expert_linear_dx": [_P, _I, _L, _I, _P, _I, _I, _I, _P, _P, _P],
             "bn_expert_linear_dw": [_P, _I, _L, _I, _P, _L, _I, _P, _I, _I, _I, _P, _P, _I, _I, _P, ctypes.c_size_t,
                                     _P],
+            "bn_swiglu": [_P, _I, _L, _I, _I, _P, _P],
+            "bn_swiglu_backward": [_P, _I, _L, _I, _I, _P, _L, _P, _P],
+            "bn_quantize_int8": [_P, _I, _L, _I, _P, _I, _I, _P, _P, _P],
+            "bn_dequantize_int8": [_P, _P, _I, _I, _P, _I, _P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)

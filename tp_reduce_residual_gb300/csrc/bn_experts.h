@@ -1,6 +1,6 @@
 // bn_experts.h -- the operators around the experts: launch arguments shared by
 // the ABI (bn_experts_abi.cu) and the kernels (bn_route.cu, bn_plan.cu,
-// bn_fp4.cu, bn_product.cu, bn_linear.cu).  Not part of the ABI.
+// bn_fp4.cu, bn_product.cu, bn_linear.cu, bn_swiglu.cu, bn_int8.cu).  Not part of the ABI.
 #pragma once
 
 #include <atomic>
@@ -96,6 +96,27 @@ struct LinearArgs {
 };
 enum LinearMode { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 
+struct SwigluArgs {
+    const void *x;         // [M, 2 F], ld elements between rows: gate and up
+    const void *dy;        // [M, F], ld_dy elements between rows (gradient) -- or null
+    void *out;             // [M, F], or the gradient [M, 2 F]
+    long long ld, ld_dy;
+    int M, F;
+    int vec;               // 16-byte vectors fit every row of every operand
+};
+
+struct Int8Args {
+    const void *x;         // [x_rows, K], ld elements between rows (quantise)
+    long long ld;
+    long long x_rows;
+    const int32_t *rows;   // [M] or null
+    int M, K;
+    int8_t *data;          // [M, K]
+    float *scales;         // [M]
+    void *out;             // [M, K] (dequantise)
+    unsigned *err;
+};
+
 // dtype: 0 BF16, 1 FP16, 2 FP32.  fmt: 0 NVFP4, 1 MXFP4.
 cudaError_t launch_route(const RouteArgs &, int dtype, bool pdl, cudaStream_t);
 cudaError_t launch_route_backward(const RouteBackwardArgs &, int dtype, bool pdl, cudaStream_t);
@@ -110,6 +131,9 @@ cudaError_t launch_product(const ProductArgs &, const uint8_t *a, const uint8_t 
 cudaError_t launch_linear(const LinearArgs &, LinearMode mode, const void *x, long long ld, const void *w, long long w_ld,
                           int sms, bool pdl, cudaStream_t);
 
+cudaError_t launch_swiglu(const SwigluArgs &, int dtype, bool backward, int sms, bool pdl, cudaStream_t);
+cudaError_t launch_quantize_int8(const Int8Args &, int dtype, bool pdl, cudaStream_t);
+cudaError_t launch_dequantize_int8(const Int8Args &, int dtype, int sms, bool pdl, cudaStream_t);
 // out [M, K] dense: row rows[m] of x at place m (16-bit values).
 cudaError_t launch_place_rows(const void *x, long long ld, int x_rows, const int32_t *rows, int M, int K, void *out, unsigned *err,
                               int sms, bool pdl, cudaStream_t);

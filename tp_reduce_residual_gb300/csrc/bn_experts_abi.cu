@@ -16,6 +16,7 @@ namespace {
 
 // Rows and slots are counted in int32, rounded up to tiles and blocks.
 constexpr long long kMaxRows = (1LL << 31) - 1024;
+constexpr int kMaxInt8K = 131056;
 
 size_t dtype_size(int dtype) { return dtype == BN_FP32 ? 4 : 2; }
 
@@ -123,6 +124,27 @@ bn_status check_rows(const void *p, const char *name, long long ld, int width)
     BN_REQUIRE(ld >= width && ld % 8 == 0, "%s: ld=%lld is not a multiple of 8 of at least %d", name, ld, width);
     if (ld > (1LL << 36)) return fail(BN_ERR_UNSUPPORTED, "%s: ld=%lld above the served maximum", name, ld);
     return check_ptr16(p, name);
+}
+
+bn_status check_int8(int M, int K)
+{
+    BN_REQUIRE(M >= 0, "M=%d is negative", M);
+    BN_REQUIRE(K >= 16 && K % 16 == 0, "K=%d is not a positive multiple of 16", K);
+    if (M > kMaxRows) return fail(BN_ERR_UNSUPPORTED, "M=%d above the served maximum %lld", M, kMaxRows);
+    // K products of two codes of at most 128 each fit 32 bits
+    if (K > kMaxInt8K) return fail(BN_ERR_UNSUPPORTED, "K=%d above the served maximum %d", K, kMaxInt8K);
+    return BN_OK;
+}
+
+bn_status check_swiglu(int dtype, int M, int F, long long ld)
+{
+    BN_TRY(check_dtype(dtype, true));
+    BN_REQUIRE(M >= 0, "M=%d is negative", M);
+    BN_REQUIRE(F >= 1, "F=%d is not positive", F);
+    BN_REQUIRE(ld >= 2LL * F, "ld=%lld below 2 * F=%lld", ld, 2LL * F);
+    if (M > kMaxRows) return fail(BN_ERR_UNSUPPORTED, "M=%d above the served maximum %lld", M, kMaxRows);
+    if (F > (1 << 28)) return fail(BN_ERR_UNSUPPORTED, "F=%d above the served maximum %d", F, 1 << 28);
+    return BN_OK;
 }
 
 // With a workspace of enough bytes, rows by index go to their places there first; x, ld and the
@@ -533,6 +555,118 @@ bn_status bn_expert_linear_dw(const void *dy, bn_dtype dtype, long long ld_dy, i
     BN_TRY(place_rows(a, x, ld, K, workspace, workspace_bytes, *d, stream));
     return launched(launch_linear(a, kWeightGrad, x, ld, dy, ld_dy, d->sms, dependent_launch(), (cudaStream_t)stream),
                     "launching expert_linear_dw");
+}
+
+bn_status bn_swiglu(const void *x, bn_dtype dtype, long long ld, int M, int F, void *y, void *stream)
+{
+    clear_message();
+    BN_TRY(check_swiglu(dtype, M, F, ld));
+    if (M == 0) return BN_OK;
+    const size_t size = dtype_size(dtype);
+    BN_TRY(check_element(x, size, "x"));
+    BN_TRY(check_element(y, size, "y"));
+    const Range writes[] = {{y, (size_t)M * F * size, "y"}};
+    const Range reads[] = {{x, span(M, ld, 2 * F, size), "x"}};
+    BN_TRY(check_overlaps(writes, 1, reads, 1));
+    const DeviceInfo *d = nullptr;
+    BN_TRY(device_info(&d));
+    SwigluArgs a = {};
+    a.x = x;
+    a.out = y;
+    a.ld = ld;
+    a.M = M;
+    a.F = F;
+    a.vec = vectors(x, ld, F, size) && vectors(y, F, F, size);
+    return launched(launch_swiglu(a, dtype, false, d->sms, dependent_launch(), (cudaStream_t)stream), "launching swiglu");
+}
+
+bn_status bn_swiglu_backward(const void *x, bn_dtype dtype, long long ld, int M, int F, const void *dy, long long ld_dy,
+                             void *dx, void *stream)
+{
+    clear_message();
+    BN_TRY(check_swiglu(dtype, M, F, ld));
+    BN_REQUIRE(ld_dy >= F, "ld_dy=%lld below F=%d", ld_dy, F);
+    if (M == 0) return BN_OK;
+    const size_t size = dtype_size(dtype);
+    BN_TRY(check_element(x, size, "x"));
+    BN_TRY(check_element(dy, size, "dy"));
+    BN_TRY(check_element(dx, size, "dx"));
+    const Range writes[] = {{dx, (size_t)M * 2 * F * size, "dx"}};
+    const Range reads[] = {{x, span(M, ld, 2 * F, size), "x"}, {dy, span(M, ld_dy, F, size), "dy"}};
+    BN_TRY(check_overlaps(writes, 1, reads, 2));
+    const DeviceInfo *d = nullptr;
+    BN_TRY(device_info(&d));
+    SwigluArgs a = {};
+    a.x = x;
+    a.dy = dy;
+    a.out = dx;
+    a.ld = ld;
+    a.ld_dy = ld_dy;
+    a.M = M;
+    a.F = F;
+    a.vec = vectors(x, ld, F, size) && vectors(dy, ld_dy, F, size) && vectors(dx, F, F, size);
+    return launched(launch_swiglu(a, dtype, true, d->sms, dependent_launch(), (cudaStream_t)stream),
+                    "launching swiglu_backward");
+}
+
+bn_status bn_quantize_int8(const void *x, bn_dtype dtype, long long ld, int x_rows, const int32_t *rows, int M, int K,
+                           int8_t *data, float *scales, void *stream)
+{
+    clear_message();
+    BN_TRY(check_dtype(dtype, true));
+    BN_TRY(check_int8(M, K));
+    const size_t size = dtype_size(dtype);
+    const int per = 16 / (int)size;
+    BN_REQUIRE(ld >= K && ld % per == 0, "ld=%lld is not a multiple of %d of at least K=%d", ld, per, K);
+    BN_REQUIRE(x_rows >= 0, "x_rows=%d is negative", x_rows);
+    BN_REQUIRE(rows || x_rows == M, "x has %d rows, M=%d are wanted and no rows are given", x_rows, M);
+    if (M == 0) return BN_OK;
+    BN_REQUIRE(x_rows > 0, "x has no rows");
+    BN_TRY(check_ptr16(x, "x"));
+    BN_REQUIRE(aligned(rows, 4), "rows is not 4-byte aligned");
+    BN_TRY(check_ptr16(data, "data"));
+    BN_TRY(check_ptr4(scales, "scales"));
+    const Range writes[] = {{data, (size_t)M * K, "data"}, {scales, (size_t)M * 4, "scales"}};
+    const Range reads[] = {{x, span(x_rows, ld, K, size), "x"}, {rows, (size_t)M * 4, "rows"}};
+    BN_TRY(check_overlaps(writes, 2, reads, 2));
+    const DeviceInfo *d = nullptr;
+    BN_TRY(device_info(&d));
+    Int8Args a = {};
+    a.x = x;
+    a.ld = ld;
+    a.x_rows = x_rows;
+    a.rows = rows;
+    a.M = M;
+    a.K = K;
+    a.data = data;
+    a.scales = scales;
+    a.err = d->err;
+    return launched(launch_quantize_int8(a, dtype, dependent_launch(), (cudaStream_t)stream), "launching quantize_int8");
+}
+
+bn_status bn_dequantize_int8(const int8_t *data, const float *scales, int M, int K, void *out, bn_dtype dtype,
+                             void *stream)
+{
+    clear_message();
+    BN_TRY(check_dtype(dtype, true));
+    BN_TRY(check_int8(M, K));
+    if (M == 0) return BN_OK;
+    BN_TRY(check_ptr16(data, "data"));
+    BN_TRY(check_ptr4(scales, "scales"));
+    BN_TRY(check_ptr16(out, "out"));
+    const Range writes[] = {{out, (size_t)M * K * dtype_size(dtype), "out"}};
+    const Range reads[] = {{data, (size_t)M * K, "data"}, {scales, (size_t)M * 4, "scales"}};
+    BN_TRY(check_overlaps(writes, 1, reads, 2));
+    const DeviceInfo *d = nullptr;
+    BN_TRY(device_info(&d));
+    Int8Args a = {};
+    a.M = M;
+    a.K = K;
+    a.data = const_cast<int8_t *>(data);
+    a.scales = const_cast<float *>(scales);
+    a.out = out;
+    return launched(launch_dequantize_int8(a, dtype, d->sms, dependent_launch(), (cudaStream_t)stream),
+                    "launching dequantize_int8");
 }
 
 }  // extern "C"

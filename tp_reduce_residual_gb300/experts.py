@@ -59,6 +59,19 @@ class FP4:
         return (*self.data.shape[:-1], 2 * self.data.shape[-1])
 
 
+@dataclass
+class Int8:
+    """Rows in 8-bit integers: ``data`` int8 [..., K] and a scale for each row, ``scales``
+    FP32 [...].  ``offsets`` as in FP4."""
+    data: torch.Tensor
+    scales: torch.Tensor
+    offsets: Optional[torch.Tensor] = None
+
+    @property
+    def shape(self):
+        return tuple(self.data.shape)
+
+
 # A decoded token's operators take a few microseconds on the GPU, so the checks
 # below are written for the host's time: an argument that is as it should be passes
 # in one expression, and only one that is not goes through beamnorm's checks for
@@ -431,3 +444,84 @@ def expert_linear_dw(dy, x, offsets=None, rows=None, dtype=None, dw=None, accumu
     _call("bn_expert_linear_dw", (dy.data_ptr(), d, ld_dy, M, x.data_ptr(), ld, x.shape[0], rp, E, N, K, op, wp, _DTYPES[want],
                                   1 if accumulate else 0, sp, n), dev.index, stream)
     return dw
+
+
+def swiglu(x, out=None, stream=None) -> torch.Tensor:
+    """The gated activation between an expert's two layers: [M,F], gate / (1 + exp(-gate)) * up
+    of ``x`` [M,2F] (gate and up side by side; BF16, FP16 or FP32, any row stride)."""
+    ld = _rows2d(x, "x")
+    M, n = x.shape
+    if n == 0 or n % 2:
+        raise ValueError(f"x must have rows of gate and up side by side (got {n} values)")
+    dev = x.device
+    dtype = _dtype(x, "x")
+    out, yp = _out(out, "out", x.dtype, (M, n // 2), dev, stream)
+    _call("bn_swiglu", (x.data_ptr(), dtype, ld, M, n // 2, yp), dev.index, stream)
+    return out
+
+
+def swiglu_backward(x, dy, dx=None, stream=None) -> torch.Tensor:
+    """Gradient of ``swiglu``: dx [M,2F] from its ``x`` and ``dy`` [M,F] (any row strides)."""
+    ld, ld_dy = _rows2d(x, "x"), _rows2d(dy, "dy")
+    M, n = x.shape
+    if n == 0 or n % 2:
+        raise ValueError(f"x must have rows of gate and up side by side (got {n} values)")
+    dev = x.device
+    dtype = _dtype(x, "x")
+    if dy.shape != (M, n // 2) or dy.dtype is not x.dtype or dy.device != dev:
+        raise ValueError(f"dy must be {x.dtype} of shape {(M, n // 2)} on {dev} (got {dy.dtype}, {tuple(dy.shape)}, {dy.device})")
+    dx, xp = _out(dx, "dx", x.dtype, (M, n), dev, stream)
+    _call("bn_swiglu_backward", (x.data_ptr(), dtype, ld, M, n // 2, dy.data_ptr(), ld_dy, xp), dev.index, stream)
+    return dx
+
+
+def quantize_int8(x, rows=None, offsets=None, data=None, scales=None, stream=None) -> Int8:
+    """Rows of ``x`` ([n,K], or [groups,n,K] such as weights, whose rows are the output
+    channels; BF16, FP16 or FP32) in 8-bit integers with a scale a row.  ``rows`` (int32
+    [M]) picks the rows; ``offsets`` are kept with the result."""
+    if not isinstance(x, torch.Tensor):
+        raise TypeError("x must be a torch.Tensor")
+    lead = None
+    if x.dim() == 3:
+        if rows is not None or offsets is not None:
+            raise ValueError("a 3-D x has equal groups: it takes neither rows nor offsets")
+        if not x.is_contiguous():
+            raise ValueError("a 3-D x must be contiguous")
+        lead = x.shape[:2]
+        x = x.view(-1, x.shape[2])
+    ld = _rows2d(x, "x")
+    n, K = x.shape
+    dev = x.device
+    dtype = _dtype(x, "x")
+    if n <= 1:
+        ld = -(-K // 8) * 8
+    if offsets is not None:
+        _ptr(offsets, "offsets", _INT32, (offsets.numel(),), dev)
+    M, rp = _places(x, rows)
+    shape = lead if lead is not None else (M,)
+    data, dp = _out(data, "data", torch.int8, (*shape, K), dev, stream)
+    scales, sp = _out(scales, "scales", _FLOAT32, tuple(shape), dev, stream)
+    _call("bn_quantize_int8", (x.data_ptr(), dtype, ld, n, rp, M, K, dp, sp), dev.index, stream)
+    return Int8(data, scales, offsets)
+
+
+def _layout_int8(q: Int8, name: str):
+    """(rows, K, and the addresses of data and scales) of 8-bit rows, after checks."""
+    if not isinstance(q, Int8):
+        raise TypeError(f"{name} must be an Int8")
+    data = q.data
+    shape = data.shape
+    if len(shape) not in (2, 3) or (len(shape) == 3 and q.offsets is not None):
+        raise ValueError(f"{name}.data must be [M, K], or [groups, rows, K] without offsets")
+    dp = _ptr(data, f"{name}.data", torch.int8, shape, data.device)
+    sp = _ptr(q.scales, f"{name}.scales", _FLOAT32, shape[:-1], data.device)
+    return q.scales.numel(), shape[-1], dp, sp
+
+
+def dequantize_int8(q: Int8, dtype=torch.bfloat16, out=None, stream=None) -> torch.Tensor:
+    """The values of 8-bit rows ([..., K]) in BF16, FP16 or FP32."""
+    M, K, dp, sp = _layout_int8(q, "q")
+    dev = q.data.device
+    out, yp = _out(out, "out", dtype if out is None else out.dtype, q.shape, dev, stream)
+    _call("bn_dequantize_int8", (dp, sp, M, K, yp, _dtype(out, "out")), dev.index, stream)
+    return out
