@@ -511,6 +511,28 @@ BN_API bn_status bn_quantize_int8(const void *x, bn_dtype dtype, long long ld, i
 BN_API bn_status bn_dequantize_int8(const int8_t *data, const float *scales, int M, int K,
                                     void *out, bn_dtype dtype, void *stream);
 
+/* Bytes of the workspace that bn_expert_product_int8 needs (the rows' codes in 16 bits),
+ * 0 on invalid arguments or no rows.  Pure host logic.
+ * Source: no passage: library utility. */
+BN_API size_t bn_expert_product_int8_workspace_bytes(int M, int K);
+
+/* out[m, n] = bf16(alpha * a_scales[m] * w_scales[e, n] * sum over k of a[m, k] * w[e, n, k])
+ * for the rows m of group e.  The sum is exact (32-bit integers), for any codes in
+ * [-128, 127]; the rest is FP32.
+ *   a, a_scales  [M, K] codes and [M] FP32, rows grouped by `offsets`
+ *   w, w_scales  [E, N, K] codes and [E, N] FP32: a scale for each output channel
+ *   offsets      [E + 1] int32, or NULL when E == 1 (every row)
+ *   out          [M, N] BF16; rows before the first offset and past the last are zeros
+ *   workspace    device memory of bn_expert_product_int8_workspace_bytes() or more,
+ *                16-byte aligned.  Nothing in it is kept
+ * Two kernels on `stream`.  N is a multiple of 8, K of 16, at most 131056.  Offsets that
+ * fall or leave [0, M] set BN_DEVERR_OFFSETS; they are clamped.
+ * Source: none -- the pages take the experts' rows as given; it has no counterpart there. */
+BN_API bn_status bn_expert_product_int8(const int8_t *a, const float *a_scales, int M,
+                                        const int8_t *w, const float *w_scales, int E, int N,
+                                        int K, const int32_t *offsets, float alpha, uint16_t *out,
+                                        void *workspace, size_t workspace_bytes, void *stream);
+
 /* ---- queries and errors ------------------------------------------------ */
 
 /* 1 if the fused entry points serve this shape (k = 0 for the reduce-only

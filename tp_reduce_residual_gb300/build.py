@@ -48,7 +48,8 @@ MODES = {
 }
 
 # the operators around the experts, one object each
-EXPERTS = ["bn_experts_abi", "bn_route", "bn_plan", "bn_fp4", "bn_product", "bn_linear", "bn_swiglu", "bn_int8"]
+EXPERTS = ["bn_experts_abi", "bn_route", "bn_plan", "bn_fp4", "bn_product", "bn_linear", "bn_swiglu", "bn_int8",
+           "bn_product8"]
 
 SOURCES = ["bn_device.cuh", "bn_internal.h", "bn_kernels.cu", "bn_abi.cu", "bn_wide.h",
            "bn_wide.cu", "bn_noalloc.cu", "bn_cluster.h", "bn_cluster.cu", "bn_host.h",

@@ -1,6 +1,6 @@
 // bn_experts.h -- the operators around the experts: launch arguments shared by
 // the ABI (bn_experts_abi.cu) and the kernels (bn_route.cu, bn_plan.cu,
-// bn_fp4.cu, bn_product.cu, bn_linear.cu, bn_swiglu.cu, bn_int8.cu).  Not part of the ABI.
+// bn_fp4.cu, bn_product.cu, bn_linear.cu, bn_swiglu.cu, bn_int8.cu, bn_product8.cu).  Not part of the ABI.
 #pragma once
 
 #include <atomic>
@@ -117,6 +117,17 @@ struct Int8Args {
     unsigned *err;
 };
 
+struct Product8Args {
+    int M, E, N, K;
+    const int32_t *offsets;   // [E + 1] or null (E = 1, all rows)
+    const float *a_scales;    // [M]
+    const float *w_scales;    // [E, N]
+    float alpha;
+    uint16_t *out;            // [M, N] BF16
+    int split;                // CTAs that share a tile's sum
+    unsigned *err;
+};
+
 // dtype: 0 BF16, 1 FP16, 2 FP32.  fmt: 0 NVFP4, 1 MXFP4.
 cudaError_t launch_route(const RouteArgs &, int dtype, bool pdl, cudaStream_t);
 cudaError_t launch_route_backward(const RouteBackwardArgs &, int dtype, bool pdl, cudaStream_t);
@@ -134,6 +145,8 @@ cudaError_t launch_linear(const LinearArgs &, LinearMode mode, const void *x, lo
 cudaError_t launch_swiglu(const SwigluArgs &, int dtype, bool backward, int sms, bool pdl, cudaStream_t);
 cudaError_t launch_quantize_int8(const Int8Args &, int dtype, bool pdl, cudaStream_t);
 cudaError_t launch_dequantize_int8(const Int8Args &, int dtype, int sms, bool pdl, cudaStream_t);
+// workspace: 2 M K bytes, for the rows widened to FP16.
+cudaError_t launch_product8(Product8Args, const int8_t *a, const int8_t *w, void *workspace, int sms, bool pdl, cudaStream_t);
 // out [M, K] dense: row rows[m] of x at place m (16-bit values).
 cudaError_t launch_place_rows(const void *x, long long ld, int x_rows, const int32_t *rows, int M, int K, void *out, unsigned *err,
                               int sms, bool pdl, cudaStream_t);

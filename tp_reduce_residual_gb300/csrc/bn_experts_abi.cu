@@ -669,4 +669,55 @@ bn_status bn_dequantize_int8(const int8_t *data, const float *scales, int M, int
                     "launching dequantize_int8");
 }
 
+size_t bn_expert_product_int8_workspace_bytes(int M, int K)
+{
+    return M > 0 && K >= 16 && K % 16 == 0 ? (size_t)M * K * 2 : 0;
+}
+
+bn_status bn_expert_product_int8(const int8_t *a, const float *a_scales, int M, const int8_t *w, const float *w_scales,
+                                 int E, int N, int K, const int32_t *offsets, float alpha, uint16_t *out,
+                                 void *workspace, size_t workspace_bytes, void *stream)
+{
+    clear_message();
+    BN_TRY(check_int8(M, K));
+    BN_REQUIRE(E >= 1, "E=%d is not positive", E);
+    BN_REQUIRE(N >= 8 && N % 8 == 0, "N=%d is not a positive multiple of 8", N);
+    BN_REQUIRE(offsets || E == 1, "offsets is NULL with E=%d experts", E);
+    BN_REQUIRE(aligned(offsets, 4), "offsets is not 4-byte aligned");
+    BN_REQUIRE(std::isfinite(alpha), "alpha must be finite");
+    if (E > kMaxExperts) return fail(BN_ERR_UNSUPPORTED, "E=%d above the served maximum %d", E, kMaxExperts);
+    if (N > (1 << 20)) return fail(BN_ERR_UNSUPPORTED, "N=%d above the served maximum %d", N, 1 << 20);
+    if (M == 0) return BN_OK;
+    BN_TRY(check_ptr16(a, "a"));
+    BN_TRY(check_ptr4(a_scales, "a_scales"));
+    BN_TRY(check_ptr16(w, "w"));
+    BN_TRY(check_ptr4(w_scales, "w_scales"));
+    BN_TRY(check_ptr16(out, "out"));
+    BN_TRY(check_ptr16(workspace, "workspace"));
+    const size_t need = bn_expert_product_int8_workspace_bytes(M, K);
+    BN_REQUIRE(workspace_bytes >= need, "workspace of %zu bytes is below %zu", workspace_bytes, need);
+    const Range writes[] = {{out, (size_t)M * N * 2, "out"}, {workspace, workspace_bytes, "workspace"}};
+    const Range reads[] = {{a, (size_t)M * K, "a"},
+                           {a_scales, (size_t)M * 4, "a_scales"},
+                           {w, (size_t)E * N * K, "w"},
+                           {w_scales, (size_t)E * N * 4, "w_scales"},
+                           {offsets, (size_t)(E + 1) * 4, "offsets"}};
+    BN_TRY(check_overlaps(writes, 2, reads, 5));
+    const DeviceInfo *d = nullptr;
+    BN_TRY(device_info(&d));
+    Product8Args p = {};
+    p.M = M;
+    p.E = E;
+    p.N = N;
+    p.K = K;
+    p.offsets = offsets;
+    p.a_scales = a_scales;
+    p.w_scales = w_scales;
+    p.alpha = alpha;
+    p.out = out;
+    p.err = d->err;
+    return launched(launch_product8(p, a, w, workspace, d->sms, dependent_launch(), (cudaStream_t)stream),
+                    "launching expert_product_int8");
+}
+
 }  // extern "C"

@@ -33,8 +33,7 @@ namespace {
 
 constexpr int kHalf = 128;      // features, and at most rows, that one CTA loads for a tile
 constexpr int kDepth = 64;      // summed values of a stage: 128 bytes
-constexpr int kBoxRows = 32;    // rows of the smaller box
-constexpr int kMaxSplit = 8;    // CTAs that share a tile's sum
+constexpr int kBoxRows = 16;    // rows of the smaller box
 constexpr int kAtom = 64 * 128; // bytes of 64 features or rows by 64 values, where the sum runs across rows
 
 enum Shape { kOne = 0, kPair = 1, kSplit = 2 };
@@ -57,7 +56,7 @@ struct LinearShape {
 
 struct LinearMaps {
     CUtensorMap p;                 // the features' operand: w, or x
-    CUtensorMap q, q_small;        // the rows' operand: x or dy, in boxes of 128 (64) and 32 rows
+    CUtensorMap q, q_small;        // the rows' operand: x or dy, in boxes of 128 (64) and 16 rows
     CUtensorMap p_rows, q_rows;    // row by row: x (and dy) of the weight gradient, x of the forward
     CUtensorMap p16, p4, q16, q4;  // the weight gradient's in boxes of 16 and 4 rows
 };
@@ -120,17 +119,6 @@ __device__ __forceinline__ uint32_t round16(float a, float b, bool fp16)
     }
     const __nv_bfloat162 h = __floats2bfloat162_rn(a, b);
     return *reinterpret_cast<const uint32_t *>(&h);
-}
-
-// A value into the shared memory of a CTA of the cluster, counted on its barrier there.
-__device__ __forceinline__ void send_cluster(uint32_t addr, uint32_t v, uint32_t bar)
-{
-    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
-                 : "memory");
-}
-__device__ __forceinline__ void arrive_cluster(uint32_t bar)
-{
-    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
 }
 
 template <int MODE, int SHAPE, bool GATHER>
@@ -230,7 +218,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
             const int d = depth();
             int k0, k1;
             stages(d, k0, k1);
-            const int boxes = nb > kHalf / 2 ? 0 : (nb + kBoxRows - 1) / kBoxRows;  // 0: one of kHalf rows
+            const int boxes = nb > kHalf / 2 && !SPLIT ? 0 : (nb + kBoxRows - 1) / kBoxRows;  // 0: one of kHalf rows
             const int q_atoms = nb > 64 ? 2 : 1;
             if constexpr (GATHER && !kWeights) {  // four rows a lane; places past the tile read zeros
                 int v[4];
@@ -580,34 +568,6 @@ cudaError_t make_linear_maps(LinearMaps *m, const LinearArgs &p, LinearMode mode
     return e;
 }
 
-// Clusters of `split` CTAs that the device holds at once, looked up once per device.
-template <typename... P>
-int resident_clusters(void (*kernel)(P...), int split, int threads, size_t smem, int sms)
-{
-    static std::atomic<int> known[64][kMaxSplit + 1];
-    int dev = 0;
-    if (cudaGetDevice(&dev) != cudaSuccess) return sms / split;
-    const int at = split;
-    int n = dev < 64 ? known[dev][at].load(std::memory_order_relaxed) : 0;
-    if (n > 0) return n;
-    cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = dim3((unsigned)(sms / split * split));
-    cfg.blockDim = dim3((unsigned)threads);
-    cfg.dynamicSmemBytes = smem;
-    cudaLaunchAttribute a;
-    a.id = cudaLaunchAttributeClusterDimension;
-    a.val.clusterDim.x = (unsigned)split;
-    a.val.clusterDim.y = a.val.clusterDim.z = 1;
-    cfg.attrs = &a;
-    cfg.numAttrs = 1;
-    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
-        (void)cudaGetLastError();
-        n = sms / split;
-    }
-    if (dev < 64) known[dev][at].store(n, std::memory_order_relaxed);
-    return n;
-}
-
 // Output tiles, at most: the groups' sizes are on the device, and as many groups as rows
 // allow may be in use.
 template <int SHAPE>
@@ -635,8 +595,8 @@ cudaError_t launch_shape(const LinearArgs &p, const LinearMaps &maps, int sms, b
     return launch_kernel(k, dim3((unsigned)grid), dim3(S::kThreads), S::smem(p.E), pdl, ctas, st, maps, p);
 }
 
-// Which shape.  A sum is split where one round leaves CTAs idle and is long enough to
-// pay for joining its parts (about 2 us a tile).  Measured, whole / split (us, bytes at
+// Which shape.  Sums are split where tiles are too few for the device and a sum is long
+// enough to pay for joining its parts (about 1.5 us, 8 stages).  Measured, whole / split (us, bytes at
 // the copy rate first): 10 experts with one row, 512 x 8192 12.6: 29.3 / 19.6 (by 3); one
 // expert, 16 rows, 4096 x 8192 10.0: 28.4 / 16.8 (4); 8 rows, 2048 x 8192 5.0: 28.3 / 13.8
 // (8); 512 x 512 5.5 / 6.4 (2): too short.
@@ -657,12 +617,9 @@ int choose_shape(LinearArgs &p, int mode, int sms)
     };
     p.split = 1;
     if (mode == kWeightGrad) return rounds(256, sms / 2) < rounds(128, sms) ? kPair : kOne;
-    const long long fit = sms / most_tiles<kSplit>(p, mode), nk = (p.D + kDepth - 1) / kDepth;
-    const int split = (int)(fit < kMaxSplit ? fit : kMaxSplit);
-    if (split >= 2 && nk * (split - 1) >= 16 * split) {
-        p.split = split;
-        return kSplit;
-    }
+    const long long nk = (p.D + kDepth - 1) / kDepth;
+    p.split = choose_split(most_tiles<kSplit>(p, mode), nk, 8, (most_tiles<kOne>(p, mode) + sms - 1) / sms * nk, sms);
+    if (p.split > 1) return kSplit;
     return 3 * rounds(256, sms / 2) < 2 * rounds(128, sms) ? kPair : kOne;
 }
 

@@ -3,6 +3,7 @@
 // memory, and tensor maps on the host.
 #pragma once
 
+#include <atomic>
 #include <mutex>
 
 #include <cuda.h>
@@ -250,6 +251,64 @@ __device__ __forceinline__ uint4 transpose8(const uint32_t *w, int lane)
     const uint32_t o0 = __shfl_xor_sync(kAll, lane & 4 ? b[0][0] : b[1][0], 4);
     const uint32_t o1 = __shfl_xor_sync(kAll, lane & 4 ? b[0][1] : b[1][1], 4);
     return lane & 4 ? make_uint4(o0, o1, b[1][0], b[1][1]) : make_uint4(b[0][0], b[0][1], o0, o1);
+}
+
+// A value into the shared memory of a CTA of the cluster, counted on its barrier there.
+__device__ __forceinline__ void send_cluster(uint32_t addr, uint32_t v, uint32_t bar)
+{
+    asm volatile("st.async.weak.shared::cluster.mbarrier::complete_tx::bytes.b32 [%0], %1, [%2];" ::"r"(addr), "r"(v), "r"(bar)
+                 : "memory");
+}
+__device__ __forceinline__ void arrive_cluster(uint32_t bar)
+{
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(bar) : "memory");
+}
+
+constexpr int kMaxSplit = 8;  // CTAs that share a tile's sum
+
+// By how many CTAs to split the sums of `tiles` tiles of `stages` stages: rounds over the
+// device times the stages of a part, a join of parts costing `join` stages more; 1 unless
+// that saves a tenth of `whole`, the same count without a split.
+inline int choose_split(long long tiles, long long stages, long long join, long long whole, int sms)
+{
+    int best = 1;
+    long long least = whole * 9;
+    for (int s = 2; s <= kMaxSplit && s * 4 <= stages; ++s) {
+        const long long units = sms / s, cost = (tiles + units - 1) / units * ((stages + s - 1) / s + join) * 10;
+        if (cost < least) {
+            least = cost;
+            best = s;
+        }
+    }
+    return best;
+}
+
+// Clusters of `split` CTAs that the device holds at once, looked up once per device.
+template <typename... P>
+int resident_clusters(void (*kernel)(P...), int split, int threads, size_t smem, int sms)
+{
+    static std::atomic<int> known[64][kMaxSplit + 1];
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess) return sms / split;
+    const int at = split;
+    int n = dev < 64 ? known[dev][at].load(std::memory_order_relaxed) : 0;
+    if (n > 0) return n;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(sms / split * split));
+    cfg.blockDim = dim3((unsigned)threads);
+    cfg.dynamicSmemBytes = smem;
+    cudaLaunchAttribute a;
+    a.id = cudaLaunchAttributeClusterDimension;
+    a.val.clusterDim.x = (unsigned)split;
+    a.val.clusterDim.y = a.val.clusterDim.z = 1;
+    cfg.attrs = &a;
+    cfg.numAttrs = 1;
+    if (cudaOccupancyMaxActiveClusters(&n, kernel, &cfg) != cudaSuccess || n < 1) {
+        (void)cudaGetLastError();
+        n = sms / split;
+    }
+    if (dev < 64) known[dev][at].store(n, std::memory_order_relaxed);
+    return n;
 }
 
 using EncodeFn = CUresult (*)(CUtensorMap *, CUtensorMapDataType, cuuint32_t, void *, const cuuint64_t *,

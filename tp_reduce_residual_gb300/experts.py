@@ -303,10 +303,17 @@ def dequantize_fp4(q: FP4, dtype=torch.bfloat16, out=None, stream=None) -> torch
     return out
 
 
-def expert_product(a: FP4, w: FP4, scale: float = 1.0, out=None, stream=None) -> torch.Tensor:
+def expert_product(a, w, scale: float = 1.0, out=None, workspace=None, stream=None) -> torch.Tensor:
     """out [M,N] BF16: each row of ``a`` ([M,K], grouped by ``a.offsets``) times
     its group's weights of ``w`` ([E,N,K]; [N,K] is one expert), times ``scale``
-    and both tensor scales.  Rows before the first group and past the last are zeros."""
+    and the operands' scales.  Both are FP4 or both Int8, whose sums are exact.  Rows
+    before the first group and past the last are zeros.  Int8 rows go through a
+    ``workspace`` (a 1-D uint8 tensor of ``product_int8_workspace_bytes``; by default one is
+    allocated for the call); FP4 ones take none."""
+    if isinstance(a, Int8):
+        return _expert_product_int8(a, w, scale, out, workspace, stream)
+    if workspace is not None:
+        raise ValueError("FP4 rows take no workspace")
     M, K, groups, op, ap, sp = _layout(a, "a")
     _, wK, E, wo, wp, wsp = _layout(w, "w")
     if wo is not None:
@@ -524,4 +531,35 @@ def dequantize_int8(q: Int8, dtype=torch.bfloat16, out=None, stream=None) -> tor
     dev = q.data.device
     out, yp = _out(out, "out", dtype if out is None else out.dtype, q.shape, dev, stream)
     _call("bn_dequantize_int8", (dp, sp, M, K, yp, _dtype(out, "out")), dev.index, stream)
+    return out
+
+
+def product_int8_workspace_bytes(M: int, K: int) -> int:
+    """Workspace bytes that ``expert_product`` needs for M Int8 rows of K values."""
+    return (_bn._lib or _bn.load()).bn_expert_product_int8_workspace_bytes(M, K)
+
+
+def _expert_product_int8(a: Int8, w: Int8, scale, out, workspace, stream) -> torch.Tensor:
+    M, K, ap, sp = _layout_int8(a, "a")
+    _, wK, wp, wsp = _layout_int8(w, "w")
+    dev = a.data.device
+    if a.data.dim() != 2:
+        raise ValueError("a.data must be [M, K]")
+    if w.offsets is not None:
+        raise ValueError("w must have equal groups (no offsets)")
+    if w.data.device != dev:
+        raise ValueError(f"w is on {w.data.device}, expected {dev}")
+    if wK != K:
+        raise ValueError(f"a has rows of {K} values, w of {wK}")
+    shape = w.data.shape
+    E, N = shape[:2] if len(shape) == 3 else (1, shape[0])
+    op = _groups(a.offsets, E, dev)
+    out, yp = _out(out, "out", torch.bfloat16, (M, N), dev, stream)
+    if workspace is not None:
+        xp, n = _bn._workspace(workspace, dev)
+    else:
+        n = product_int8_workspace_bytes(M, K)
+        workspace = torch.empty(n, dtype=_UINT8, device=dev) if stream is None else _bn._empty((n,), _UINT8, dev, stream)
+        xp = workspace.data_ptr()
+    _call("bn_expert_product_int8", (ap, sp, M, wp, wsp, E, N, K, op, scale, yp, xp, n), dev.index, stream)
     return out
