@@ -82,9 +82,9 @@ struct ProductArgs {
 
 // One product of an expert's linear layer.  Forward: out [M, F] = x [M, D] of rows of a
 // group times w [E, F, D]; input gradient: out [M, F] = dy [M, D] times w [E, D, F];
-// weight gradient: out [E, N, F] = dy [M, N] transposed times x [M, F], group by group.
+// weight gradient: out [E, F, K] = dy [M, F] transposed times x [M, K], group by group.
 struct LinearArgs {
-    int M, E, F, D, N;
+    int M, E, F, D, K;
     const int32_t *offsets;   // [E + 1] or null (E = 1, all rows)
     const int32_t *rows;      // [M] or null: the row of x at each place
     int x_rows;

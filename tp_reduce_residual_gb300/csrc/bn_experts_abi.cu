@@ -163,14 +163,14 @@ bn_status place_rows(LinearArgs &a, const void *&x, long long &ld, int K, void *
     return BN_OK;
 }
 
-LinearArgs linear_args(int dtype, int M, int E, int F, int D, int N, const int32_t *offsets, void *out, unsigned *err)
+LinearArgs linear_args(int dtype, int M, int E, int F, int D, int K, const int32_t *offsets, void *out, unsigned *err)
 {
     LinearArgs a = {};
     a.M = M;
     a.E = E;
     a.F = F;
     a.D = D;
-    a.N = N;
+    a.K = K;
     a.offsets = offsets;
     a.out = out;
     a.dtype = dtype;
@@ -547,7 +547,7 @@ bn_status bn_expert_linear_dw(const void *dy, bn_dtype dtype, long long ld_dy, i
     BN_TRY(check_overlaps(writes, 2, reads, 4));
     const DeviceInfo *d = nullptr;
     BN_TRY(device_info(&d));
-    LinearArgs a = linear_args(dtype, M, E, K, 0, N, offsets, dw, d->err);
+    LinearArgs a = linear_args(dtype, M, E, N, 0, K, offsets, dw, d->err);
     a.rows = rows;
     a.x_rows = x_rows;
     a.out_fp32 = dw_dtype == BN_FP32;

@@ -7,12 +7,14 @@
 //   weight gradient  dw[e, n, k] = sum_m dy[m, n] * x[rows[m], k]
 // y and dx of rows of no group are zeros, dw of an empty group too.
 //
-// One kernel in three modes.  The output's contiguous dimension (n, k, k: features) is
-// the tensor core's M operand and the other its N operand, so that the few rows an
-// expert has in a decode batch cost a narrow product and each weight is read once, and
-// so that all modes store alike.  What is summed over lies along the rows in memory
-// (forward: both operands; input gradient: dy) or across them (w there, both operands
-// of the weight gradient): the tensor core takes either, as a bit of its descriptor.
+// One kernel in three modes.  Forward and input gradient: the output's contiguous
+// dimension (n, k: features) is the tensor core's M operand and rows are its N operand, so
+// that the few rows an expert has in a decode batch cost a narrow product and each weight is
+// read once.  Weight gradient: n and k, so that a lane holds a part of a row of dw, which
+// goes out by TMA; its tiles are all whole and its sums short, so their way out counts.  What is
+// summed over lies along the rows in memory (forward: both operands; input gradient: dy)
+// or across them (w there, both operands of the weight gradient): the tensor core takes
+// either, as a bit of its descriptor.
 // Persistent CTAs walk the output tiles; stages of 64 values of the sum are filled by
 // TMA (128-byte swizzle), one thread issues the products, the output warps take an
 // accumulator out while the next one is filled.  Rows given by index are fetched four
@@ -38,36 +40,40 @@ constexpr int kAtom = 64 * 128; // bytes of 64 features or rows by 64 values, wh
 
 enum Shape { kOne = 0, kPair = 1, kSplit = 2 };
 
-template <int SHAPE>
+template <int SHAPE, bool WEIGHTS = false>
 struct LinearShape {
     static constexpr int kCtas = SHAPE == kPair ? 2 : 1;       // CTAs of one product
     static constexpr int kTile = SHAPE == kPair ? 256 : 128;   // features of an output tile
     static constexpr int kRows = SHAPE == kSplit ? 64 : kTile; // its rows
     static constexpr int kStep = SHAPE == kPair ? 32 : 16;     // rows of a product are rounded up to this
-    static constexpr int kStages = SHAPE == kSplit ? 7 : 6;
+    static constexpr int kStages = SHAPE == kSplit ? 7 : WEIGHTS ? 5 : 6;
     static constexpr int kOffQ = kHalf * 128;
     static constexpr int kStageBytes = kOffQ + kRows / kCtas * 128;
     static constexpr int kColumns = 2 * kRows;      // tensor memory: two accumulators
     static constexpr int kJoinBytes = SHAPE == kSplit ? (kRows + kMaxSplit) * kHalf * 4 : 0;  // parts of a split sum
     static constexpr int kOutWarps = SHAPE == kPair ? 8 : 4;
     static constexpr int kThreads = 64 + 32 * kOutWarps;  // copies, products, output
-    static constexpr size_t smem(int E) { return 1024 + (size_t)kStages * kStageBytes + kJoinBytes + 2 * sizeof(int) * (size_t)(E + 1); }
+    // output warps' boxes of 32 rows by 128 bytes on their way to a weight gradient
+    static constexpr int kOutBoxes = SHAPE == kPair ? 1 : 2;
+    static constexpr int kOutBytes = WEIGHTS ? kOutWarps * kOutBoxes * 4096 : 0;
+    static constexpr size_t smem(int E) { return 1024 + (size_t)kStages * kStageBytes + kOutBytes + kJoinBytes + 2 * sizeof(int) * (size_t)(E + 1); }
 };
 
 struct LinearMaps {
-    CUtensorMap p;                 // the features' operand: w, or x
-    CUtensorMap q, q_small;        // the rows' operand: x or dy, in boxes of 128 (64) and 16 rows
-    CUtensorMap p_rows, q_rows;    // row by row: x (and dy) of the weight gradient, x of the forward
+    CUtensorMap p;                 // the features' operand: w, or dy
+    CUtensorMap q, q_small;        // the rows' operand: x, or dy of the input gradient, in boxes of 128 (64) and 16 rows
+    CUtensorMap p_rows, q_rows;    // row by row: dy and x of the weight gradient, x of the forward
     CUtensorMap p16, p4, q16, q4;  // the weight gradient's in boxes of 16 and 4 rows
+    CUtensorMap out;               // the weight gradient in boxes of 32 rows by 128 bytes
 };
 
-// The weight gradient's tiles: experts one after another, of one expert the row tiles
-// (of N) of a feature tile next to each other.
+// The weight gradient's tiles: experts one after another, of one expert the tiles along a
+// row (of K) of a feature tile (of N) next to each other.
 template <int TILE>
 class WeightTiles {
 public:
-    __device__ WeightTiles(int E, int N, int F, unsigned first, unsigned step)
-        : tiles_r_((unsigned)(N + TILE - 1) / TILE), tiles_f_((unsigned)(F + TILE - 1) / TILE), N_(N), step_(step), id_(first),
+    __device__ WeightTiles(int E, int K, int F, unsigned first, unsigned step)
+        : tiles_r_((unsigned)(K + TILE - 1) / TILE), tiles_f_((unsigned)(F + TILE - 1) / TILE), K_(K), step_(step), id_(first),
           total_((unsigned long long)tiles_r_ * tiles_f_ * (unsigned)E)
     {
     }
@@ -79,14 +85,14 @@ public:
         t.e = (int)e;
         t.f = (int)(local / tiles_r_);
         t.row0 = (int)(local - (unsigned)t.f * tiles_r_) * TILE;
-        t.rows = min(TILE, N_ - t.row0);
+        t.rows = min(TILE, K_ - t.row0);
         id_ += step_;
         return true;
     }
 
 private:
     unsigned tiles_r_, tiles_f_;
-    int N_;
+    int K_;
     unsigned step_;
     unsigned long long id_, total_;
 };
@@ -125,7 +131,7 @@ template <int MODE, int SHAPE, bool GATHER>
 __global__ void __launch_bounds__(LinearShape<SHAPE>::kThreads, 1)
 linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearArgs p)
 {
-    using S = LinearShape<SHAPE>;
+    using S = LinearShape<SHAPE, MODE == kWeightGrad>;
     constexpr bool PAIR = SHAPE == kPair, SPLIT = SHAPE == kSplit;
     constexpr int kStages = S::kStages, kTile = S::kTile, kRows = S::kRows;
     constexpr bool kWeights = MODE == kWeightGrad;
@@ -136,7 +142,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     __shared__ int4 quads[32];  // row indexes of the copying warp
-    float *parts = reinterpret_cast<float *>(raw + (base - smem_addr(raw)) + kStages * S::kStageBytes);
+    float *parts = reinterpret_cast<float *>(raw + (base - smem_addr(raw)) + kStages * S::kStageBytes + S::kOutBytes);
     int *start = reinterpret_cast<int *>(parts) + S::kJoinBytes / 4;
     int *cum = start + p.E + 1;
     const int warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
@@ -189,7 +195,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
     ctl.pipe_polls = kMaxSpins;
     auto tiles = [&]() {
         if constexpr (kWeights)
-            return WeightTiles<kTile>(p.E, p.N, p.F, (unsigned)unit, (unsigned)units);
+            return WeightTiles<kTile>(p.E, p.K, p.F, (unsigned)unit, (unsigned)units);
         else
             return Tiles<kRows>(start, cum, p.E, (unsigned)((p.F + kTile - 1) / kTile), (unsigned)unit, (unsigned)units);
     }();
@@ -289,45 +295,40 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                     const uint32_t p_bytes = 2u * 128u * (uint32_t)live, q_bytes = (uint32_t)(q_atoms * 128 * live);
                     if (elect_one()) {
                         if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, S::kCtas * (p_bytes + q_bytes));
-                        if (!GATHER && !tail) {
-                            tma_2d<PAIR>(at, &maps.p, f0, m0, bar);
-                            tma_2d<PAIR>(at + kAtom, &maps.p, f0 + 64, m0, bar);
-                        }
-                        if (!tail) {
-                            tma_2d<PAIR>(q, &maps.q, b0, m0, bar);
-                            if (q_atoms == 2) tma_2d<PAIR>(q + kAtom, &maps.q, b0 + 64, m0, bar);
-                        }
+                        // rows i and on of this stage, of dy and (unless rows come by index) of x
+                        const auto box = [&](const CUtensorMap *mp, const CUtensorMap *mq, int i, int y) {
+                            tma_2d<PAIR>(at + i * 128, mp, f0, y, bar);
+                            tma_2d<PAIR>(at + kAtom + i * 128, mp, f0 + 64, y, bar);
+                            if (!GATHER) {
+                                tma_2d<PAIR>(q + i * 128, mq, b0, y, bar);
+                                if (q_atoms == 2) tma_2d<PAIR>(q + kAtom + i * 128, mq, b0 + 64, y, bar);
+                            }
+                        };
                         if constexpr (GATHER) {
 #pragma unroll 4
                             for (int i = 0; i < live / 4; ++i) {
                                 const int4 y = quads[i];
-                                tma_rows<PAIR>(at + i * 512, &maps.p_rows, f0, y, bar);
-                                tma_rows<PAIR>(at + kAtom + i * 512, &maps.p_rows, f0 + 64, y, bar);
+                                tma_rows<PAIR>(q + i * 512, &maps.q_rows, b0, y, bar);
+                                if (q_atoms == 2) tma_rows<PAIR>(q + kAtom + i * 512, &maps.q_rows, b0 + 64, y, bar);
                             }
                         }
-                        if (tail) {
+                        if (!tail) {
+                            box(&maps.p, &maps.q, 0, m0);
+                        } else {
                             // 16 rows at a time while all are the group's, then 4 (past it: boxes
                             // outside the map, zeros); four that the group's end cuts, by index
-                            const auto box = [&](const CUtensorMap *mp, const CUtensorMap *mq, int i, int y) {
-                                if (!GATHER) {
-                                    tma_2d<PAIR>(at + i * 128, mp, f0, y, bar);
-                                    tma_2d<PAIR>(at + kAtom + i * 128, mp, f0 + 64, y, bar);
-                                }
-                                tma_2d<PAIR>(q + i * 128, mq, b0, y, bar);
-                                if (q_atoms == 2) tma_2d<PAIR>(q + kAtom + i * 128, mq, b0 + 64, y, bar);
-                            };
                             const int left = d - r0;
                             int i = 0;
                             for (; i + 16 <= left; i += 16) box(&maps.p16, &maps.q16, i, m0 + i);
                             for (; i + 4 <= left; i += 4) box(&maps.p4, &maps.q4, i, m0 + i);
                             if (i < left) {
                                 const int4 y = {m0 + i, i + 1 < left ? m0 + i + 1 : p.M, i + 2 < left ? m0 + i + 2 : p.M, p.M};
+                                tma_rows<PAIR>(at + i * 128, &maps.p_rows, f0, y, bar);
+                                tma_rows<PAIR>(at + kAtom + i * 128, &maps.p_rows, f0 + 64, y, bar);
                                 if (!GATHER) {
-                                    tma_rows<PAIR>(at + i * 128, &maps.p_rows, f0, y, bar);
-                                    tma_rows<PAIR>(at + kAtom + i * 128, &maps.p_rows, f0 + 64, y, bar);
+                                    tma_rows<PAIR>(q + i * 128, &maps.q_rows, b0, y, bar);
+                                    if (q_atoms == 2) tma_rows<PAIR>(q + kAtom + i * 128, &maps.q_rows, b0 + 64, y, bar);
                                 }
-                                tma_rows<PAIR>(q + i * 128, &maps.q_rows, b0, y, bar);
-                                if (q_atoms == 2) tma_rows<PAIR>(q + kAtom + i * 128, &maps.q_rows, b0 + 64, y, bar);
                                 i += 4;
                             }
                             for (; i < live; i += 4) box(&maps.p4, &maps.q4, i, p.M);
@@ -402,17 +403,16 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
         const int quad = warp & 3;         // the lanes of tensor memory that this warp reads
         const int half = (warp - 2) >> 2;  // of a pair's columns
         const bool fp16 = p.dtype == BN_FP16;
-        uint32_t n = 0;
+        uint32_t n = 0, stored = 0;
         for (; tiles.next(t, lane); ++n) {
             const uint32_t buf = n & 1u;
             // this warp's columns: at most 128
             const int cut = PAIR ? (t.rows + 31) / 32 * 16 : t.rows;
             const int lo = half ? cut : 0, hi = half ? t.rows : min(cut, t.rows);
-            const bool none = kWeights && depth() == 0;  // an empty group
             if (!__all_sync(kAll, wait_phase<PAIR, kPipe>(acc_full + 8 * buf, (n >> 1) & 1u, ctl))) break;
             fence_after();
             const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + buf * kRows;
-            const long long row0 = kWeights ? (long long)t.e * p.N + t.row0 : t.row0;
+            const long long row0 = t.row0;
             const int f0 = t.f * kTile + (int)rank * kHalf + quad * 32;
             const auto release = [&]() {
                 fence_before();
@@ -460,57 +460,89 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 }
                 __syncwarp();
                 if (lane < (int)parts_n) arrive_cluster(mapa(joinable, (uint32_t)lane));
-                continue;
-            }
-            if (kWeights && p.out_fp32) {  // a lane's feature, row by row: 128 bytes a warp
-                float *out = static_cast<float *>(p.out) + row0 * p.F + f0 + lane;
-                const bool mine = f0 + lane < p.F;
-                for (int c0 = lo; c0 < hi; c0 += 16) {
-                    uint32_t v[16];
-                    read16(acc + c0, v);
-                    if (c0 + 16 >= hi) release();
-                    if (mine) {
-                        float old[16];
+            } else if constexpr (kWeights) {
+                // A lane's row of dw, 128 bytes of it at a time through shared memory to a box of
+                // 32 rows; what lies past the matrix is not stored.  Each half has 128 columns.
+                const bool none = depth() == 0;  // an empty group: zeros, or nothing to add
+                const int width = p.out_fp32 ? 32 : 64;
+                const uint32_t boxes = base + kStages * S::kStageBytes + (uint32_t)(warp - 2) * S::kOutBoxes * 4096u;
+                const int end = none && p.accumulate ? 0 : min(half * 128 + 128, t.rows);
+                for (int c = half * 128; c < end; c += width) {
+                    const uint32_t at = boxes + (uint32_t)(stored++ % S::kOutBoxes) * 4096u;
+                    uint32_t v[32];
 #pragma unroll
-                        for (int i = 0; i < 16; ++i)
-                            old[i] = p.accumulate && c0 + i < hi ? out[(long long)(c0 + i) * p.F] : 0.0f;
+                    for (int b = 0; b < 2; ++b) {
+                        uint32_t x[16];
+                        if (p.out_fp32) {
+                            read16(acc + c + 16 * b, x);
 #pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const float sum = none ? 0.0f : __uint_as_float(v[i]);
-                            if (c0 + i < hi) out[(long long)(c0 + i) * p.F] = p.accumulate ? old[i] + sum : sum;
+                            for (int i = 0; i < 16; ++i) v[16 * b + i] = x[i];
+                        } else {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                read16(acc + c + 32 * b + 16 * h, x);
+#pragma unroll
+                                for (int i = 0; i < 8; ++i)
+                                    v[16 * b + 8 * h + i] = round16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), fp16);
+                            }
                         }
                     }
+                    if (c + width >= end) release();
+                    // the copy that read this box last has ended
+                    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(S::kOutBoxes - 1) : "memory");
+                    __syncwarp();
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const uint4 w = none ? make_uint4(0, 0, 0, 0) : make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
+                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (uint32_t)lane * 128u + (uint32_t)((i ^ (lane & 7)) << 4)),
+                                     "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+                    }
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
+                    if (lane == 0) {  // always this lane: copies are counted by thread
+                        if (f0 < p.F) {
+                            if (p.accumulate)
+                                asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&maps.out),
+                                             "r"(t.row0 + c), "r"(f0), "r"(t.e), "r"(at) : "memory");
+                            else
+                                asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&maps.out),
+                                             "r"(t.row0 + c), "r"(f0), "r"(t.e), "r"(at) : "memory");
+                        }
+                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    }
                 }
-                if (lo >= hi) release();
-                continue;
-            }
-            // the whole tile in 16 bits in registers, so that the next product can start
-            uint32_t packed[8][8];
+                if (half * 128 >= end) release();
+            } else {
+                // the whole tile in 16 bits in registers, so that the next product can start
+                uint32_t packed[8][8];
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                if (lo + 16 * b < hi) {
-                    uint32_t v[16];
-                    read16(acc + lo + 16 * b, v);
+                for (int b = 0; b < 8; ++b) {
+                    if (lo + 16 * b < hi) {
+                        uint32_t v[16];
+                        read16(acc + lo + 16 * b, v);
 #pragma unroll
-                    for (int i = 0; i < 8; ++i)
-                        packed[b][i] = none ? 0u : round16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), fp16);
+                        for (int i = 0; i < 8; ++i)
+                            packed[b][i] = round16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), fp16);
+                    }
                 }
-            }
-            release();
-            const int f = f0 + (lane & ~7);
-            uint16_t *out = static_cast<uint16_t *>(p.out) + (row0 + (lane & 7)) * p.F + f;
+                release();
+                const int f = f0 + (lane & ~7);
+                uint16_t *out = static_cast<uint16_t *>(p.out) + (row0 + (lane & 7)) * p.F + f;
 #pragma unroll
-            for (int b = 0; b < 8; ++b) {
-                if (lo + 16 * b < hi) {
+                for (int b = 0; b < 8; ++b) {
+                    if (lo + 16 * b < hi) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        const uint4 v = transpose8(packed[b] + 4 * h, lane);
-                        const int c = lo + 16 * b + 8 * h;
-                        if (c + (lane & 7) < hi && f < p.F) *reinterpret_cast<uint4 *>(out + (long long)c * p.F) = v;
+                        for (int h = 0; h < 2; ++h) {
+                            const uint4 v = transpose8(packed[b] + 4 * h, lane);
+                            const int c = lo + 16 * b + 8 * h;
+                            if (c + (lane & 7) < hi && f < p.F) *reinterpret_cast<uint4 *>(out + (long long)c * p.F) = v;
+                        }
                     }
                 }
             }
         }
+        // the last boxes have left shared memory, and are written
+        if constexpr (kWeights) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if constexpr (!kWeights) {  // rows of no group: before the first, and past the last
             const long long step = (long long)gridDim.x * (S::kThreads - 64);
             uint4 *out = static_cast<uint4 *>(p.out);
@@ -543,14 +575,17 @@ cudaError_t make_linear_maps(LinearMaps *m, const LinearArgs &p, LinearMode mode
     cudaError_t e;
     if (mode == kWeightGrad) {
         const long long n = p.rows ? p.x_rows : p.M;
-        e = matrix(&m->p, x, n, p.F, ld, kDepth);
-        if (e == cudaSuccess) e = matrix(&m->p_rows, x, n, p.F, ld, 1);
-        if (e == cudaSuccess) e = matrix(&m->q, w, p.M, p.N, w_ld, kDepth);
-        if (e == cudaSuccess) e = matrix(&m->q_rows, w, p.M, p.N, w_ld, 1);
-        if (e == cudaSuccess) e = matrix(&m->p16, x, n, p.F, ld, 16);
-        if (e == cudaSuccess) e = matrix(&m->p4, x, n, p.F, ld, 4);
-        if (e == cudaSuccess) e = matrix(&m->q16, w, p.M, p.N, w_ld, 16);
-        if (e == cudaSuccess) e = matrix(&m->q4, w, p.M, p.N, w_ld, 4);
+        e = matrix(&m->p, w, p.M, p.F, w_ld, kDepth);
+        if (e == cudaSuccess) e = matrix(&m->p_rows, w, p.M, p.F, w_ld, 1);
+        if (e == cudaSuccess) e = matrix(&m->p16, w, p.M, p.F, w_ld, 16);
+        if (e == cudaSuccess) e = matrix(&m->p4, w, p.M, p.F, w_ld, 4);
+        if (e == cudaSuccess) e = matrix(&m->q, x, n, p.K, ld, kDepth);
+        if (e == cudaSuccess) e = matrix(&m->q_rows, x, n, p.K, ld, 1);
+        if (e == cudaSuccess) e = matrix(&m->q16, x, n, p.K, ld, 16);
+        if (e == cudaSuccess) e = matrix(&m->q4, x, n, p.K, ld, 4);
+        if (e == cudaSuccess)
+            e = make_map<3>(&m->out, p.out_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, p.out_fp32 ? 4 : 2, p.out,
+                            {(cuuint64_t)p.K, (cuuint64_t)p.F, (cuuint64_t)p.E}, {p.out_fp32 ? 32u : 64u, 32, 1}, CU_TENSOR_MAP_SWIZZLE_128B);
         m->q_small = m->q;
         return e;
     }
@@ -559,12 +594,12 @@ cudaError_t make_linear_maps(LinearMaps *m, const LinearArgs &p, LinearMode mode
                     CU_TENSOR_MAP_SWIZZLE_128B);
     if (p.rows) {
         if (e == cudaSuccess) e = matrix(&m->q_rows, x, p.x_rows, p.D, ld, 1);
-        m->q = m->q_small = m->p_rows = m->p16 = m->p4 = m->q16 = m->q4 = m->q_rows;
+        m->out = m->q = m->q_small = m->p_rows = m->p16 = m->p4 = m->q16 = m->q4 = m->q_rows;
         return e;
     }
     if (e == cudaSuccess) e = matrix(&m->q, x, p.M, p.D, ld, kHalf);
     if (e == cudaSuccess) e = matrix(&m->q_small, x, p.M, p.D, ld, kBoxRows);
-    m->p_rows = m->q_rows = m->p16 = m->p4 = m->q16 = m->q4 = m->q_small;
+    m->out = m->p_rows = m->q_rows = m->p16 = m->p4 = m->q16 = m->q4 = m->q_small;
     return e;
 }
 
@@ -575,7 +610,7 @@ long long most_tiles(const LinearArgs &p, int mode)
 {
     using S = LinearShape<SHAPE>;
     const long long groups = p.E < p.M ? p.E : p.M;
-    const long long rows = mode == kWeightGrad ? (long long)p.E * ((p.N + S::kRows - 1) / S::kRows)
+    const long long rows = mode == kWeightGrad ? (long long)p.E * ((p.K + S::kRows - 1) / S::kRows)
                                                : ((long long)p.M + groups * (S::kRows - 1)) / S::kRows;
     return rows * ((p.F + S::kTile - 1) / S::kTile);
 }
@@ -583,7 +618,7 @@ long long most_tiles(const LinearArgs &p, int mode)
 template <int MODE, int SHAPE, bool GATHER>
 cudaError_t launch_shape(const LinearArgs &p, const LinearMaps &maps, int sms, bool pdl, cudaStream_t st)
 {
-    using S = LinearShape<SHAPE>;
+    using S = LinearShape<SHAPE, MODE == kWeightGrad>;
     static KernelSetup setup;
     auto *k = linear_kernel<MODE, SHAPE, GATHER>;
     const cudaError_t e = setup(k, (int)S::smem(kMaxExperts));
@@ -612,7 +647,7 @@ int choose_shape(LinearArgs &p, int mode, int sms)
     const long long groups = p.E < p.M ? p.E : p.M;
     const auto rounds = [&](int tile, int units) {
         const long long even = p.M / tile + groups / 2;
-        const long long rows = mode == kWeightGrad ? (long long)p.E * ((p.N + tile - 1) / tile) : even > groups ? even : groups;
+        const long long rows = mode == kWeightGrad ? (long long)p.E * ((p.K + tile - 1) / tile) : even > groups ? even : groups;
         return (rows * ((p.F + tile - 1) / tile) + units - 1) / units;
     };
     p.split = 1;
