@@ -450,7 +450,7 @@ BN_API size_t bn_expert_linear_workspace_bytes(int M, int K);
  *            leave [0, M] set BN_DEVERR_OFFSETS; they are clamped
  * Rows of y and dx before the first offset and past the last are zeros; such rows of
  * x and dy are not read into any result.  dw of an empty group is zeros.  N and K are
- * multiples of 8.
+ * multiples of 8, at most 2^20, and N * K at most 2^37.
  *   workspace  device memory of workspace_bytes, 16-byte aligned, or NULL; used when rows
  *            is given and it holds bn_expert_linear_workspace_bytes() (not 0), for two
  *            kernels on `stream` instead of one: rows go to their places there first.

@@ -229,3 +229,94 @@ def test_split_sums(sizes, N, K, gather):
     t = dict(d, w=d["w"].transpose(1, 2).contiguous(), x=d["dy"], dy=d["x"] if not gather else d["x"][d["rows"].long()], rows=None)
     check(t, whole=True)
     check(make(sizes, N, K, "fp16", whole=False, gather=gather), whole=False)
+
+
+def test_offsets_past_32_bits():
+    """Rows, weights and gradients whose elements lie beyond 2^31."""
+    g = torch.Generator(device="cuda").manual_seed(5)
+    M, N, K = 270000, 8192, 16
+    x, w = values((M, K), torch.bfloat16, g, True), values((N, K), torch.bfloat16, g, True)
+    y = experts.expert_linear(x, w)
+    for s in (slice(0, 3), slice(131070, 131080), slice(262140, 262150), slice(M - 3, M)):
+        assert torch.equal(y[s], (x[s].double() @ w.double().T).bfloat16())
+    wide = experts.expert_linear_dw(y[:, :64], y)  # rows of dy and x far apart
+    assert wide.shape == (64, N) and torch.isfinite(wide).all()
+    dx = experts.expert_linear_dx(y, w)  # sums past 2^24: to FP32 rounding
+    want = y[M - 2:].double() @ w.double()
+    assert ((dx[M - 2:].double() - want).abs() <= 2.0 ** -8 * want.abs() + N * 2.0 ** -23 * (y[M - 2:].double().abs() @ w.double().abs())).all()
+    del x, w, y, wide, dx
+    E, N, K = 40, 8192, 8192
+    w = torch.zeros(E, N, K, dtype=torch.bfloat16, device="cuda")
+    w[-1] = values((N, K), torch.bfloat16, g, True)
+    o = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    o[E - 1], o[E] = 2, 40
+    x, dy = values((40, K), torch.bfloat16, g, True), values((40, N), torch.bfloat16, g, True)
+    y, dx = experts.expert_linear(x, w, o), experts.expert_linear_dx(dy, w, o)
+    dw = experts.expert_linear_dw(dy, x, o)
+    assert torch.equal(y[2:], (x[2:].double() @ w[-1].double().T).bfloat16()) and torch.equal(dx[2:], (dy[2:].double() @ w[-1].double()).bfloat16())
+    assert (y[:2] == 0).all() and (dx[:2] == 0).all() and (dw[0] == 0).all()
+    assert torch.equal(dw[-1], (dy[2:].double().T @ x[2:].double()).bfloat16())
+
+
+def test_streams():
+    """Calls on a stream of the caller's, with outputs and workspace from its pool, and two at once."""
+    d = make([300, 0, 500], 512, 256, "bf16", gather=True)
+    want = [v.bfloat16() for v in exact(d)]
+    a, b = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = []
+    for _ in range(4):
+        for s in (a, b):
+            got.append((s, experts.expert_linear(d["x"], d["w"], d["offsets"], rows=d["rows"], stream=s),
+                        experts.expert_linear_dx(d["dy"], d["w"], d["offsets"], stream=s.cuda_stream),
+                        experts.expert_linear_dw(d["dy"], d["x"], d["offsets"], rows=d["rows"], stream=s)))
+    a.synchronize()
+    b.synchronize()
+    for _, *v in got:
+        assert all(torch.equal(x, y) for x, y in zip(v, want))
+
+
+def test_equal_calls_give_equal_bits():
+    for sizes, N, K in (([200, 31, 900], 264, 1032), ([5], 72, 4096)):
+        d = make(sizes, N, K, "bf16", whole=False)
+        first = run(d, torch.float32)
+        for _ in range(3):
+            assert all(torch.equal(a, b) for a, b in zip(run(d, torch.float32), first))
+
+
+def test_gradients_against_differences():
+    """The forward's own change along the gradients, in FP32 sums of BF16 values."""
+    d = make([30, 0, 50], 64, 96, "bf16", whole=False, seed=11)
+    y, dx, dw = run(d, torch.float32)
+    x, w, dy = d["x"].double(), d["w"].double(), d["dy"].double()
+    o = d["offsets"].tolist()
+
+    def value(x, w):
+        return sum((x[o[e]:o[e + 1]] @ w[e].T * dy[o[e]:o[e + 1]]).sum() for e in range(3))
+
+    for which, v in (("x", dx.double()), ("w", dw.double())):
+        v = v / v.norm()
+        ends = [value(x + s * v, w) if which == "x" else value(x, w + s * v) for s in (0.5, -0.5)]  # linear: any step
+        want = ((dx if which == "x" else dw).double() * v).sum()
+        assert abs(ends[0] - ends[1] - want) <= 2.0 ** -8 * abs(want)
+
+
+def test_captured_and_replayed():
+    d = make([90, 0, 40], 136, 264, "bf16", gather=True)
+    run(d)
+    torch.cuda.synchronize()
+    graphs = []
+    for _ in range(2):  # two graphs with workspaces of their own
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = run(d)
+        graphs.append((g, out))
+    for seed in range(3):
+        n = make([90, 0, 40], 136, 264, "bf16", gather=True, seed=seed + 20)
+        for k in ("x", "w", "dy", "rows"):
+            d[k].copy_(n[k])
+        for g, _ in graphs:
+            g.replay()
+        want = exact(d)
+        for _, out in graphs:
+            assert all(torch.equal(a, b.bfloat16()) for a, b in zip(out, want))

@@ -133,3 +133,43 @@ def test_workspace_and_offsets():
     assert bn.check_device_error(raise_on_error=False) == bn.DEVERR_OFFSETS
     empty = experts.Int8(a.data[:0], a.scales[:0], torch.zeros(3, dtype=torch.int32, device="cuda"))
     assert experts.expert_product(empty, w).shape == (0, 64)
+
+
+def test_offsets_past_32_bits():
+    M, N, K = 270000, 8192, 16
+    a, w = make([M], N, K)
+    out = experts.expert_product(a, w)
+    for lo, hi in ((0, 3), (131070, 131080), (262140, 262150), (M - 3, M)):
+        part = experts.Int8(a.data[lo:hi], a.scales[lo:hi], torch.tensor([0, hi - lo], dtype=torch.int32))
+        assert torch.equal(out[lo:hi], expected(part, w))
+    del a, w, out
+    E, N, K = 40, 8192, 8192
+    w = experts.Int8(torch.zeros(E, N, K, dtype=torch.int8, device="cuda"), torch.ones(E, N, device="cuda"))
+    w.data[-1] = torch.randint(-128, 128, (N, K), device="cuda").to(torch.int8)
+    o = torch.zeros(E + 1, dtype=torch.int32, device="cuda")
+    o[E - 1], o[E] = 2, 40
+    a = experts.Int8(torch.randint(-128, 128, (40, K), device="cuda").to(torch.int8), torch.rand(40, device="cuda"), o)
+    check(a, w)
+
+
+def test_streams_and_graphs():
+    a, w = make([300, 0, 500], 512, 256)
+    want = expected(a, w)
+    s, t = torch.cuda.Stream(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    got = [experts.expert_product(a, w, stream=x) for _ in range(4) for x in (s, t)]
+    s.synchronize()
+    t.synchronize()
+    assert all(torch.equal(x, want) for x in got)
+    graphs = []
+    for _ in range(2):  # two graphs with workspaces of their own
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            out = experts.expert_product(a, w)
+        graphs.append((g, out))
+    for seed in range(3):
+        n, _ = make([300, 0, 500], 512, 256, seed=seed + 9)
+        a.data.copy_(n.data)
+        for g, _ in graphs:
+            g.replay()
+        assert all(torch.equal(out, expected(a, w)) for _, out in graphs)

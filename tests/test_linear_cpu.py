@@ -34,7 +34,7 @@ LINEAR = dict(x=at(0), dtype=0, ld=64, x_rows=20, rows=at(1), M=40, w=at(2), E=4
 @pytest.mark.parametrize("kw,status,needle", [
     (dict(dtype=2), 1, "dtype 2"), (dict(dtype=7), 1, "dtype 7"), (dict(M=-1), 1, "M=-1"), (dict(E=0), 1, "E=0"), (dict(E=1025), 2, "E=1025"),
     (dict(N=12), 1, "N=12"), (dict(N=0), 1, "N=0"), (dict(K=60), 1, "K=60"), (dict(K=1 << 21, ld=1 << 21), 2, "above the served"),
-    (dict(N=1 << 21), 2, "above the served"), (dict(M=2 ** 31 - 8), 2, "M="), (dict(ld=60), 1, "ld=60"), (dict(ld=68), 1, "ld=68"),
+    (dict(N=1 << 21), 2, "above the served"), (dict(N=1 << 20, K=1 << 18, ld=1 << 18), 2, "N * K"), (dict(M=2 ** 31 - 8), 2, "M="), (dict(ld=60), 1, "ld=60"), (dict(ld=68), 1, "ld=68"),
     (dict(ld=1 << 40), 2, "ld="), (dict(rows=None), 1, "no rows are given"), (dict(x_rows=0), 1, "no rows"), (dict(x_rows=-1), 1, "x_rows=-1"),
     (dict(offsets=None), 1, "offsets is NULL"), (dict(offsets=at(3) + 2), 1, "offsets is not"), (dict(x=None), 1, "x is NULL"),
     (dict(x=at(0) + 8), 1, "x is not 16-byte"), (dict(rows=at(1) + 1), 1, "rows"), (dict(w=None), 1, "w is NULL"), (dict(y=None), 1, "y is NULL"),

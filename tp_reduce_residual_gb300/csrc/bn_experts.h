@@ -144,7 +144,7 @@ cudaError_t launch_linear(const LinearArgs &, LinearMode mode, const void *x, lo
 
 cudaError_t launch_swiglu(const SwigluArgs &, int dtype, bool backward, int sms, bool pdl, cudaStream_t);
 cudaError_t launch_quantize_int8(const Int8Args &, int dtype, bool pdl, cudaStream_t);
-cudaError_t launch_dequantize_int8(const Int8Args &, int dtype, int sms, bool pdl, cudaStream_t);
+cudaError_t launch_dequantize_int8(const Int8Args &, int dtype, bool pdl, cudaStream_t);
 // workspace: 2 M K bytes, for the rows widened to FP16.
 cudaError_t launch_product8(Product8Args, const int8_t *a, const int8_t *w, void *workspace, int sms, bool pdl, cudaStream_t);
 // out [M, K] dense: row rows[m] of x at place m (16-bit values).

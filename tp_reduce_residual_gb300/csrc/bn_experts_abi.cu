@@ -116,6 +116,8 @@ bn_status check_linear(int dtype, int M, int E, int N, int K, const int32_t *off
     if (M > kMaxRows) return fail(BN_ERR_UNSUPPORTED, "M=%d above the served maximum %lld", M, kMaxRows);
     if (N > (1 << 20) || K > (1 << 20))
         return fail(BN_ERR_UNSUPPORTED, "N=%d, K=%d: above the served maximum %d", N, K, 1 << 20);
+    if ((long long)N * K > (1LL << 37))  // an expert's bytes in a tensor map
+        return fail(BN_ERR_UNSUPPORTED, "N * K=%lld above the served maximum %lld", (long long)N * K, 1LL << 37);
     return BN_OK;
 }
 
@@ -665,7 +667,7 @@ bn_status bn_dequantize_int8(const int8_t *data, const float *scales, int M, int
     a.data = const_cast<int8_t *>(data);
     a.scales = const_cast<float *>(scales);
     a.out = out;
-    return launched(launch_dequantize_int8(a, dtype, d->sms, dependent_launch(), (cudaStream_t)stream),
+    return launched(launch_dequantize_int8(a, dtype, dependent_launch(), (cudaStream_t)stream),
                     "launching dequantize_int8");
 }
 

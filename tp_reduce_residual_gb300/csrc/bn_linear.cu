@@ -681,14 +681,14 @@ __global__ void __launch_bounds__(256) place_rows_kernel(const uint4 *x, long lo
     griddep_launch_dependents();
     griddep_wait();
     const int lane = threadIdx.x & 31, warps = (int)gridDim.x * 8;
-    for (int m = (int)blockIdx.x * 8 + ((int)threadIdx.x >> 5); m < M; m += warps) {
+    for (long long m = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); m < M; m += warps) {
         int r = __ldg(rows + m);
         if ((unsigned)r >= (unsigned)x_rows) {
             if (lane == 0) atomicOr(err, BN_DEVERR_PERM_RANGE);
             r = 0;
         }
         const uint4 *from = x + (long long)r * ld;
-        uint4 *to = out + (long long)m * vectors;
+        uint4 *to = out + m * vectors;
         int i = lane;
         for (; i + 96 < vectors; i += 128) {
             uint4 v[4];

@@ -274,7 +274,7 @@ inline int choose_split(long long tiles, long long stages, long long join, long 
     int best = 1;
     long long least = whole * 9;
     for (int s = 2; s <= kMaxSplit && s * 4 <= stages; ++s) {
-        const long long units = sms / s, cost = (tiles + units - 1) / units * ((stages + s - 1) / s + join) * 10;
+        const long long units = sms > s ? sms / s : 1, cost = (tiles + units - 1) / units * ((stages + s - 1) / s + join) * 10;
         if (cost < least) {
             least = cost;
             best = s;

@@ -389,7 +389,8 @@ def expert_linear(x, w, offsets=None, rows=None, out=None, workspace=None, strea
     groups, ``rows`` (int32 [M]) the row of x at each place, as ``plan`` gives them;
     without ``rows`` x is grouped already.  Rows of no group are zeros.  More than a few
     rows by index go through a ``workspace`` (a 1-D uint8 tensor of
-    ``linear_workspace_bytes``; by default one is allocated for the call)."""
+    ``linear_workspace_bytes``; by default one is allocated for the call).  One
+    workspace serves one call at a time."""
     ld = _stride(x, "x")
     dev = x.device
     dtype = _dtype(x, "x", fp32=False)
