@@ -120,6 +120,7 @@ struct Int8Args {
 struct Product8Args {
     int M, E, N, K;
     const int32_t *offsets;   // [E + 1] or null (E = 1, all rows)
+    const int8_t *a;          // [M, K]
     const float *a_scales;    // [M]
     const float *w_scales;    // [E, N]
     float alpha;
@@ -145,8 +146,8 @@ cudaError_t launch_linear(const LinearArgs &, LinearMode mode, const void *x, lo
 cudaError_t launch_swiglu(const SwigluArgs &, int dtype, bool backward, int sms, bool pdl, cudaStream_t);
 cudaError_t launch_quantize_int8(const Int8Args &, int dtype, bool pdl, cudaStream_t);
 cudaError_t launch_dequantize_int8(const Int8Args &, int dtype, bool pdl, cudaStream_t);
-// workspace: 2 M K bytes, for the rows widened to FP16.
-cudaError_t launch_product8(Product8Args, const int8_t *a, const int8_t *w, void *workspace, int sms, bool pdl, cudaStream_t);
+// workspace: 2 M K bytes, for the rows widened to FP16 (large groups).
+cudaError_t launch_product8(Product8Args, const int8_t *w, void *workspace, int sms, bool pdl, cudaStream_t);
 // out [M, K] dense: row rows[m] of x at place m (16-bit values).
 cudaError_t launch_place_rows(const void *x, long long ld, int x_rows, const int32_t *rows, int M, int K, void *out, unsigned *err,
                               int sms, bool pdl, cudaStream_t);

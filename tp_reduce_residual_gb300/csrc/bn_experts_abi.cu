@@ -713,12 +713,13 @@ bn_status bn_expert_product_int8(const int8_t *a, const float *a_scales, int M, 
     p.N = N;
     p.K = K;
     p.offsets = offsets;
+    p.a = a;
     p.a_scales = a_scales;
     p.w_scales = w_scales;
     p.alpha = alpha;
     p.out = out;
     p.err = d->err;
-    return launched(launch_product8(p, a, w, workspace, d->sms, dependent_launch(), (cudaStream_t)stream),
+    return launched(launch_product8(p, w, workspace, d->sms, dependent_launch(), (cudaStream_t)stream),
                     "launching expert_product_int8");
 }
 

@@ -8,17 +8,27 @@
 // whole numbers up to 2048 are exact in FP16, so codes are widened to FP16 on the
 // way to the tensor core: a product of two is at most 2^14, and 1024 of them sum
 // exactly in its FP32 accumulator.  After every 1024 the output warps add the
-// accumulator to 32-bit integers in registers.
+// accumulator to 32-bit integers in registers, while the other accumulator is filled.
 //
 // Weights are the tensor core's M operand.  They come to shared memory as codes (TMA,
-// 128-byte swizzle, 128 values of K a stage); four warps widen them, a lane a weight
-// row, into tensor memory, from where the tensor core takes its M operand: so they pass
-// through shared memory as bytes only.  Rows are widened by a kernel ahead into a
-// workspace (2 bytes a code, once, where every feature tile reads them again).
+// 128-byte swizzle, 128 values of K a stage); eight warps widen them, a lane a weight
+// row, every second stage, into tensor memory, from where the tensor core takes its M
+// operand: so they pass through shared memory as bytes only.
 //
-// Two shapes.  Narrow: one CTA, tiles of 128 features by 32 rows, two accumulators; where
-// one round of tiles leaves CTAs idle, clusters of CTAs each sum a part of K.  A pair of
-// CTAs (cta_group::2): tiles of 256 by 128, of which each CTA loads half of either operand.
+// Two shapes.  Narrow: one CTA, tiles of 128 features by 32 rows, whose codes two more warps
+// widen into shared memory; where tiles are too few for the device, clusters of CTAs each
+// sum a part of K.  Pairs of CTAs (cta_group::2): tiles of 256 by 128, of which each CTA
+// loads half of either operand; rows are widened once by a kernel ahead into a workspace,
+// as every feature tile reads them again.
+//
+// Measured.  Few rows: the stream of weights; 100 tokens with 8 of 256 experts of 6144 x
+// 1024 (1.17 GB reached) 179 us, 6.5 TB/s; one token with 10 of 1024 x 8192 (84 MB) 24.5 us, of
+// which the first codes take 2.3 to arrive.  Rings: with one ring for codes and products 28
+// us, with the rows widened ahead 26; with 16 widening warps no faster.  Large groups: 4096
+// tokens with 8 of 64, 4096 x 5120: 950 us, 1.44 PFLOP/s; without the widening stores 11 % less
+// time, with one product in eight 16 % less, with neither 20 %: the copies' 64 bytes a
+// cycle and SM (60 is what one takes in), which wider tiles would lower, but 256 sums a
+// lane pair do not fit the registers beside the widening warps.
 #include <cuda_fp16.h>
 
 #include "../../include/beamnorm.h"
@@ -44,10 +54,9 @@ struct Shape8 {
     static constexpr int kStep = PAIR ? 32 : 16;     // rows of a product are rounded up to this
     // Rings of their own: codes wait for copies from DRAM and are free once widened; rows, and
     // the weights in tensor memory, once the products have read them.
-    static constexpr int kW = PAIR ? 6 : 8;          // stages of codes
-    static constexpr int kX = PAIR ? 6 : 7;          // stages of rows
-    static constexpr int kSlots = PAIR ? 4 : 7;      // stages of widened weights, at most kX
-    static constexpr int kWBytes = kHalf * kDepth;
+    static constexpr int kW = PAIR ? 8 : 7;          // stages of codes
+    static constexpr int kX = PAIR ? 4 : 6;          // stages of rows, and of weights in tensor memory
+    static constexpr int kWBytes = (kHalf + (PAIR ? 0 : kRows)) * kDepth;  // narrow: the rows' codes behind the weights'
     static constexpr int kAtom = kRows / kCtas * 128;  // rows of 64 values
     static constexpr int kBox = kRows / kCtas;       // rows of the larger box; the smaller one has half
     static constexpr int kXBytes = 2 * kAtom;
@@ -56,17 +65,16 @@ struct Shape8 {
     static constexpr int kJoinBytes = PAIR ? 0 : (kRows + kMaxSplit) * kHalf * 4;
     static constexpr int kOutWarps = PAIR ? 8 : 4;
     static constexpr int kWideners = 8;              // warps that widen, two for every 32 weight rows
-    static constexpr int kOutWarp = 4 + kWideners;   // warps: codes, products, rows, 1 idle, widening, output
+    static constexpr int kOutWarp = 4 + kWideners;   // warps: codes, products, 2 for rows, widening, output
     static constexpr int kThreads = 32 * (kOutWarp + kOutWarps);
     static constexpr size_t smem(int E) { return 1024 + (size_t)kRingBytes + kJoinBytes + 2 * sizeof(int) * (size_t)(E + 1); }
 };
-static_assert(Shape8<true>::kSlots <= Shape8<true>::kX && Shape8<false>::kSlots <= Shape8<false>::kX, "a barrier's phases");
-static_assert(Shape8<true>::kColumnA + Shape8<true>::kSlots * kAColumns <= kTmemColumns, "tensor memory");
-static_assert(Shape8<false>::kColumnA + Shape8<false>::kSlots * kAColumns <= kTmemColumns, "tensor memory");
+static_assert(Shape8<true>::kColumnA + Shape8<true>::kX * kAColumns <= kTmemColumns, "tensor memory");
+static_assert(Shape8<false>::kColumnA + Shape8<false>::kX * kAColumns <= kTmemColumns, "tensor memory");
 
 struct Maps8 {
     CUtensorMap w;           // codes: boxes of 128 rows by 128
-    CUtensorMap x, x_small;  // widened rows: boxes of 64 values by all rows of a tile's share, or half
+    CUtensorMap x, x_small;  // rows, all of a tile's share or half: widened in boxes of 64 values (pairs), or codes of 128
 };
 
 // The product with its M operand in tensor memory.
@@ -101,6 +109,24 @@ __device__ __forceinline__ uint4 load_shared(uint32_t addr)
     return v;
 }
 
+__device__ __forceinline__ void store_shared(uint32_t addr, const uint4 &v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
+// A place in a ring of N stages, and the parity of its round.
+template <int N>
+struct Ring {
+    uint32_t at = 0, phase = 0;
+    __device__ __forceinline__ void next()
+    {
+        if (++at == N) {
+            at = 0;
+            phase ^= 1u;
+        }
+    }
+};
+
 __device__ __forceinline__ void store32(uint32_t tmem, const uint32_t *v)
 {
     asm volatile(
@@ -123,22 +149,22 @@ __global__ void __launch_bounds__(Shape8<PAIR>::kThreads, 1)
 product8_kernel(const __grid_constant__ Maps8 maps, const __grid_constant__ Product8Args p)
 {
     using S = Shape8<PAIR>;
-    constexpr int kW = S::kW, kX = S::kX, kSlots = S::kSlots, kTile = S::kTile, kRows = S::kRows;
+    constexpr int kW = S::kW, kX = S::kX, kTile = S::kTile, kRows = S::kRows;
     constexpr int kSums = kRows / S::kCtas;  // columns of an output warp: all, or half of a pair's 128
     extern __shared__ __align__(1024) uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
-    __shared__ __align__(8) uint64_t bars[2 * kW + 2 * kX + kSlots + 7];
+    __shared__ __align__(8) uint64_t bars[2 * kW + 2 * kX + 7];
     __shared__ uint32_t tmem_slot;
     __shared__ int abort_flag;
     int *parts = reinterpret_cast<int *>(raw + (base - smem_addr(raw)) + S::kRingBytes);
     int *start = parts + S::kJoinBytes / 4;
     int *cum = start + p.E + 1;
     const int warp = __shfl_sync(kAll, (int)threadIdx.x >> 5, 0), lane = threadIdx.x & 31;
-    // w_full: this CTA's codes have landed; w_empty: they are widened; x_full: the rows have
-    // landed (a pair's on the first CTA's barrier); ready: the weights are in tensor memory
-    // (likewise); empty: the products have read them, and the rows
-    const uint32_t w_full = smem_addr(bars), w_empty = w_full + 8 * kW, x_full = w_empty + 8 * kW, empty = x_full + 8 * kX, ready = empty + 8 * kX;
-    const uint32_t acc_full = ready + 8 * kSlots, acc_empty = acc_full + 16, done = acc_empty + 16, joined = done + 8, joinable = joined + 8;
+    // w_full: this CTA's codes have landed; w_empty: they are widened; ready: a stage's
+    // weights are in tensor memory and its rows in shared memory (a pair's on the first CTA's
+    // barrier); empty: the products have read both
+    const uint32_t w_full = smem_addr(bars), w_empty = w_full + 8 * kW, ready = w_empty + 8 * kW, empty = ready + 8 * kX;
+    const uint32_t acc_full = empty + 8 * kX, acc_empty = acc_full + 16, done = acc_empty + 16, joined = done + 8, joinable = joined + 8;
     const uint32_t rank = PAIR ? cluster_ctarank() : 0u;
     const uint32_t parts_n = PAIR ? 1u : (uint32_t)p.split, part = PAIR || parts_n == 1 ? 0u : cluster_ctarank();
     const int ctas = PAIR ? 2 : p.split;
@@ -153,13 +179,12 @@ product8_kernel(const __grid_constant__ Maps8 maps, const __grid_constant__ Prod
         abort_flag = 0;
         for (int i = 0; i < kW; ++i) {
             mbar_init(w_full + 8 * i, 1);
-            mbar_init(w_empty + 8 * i, 4);
+            mbar_init(w_empty + 8 * i, PAIR ? 4 : 5);
         }
         for (int i = 0; i < kX; ++i) {
-            mbar_init(x_full + 8 * i, 1);
+            mbar_init(ready + 8 * i, S::kCtas * 4 + 1);
             mbar_init(empty + 8 * i, 1);
         }
-        for (int i = 0; i < kSlots; ++i) mbar_init(ready + 8 * i, S::kCtas * 4);
         for (int i = 0; i < 2; ++i) {
             mbar_init(acc_full + 8 * i, 1);
             mbar_init(acc_empty + 8 * i, S::kCtas * S::kOutWarps);
@@ -190,7 +215,7 @@ product8_kernel(const __grid_constant__ Maps8 maps, const __grid_constant__ Prod
     const int k0 = (int)(part * nk / parts_n), k1 = (int)((part + 1) * nk / parts_n);
 
     const uint32_t rows_at = base + kW * S::kWBytes;
-    if (warp == 0) {  // the weights' codes
+    if (warp == 0) {  // the codes
         uint32_t it = 0;  // stages filled
         bool ok = true;
         while (ok && tiles.next(t, lane)) {
@@ -200,30 +225,32 @@ product8_kernel(const __grid_constant__ Maps8 maps, const __grid_constant__ Prod
                 ok = __all_sync(kAll, wait_phase<false, kPipe>(w_empty + 8 * s, ((it / kW) & 1u) ^ 1u, ctl));
                 if (!ok) break;
                 if (elect_one()) {
-                    mbar_arrive_expect_tx(w_full + 8 * s, S::kWBytes);
-                    tma_3d<false>(base + s * S::kWBytes, &maps.w, k * kDepth, f0, t.e, w_full + 8 * s);
+                    const uint32_t at = base + s * S::kWBytes, bar = w_full + 8 * s;
+                    const int rows = PAIR ? 0 : t.rows <= S::kBox / 2 ? S::kBox / 2 : S::kBox;
+                    mbar_arrive_expect_tx(bar, (uint32_t)(kHalf + rows) * kDepth);
+                    tma_3d<false>(at, &maps.w, k * kDepth, f0, t.e, bar);
+                    if (!PAIR) tma_2d<false>(at + kHalf * kDepth, rows == S::kBox ? &maps.x : &maps.x_small, k * kDepth, t.row0, bar);
                 }
             }
         }
         // no copy may be in flight into a CTA that leaves
         for (uint32_t i = it > kW ? it - kW : 0; i < it; ++i) wait_phase<false, kDrain>(w_full + 8 * (i % kW), (i / kW) & 1u, ctl);
         __syncwarp();
-    } else if (warp == 2) {  // the rows
+    } else if (PAIR && warp == 2) {  // the rows, widened by the kernel ahead
+        Ring<kX> ring;
         uint32_t it = 0;  // stages filled
         bool ok = true;
         while (ok && tiles.next(t, lane)) {
-            // this CTA's rows of the product's N operand: all, or half of the rounded count
             const int columns = (t.rows + S::kStep - 1) / S::kStep * S::kStep;
-            const int nb = PAIR ? columns / 2 : columns, b0 = t.row0 + (PAIR ? (int)rank * nb : 0);
+            const int nb = columns / 2, b0 = t.row0 + (int)rank * nb;  // this CTA's half
             const bool small = nb <= S::kBox / 2;
             const uint32_t bytes = 2u * 128u * (small ? S::kBox / 2 : S::kBox);
-            for (int k = k0; k < k1; ++k, ++it) {
-                const uint32_t s = it % kX;
-                ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(empty + 8 * s, ((it / kX) & 1u) ^ 1u, ctl));
+            for (int k = k0; k < k1; ++k, ++it, ring.next()) {
+                ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(empty + 8 * ring.at, ring.phase ^ 1u, ctl));
                 if (!ok) break;
                 if (elect_one()) {
-                    const uint32_t x = rows_at + s * S::kXBytes, bar = PAIR ? mapa(x_full + 8 * s, 0) : x_full + 8 * s;
-                    if (rank == 0) mbar_arrive_expect_tx(x_full + 8 * s, S::kCtas * bytes);
+                    const uint32_t x = rows_at + ring.at * S::kXBytes, bar = mapa(ready + 8 * ring.at, 0);
+                    if (rank == 0) mbar_arrive_expect_tx(ready + 8 * ring.at, S::kCtas * bytes);
                     const CUtensorMap *map = small ? &maps.x_small : &maps.x;
                     tma_2d<PAIR>(x, map, k * kDepth, b0, bar);
                     tma_2d<PAIR>(x + S::kAtom, map, k * kDepth + 64, b0, bar);  // past K: zeros
@@ -234,15 +261,52 @@ product8_kernel(const __grid_constant__ Maps8 maps, const __grid_constant__ Prod
         const uint32_t old = it > kX ? it - kX : 0;
         for (uint32_t i = old; ok && i < it; ++i)
             ok = wait_phase<PAIR, kPipe>(empty + 8 * (i % kX), (i / kX) & 1u, ctl);
-        if (!ok) {  // after a timeout: wait for the copies, and where their barrier is the other CTA's, for a while
-            for (uint32_t i = old; rank == 0 && i < it; ++i) wait_phase<false, kDrain>(x_full + 8 * (i % kX), (i / kX) & 1u, ctl);
-            for (const long long t0 = clock64(); rank != 0 && clock64() - t0 < (1 << 22);) {}
+        // after a timeout the copies' barrier may never complete: give them a while
+        if (!ok) for (const long long t0 = clock64(); clock64() - t0 < (1 << 22);) {}
+        __syncwarp();
+    } else if (!PAIR && (warp == 2 || warp == 3)) {  // the rows' codes, widened: every second stage
+        // a lane takes a row's 64 codes of one half of the stage (up to 16 rows), or both
+        Ring<kX> ring;
+        const uint32_t turn = (uint32_t)warp & 1u;
+        uint32_t it = 0;
+        bool ok = true;
+        while (ok && tiles.next(t, lane)) {
+            const bool few = t.rows <= 16;
+            const int row = few ? lane & 15 : lane, first = few ? 4 * (lane >> 4) : 0, last = few ? first + 4 : 8;
+            for (int k = k0; k < k1; ++k, ++it, ring.next()) {
+                if ((it & 1u) != turn) continue;
+                const uint32_t s = it % kW;
+                ok = __all_sync(kAll, wait_phase<false, kPipe>(empty + 8 * ring.at, ring.phase ^ 1u, ctl)) &&
+                     __all_sync(kAll, wait_phase<false, kPipe>(w_full + 8 * s, (it / kW) & 1u, ctl));
+                if (!ok) break;
+                const uint32_t from = base + s * S::kWBytes + kHalf * kDepth + (uint32_t)row * 128u;
+                const uint32_t to = rows_at + ring.at * S::kXBytes + (uint32_t)row * 128u;
+#pragma unroll 4
+                for (int c = first; c < last; ++c) {  // 16 codes: two pieces of 16 bytes of a row's 128
+                    const uint4 q = load_shared(from + ((c ^ (row & 7)) << 4));
+                    uint4 a, b;
+                    widen4(q.x, a.x, a.y);
+                    widen4(q.y, a.z, a.w);
+                    widen4(q.z, b.x, b.y);
+                    widen4(q.w, b.z, b.w);
+                    const uint32_t x = to + (c >> 2) * S::kAtom;
+                    store_shared(x + (((2 * (c & 3)) ^ (row & 7)) << 4), a);
+                    store_shared(x + (((2 * (c & 3) + 1) ^ (row & 7)) << 4), b);
+                }
+                asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                __syncwarp();
+                if (lane == 0) {
+                    mbar_arrive(w_empty + 8 * s);
+                    mbar_arrive(ready + 8 * ring.at);
+                }
+            }
         }
         __syncwarp();
     } else if (warp == 1) {
         // of a pair's CTAs the first issues the products
         if (rank == 0) {
-            uint32_t it = 0, n = 0;  // stages, and sums of up to kExact stages
+            Ring<kX> ring;
+            uint32_t n = 0;  // sums of up to kExact stages
             bool ok = true;
             while (ok && tiles.next(t, lane)) {
                 const uint32_t columns = (uint32_t)((t.rows + S::kStep - 1) / S::kStep * S::kStep);
@@ -254,14 +318,12 @@ product8_kernel(const __grid_constant__ Maps8 maps, const __grid_constant__ Prod
                     if (!ok) break;
                     const uint32_t acc = tmem + buf * kRows;
                     const int end = min(c + kExact, k1);
-                    for (int k = c; k < end; ++k, ++it) {
-                        const uint32_t s = it % kX, slot = it % kSlots;
-                        ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(x_full + 8 * s, (it / kX) & 1u, ctl)) &&
-                             __all_sync(kAll, wait_phase<PAIR, kPipe>(ready + 8 * slot, (it / kSlots) & 1u, ctl));
+                    for (int k = c; k < end; ++k, ring.next()) {
+                        ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(ready + 8 * ring.at, ring.phase, ctl));
                         if (!ok) break;
                         fence_after();
-                        const uint32_t a = tmem + S::kColumnA + slot * kAColumns;
-                        const uint64_t b = rows_desc(rows_at + s * S::kXBytes);
+                        const uint32_t a = tmem + S::kColumnA + ring.at * kAColumns;
+                        const uint64_t b = rows_desc(rows_at + ring.at * S::kXBytes);
                         if (elect_one()) {
                             const auto step = [&](int j) {  // 16 values: 8 columns, 32 bytes along a row
                                 product8<PAIR>(acc, a + 8 * j, b + (j >> 2) * (S::kAtom >> 4) + (j & 3) * 2, idesc, k > c || j > 0);
@@ -273,7 +335,7 @@ product8_kernel(const __grid_constant__ Maps8 maps, const __grid_constant__ Prod
                                 const int steps = (p.K - k * kDepth + 15) / 16;
                                 for (int j = 0; j < steps; ++j) step(j);
                             }
-                            commit<PAIR>(empty + 8 * s);
+                            commit<PAIR>(empty + 8 * ring.at);
                             if (k == end - 1) commit<PAIR>(acc_full + 8 * buf);
                         }
                     }
@@ -291,22 +353,20 @@ product8_kernel(const __grid_constant__ Maps8 maps, const __grid_constant__ Prod
         const int quad = warp & 3, row = quad * 32 + lane;  // this lane's weight row, and its lane of tensor memory
         const uint32_t turn = (uint32_t)(warp - 4) >> 2;  // every kTurns-th stage is this warp's
         constexpr uint32_t kTurns = S::kWideners / 4;
+        Ring<kX> ring;
         uint32_t it = 0;
         bool ok = true;
         while (ok && tiles.next(t, lane)) {
-            for (int k = k0; k < k1; ++k, ++it) {
+            for (int k = k0; k < k1; ++k, ++it, ring.next()) {
                 if (it % kTurns != turn) continue;
-                const uint32_t s = it % kW, slot = it % kSlots;
-                if (it >= kSlots) {  // the products have read this slot's last weights
-                    const uint32_t last = it - kSlots;
-                    ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(empty + 8 * (last % kX), (last / kX) & 1u, ctl));
-                    if (!ok) break;
-                }
-                ok = __all_sync(kAll, wait_phase<false, kPipe>(w_full + 8 * s, (it / kW) & 1u, ctl));
+                const uint32_t s = it % kW;
+                // the products have read what this place of tensor memory held
+                ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(empty + 8 * ring.at, ring.phase ^ 1u, ctl)) &&
+                     __all_sync(kAll, wait_phase<false, kPipe>(w_full + 8 * s, (it / kW) & 1u, ctl));
                 if (!ok) break;
                 fence_after();
                 const uint32_t from = base + s * S::kWBytes + row * 128;
-                const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + S::kColumnA + slot * kAColumns;
+                const uint32_t to = tmem + ((uint32_t)(quad * 32) << 16) + S::kColumnA + ring.at * kAColumns;
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
                     uint4 q[4];
@@ -330,8 +390,8 @@ product8_kernel(const __grid_constant__ Maps8 maps, const __grid_constant__ Prod
                 fence_before();
                 __syncwarp();
                 if (lane == 0) {
-                    if (PAIR) arrive_first(ready + 8 * slot);
-                    else mbar_arrive(ready + 8 * slot);
+                    if (PAIR) arrive_first(ready + 8 * ring.at);
+                    else mbar_arrive(ready + 8 * ring.at);
                 }
             }
         }
@@ -510,25 +570,31 @@ bool choose_pairs(Product8Args &p, int sms)
 
 }  // namespace
 
-cudaError_t launch_product8(Product8Args p, const int8_t *a, const int8_t *w, void *workspace, int sms, bool pdl, cudaStream_t st)
+cudaError_t launch_product8(Product8Args p, const int8_t *w, void *workspace, int sms, bool pdl, cudaStream_t st)
 {
     cudaError_t e = tensor_maps_ready();
     if (e != cudaSuccess) return e;
-    const long long n = (long long)p.M * p.K / 16, blocks = (n + 255) / 256, most = 16LL * sms;
-    e = launch_kernel(widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, pdl, 1, st,
-                      reinterpret_cast<const uint4 *>(a), n, static_cast<uint4 *>(workspace));
-    if (e != cudaSuccess) return e;
     Maps8 m;
     const bool pair = choose_pairs(p, sms);
-    const auto rows = [&](CUtensorMap *map, int box) {
+    if (pair) {
+        const long long n = (long long)p.M * p.K / 16, blocks = (n + 255) / 256, most = 16LL * sms;
+        e = launch_kernel(widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, pdl, 1, st,
+                          reinterpret_cast<const uint4 *>(p.a), n, static_cast<uint4 *>(workspace));
+        if (e != cudaSuccess) return e;
+    }
+    const auto codes = [&](CUtensorMap *map, int box) {
+        return make_map<2>(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, p.a, {(cuuint64_t)p.K, (cuuint64_t)p.M}, {kDepth, (cuuint32_t)box},
+                           CU_TENSOR_MAP_SWIZZLE_128B);
+    };
+    const auto widened = [&](CUtensorMap *map, int box) {
         return make_map<2>(map, CU_TENSOR_MAP_DATA_TYPE_UINT16, 2, workspace, {(cuuint64_t)p.K, (cuuint64_t)p.M}, {64, (cuuint32_t)box},
                            CU_TENSOR_MAP_SWIZZLE_128B);
     };
     e = make_map<3>(&m.w, CU_TENSOR_MAP_DATA_TYPE_UINT8, 1, w, {(cuuint64_t)p.K, (cuuint64_t)p.N, (cuuint64_t)p.E}, {kDepth, kHalf, 1},
                     CU_TENSOR_MAP_SWIZZLE_128B);
     const int box = pair ? Shape8<true>::kBox : Shape8<false>::kBox;
-    if (e == cudaSuccess) e = rows(&m.x, box);
-    if (e == cudaSuccess) e = rows(&m.x_small, box / 2);
+    if (e == cudaSuccess) e = pair ? widened(&m.x, box) : codes(&m.x, box);
+    if (e == cudaSuccess) e = pair ? widened(&m.x_small, box / 2) : codes(&m.x_small, box / 2);
     if (e != cudaSuccess) return e;
     return pair ? launch_shape8<true>(p, m, sms, pdl, st) : launch_shape8<false>(p, m, sms, pdl, st);
 }
