@@ -320,3 +320,9 @@ def test_captured_and_replayed():
         want = exact(d)
         for _, out in graphs:
             assert all(torch.equal(a, b.bfloat16()) for a, b in zip(out, want))
+
+
+@pytest.mark.parametrize("sizes,N,K", [([4001], 4104, 520), ([4001], 520, 4104), ([3000, 0, 5000], 2056, 264), ([2300, 2600, 90], 264, 4096)])
+def test_tall_tiles(sizes, N, K):
+    """A few large groups: pairs whose tiles have 512 rows, with odd last tiles of one block and of two."""
+    check(make(sizes, N, K, "bf16", seed=13, before=1, after=40), whole=True)

@@ -22,8 +22,19 @@
 // gradient come the same way: an index outside x reads zeros, where a box would
 // bring in the next group's rows.
 //
-// Two shapes, as in bn_product.cu: one CTA with tiles of 128 x 128, and a pair of CTAs
-// (cta_group::2) with tiles of 256 x 256 of which each loads half of either operand.
+// Shapes, as in bn_product.cu: one CTA with tiles of 128 x 128, or a pair of CTAs
+// (cta_group::2) with tiles of 256 x 256 of which each loads half of either operand.  Tall
+// pairs take 512 rows, in both accumulators, with the same features: 48 bytes a cycle and SM
+// to fill for 64, at no overlap of a tile's way out with the next.  Where tiles are too few
+// for the device, clusters of CTAs each sum a part.
+//
+// Measured.  What one SM takes in (60 bytes a cycle) bounds pairs: 4096 tokens with 8 of
+// 64 experts of 4096 x 5120 866 us (1.59 PFLOP/s), their last tiles not full; one expert of 8192
+// x 8192 and as many rows 549 us by tall pairs (2.00 PFLOP/s).  Rows by index cost the
+// place in the workspace, 70 us of 1020.  Few rows: the stream of weights; 100 tokens with 8 of
+// 256 experts of 6144 x 512 179 us (6.7 TB/s), one token with 10 of 512 x 8192 19 us (4.4).
+// dw of 4096 tokens with 8 of 64, 5120 x 2048 (1.34 GB) 500 us: shared memory carries the
+// operands and what goes out.
 #include "../../include/beamnorm.h"
 #include "bn_device.cuh"
 #include "bn_experts.h"
@@ -38,20 +49,24 @@ constexpr int kDepth = 64;      // summed values of a stage: 128 bytes
 constexpr int kBoxRows = 16;    // rows of the smaller box
 constexpr int kAtom = 64 * 128; // bytes of 64 features or rows by 64 values, where the sum runs across rows
 
-enum Shape { kOne = 0, kPair = 1, kSplit = 2 };
+enum Shape { kOne = 0, kPair = 1, kSplit = 2, kTall = 3 };
 
 template <int SHAPE, bool WEIGHTS = false>
 struct LinearShape {
-    static constexpr int kCtas = SHAPE == kPair ? 2 : 1;       // CTAs of one product
-    static constexpr int kTile = SHAPE == kPair ? 256 : 128;   // features of an output tile
-    static constexpr int kRows = SHAPE == kSplit ? 64 : kTile; // its rows
-    static constexpr int kStep = SHAPE == kPair ? 32 : 16;     // rows of a product are rounded up to this
-    static constexpr int kStages = SHAPE == kSplit ? 7 : WEIGHTS ? 5 : 6;
+    static constexpr bool kPairs = SHAPE == kPair || SHAPE == kTall;
+    static constexpr int kCtas = kPairs ? 2 : 1;               // CTAs of one product
+    static constexpr int kTile = kPairs ? 256 : 128;           // features of an output tile
+    static constexpr int kBlock = SHAPE == kSplit ? 64 : kTile;  // rows of one product
+    static constexpr int kBlocks = SHAPE == kTall ? 2 : 1;     // products of a tile
+    static constexpr int kRows = kBlock * kBlocks;
+    static constexpr int kStep = kPairs ? 32 : 16;             // rows of a product are rounded up to this
+    static constexpr int kStages = SHAPE == kSplit ? 7 : SHAPE == kTall ? 4 : WEIGHTS ? 5 : 6;
     static constexpr int kOffQ = kHalf * 128;
-    static constexpr int kStageBytes = kOffQ + kRows / kCtas * 128;
-    static constexpr int kColumns = 2 * kRows;      // tensor memory: two accumulators
+    static constexpr int kBlockBytes = kBlock / kCtas * 128;
+    static constexpr int kStageBytes = kOffQ + kBlocks * kBlockBytes;
+    static constexpr int kColumns = 2 * kBlock;                // tensor memory: two accumulators
     static constexpr int kJoinBytes = SHAPE == kSplit ? (kRows + kMaxSplit) * kHalf * 4 : 0;  // parts of a split sum
-    static constexpr int kOutWarps = SHAPE == kPair ? 8 : 4;
+    static constexpr int kOutWarps = kPairs ? 8 : 4;
     static constexpr int kThreads = 64 + 32 * kOutWarps;  // copies, products, output
     // output warps' boxes of 32 rows by 128 bytes on their way to a weight gradient
     static constexpr int kOutBoxes = SHAPE == kPair ? 1 : 2;
@@ -132,8 +147,8 @@ __global__ void __launch_bounds__(LinearShape<SHAPE>::kThreads, 1)
 linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearArgs p)
 {
     using S = LinearShape<SHAPE, MODE == kWeightGrad>;
-    constexpr bool PAIR = SHAPE == kPair, SPLIT = SHAPE == kSplit;
-    constexpr int kStages = S::kStages, kTile = S::kTile, kRows = S::kRows;
+    constexpr bool PAIR = S::kPairs, SPLIT = SHAPE == kSplit;
+    constexpr int kStages = S::kStages, kTile = S::kTile, kRows = S::kRows, kBlock = S::kBlock, kBlocks = S::kBlocks;
     constexpr bool kWeights = MODE == kWeightGrad;
     constexpr bool kAcrossP = MODE != kForward, kAcrossQ = kWeights;
     extern __shared__ __align__(1024) uint8_t raw[];
@@ -208,7 +223,10 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
         k0 = SPLIT ? (int)(part * (uint32_t)nk / parts_n) : 0;
         k1 = SPLIT ? (int)((part + 1) * (uint32_t)nk / parts_n) : nk;
     };
-    const auto columns_of = [&]() { return (t.rows + S::kStep - 1) / S::kStep * S::kStep; };
+    // a tile's products, the rows of one, and its columns
+    const auto blocks_of = [&]() { return kBlocks == 1 ? 1 : (t.rows + kBlock - 1) / kBlock; };
+    const auto rows_of = [&](int b) { return kBlocks == 1 ? t.rows : min(kBlock, t.rows - b * kBlock); };
+    const auto columns_of = [&](int b) { return (rows_of(b) + S::kStep - 1) / S::kStep * S::kStep; };
 
     // The copying and the issuing warp run their loops as a whole, so that loop
     // state stays in uniform registers; one elected thread does each stage's work,
@@ -218,13 +236,16 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
         bool ok = true;
         while (ok && tiles.next(t, lane)) {
             const int f0 = t.f * kTile + (int)rank * kHalf;
-            // this CTA's rows of the product's N operand: all, or half of the rounded count
-            const int columns = columns_of();
-            const int nb = PAIR ? columns / 2 : columns, b0 = t.row0 + (PAIR ? (int)rank * nb : 0);
+            // this CTA's rows of a product's N operand: all, or half of the rounded count
+            const auto half_of = [&](int b) { return PAIR ? columns_of(b) / 2 : columns_of(b); };
+            const int nb = half_of(0), b0 = t.row0 + (PAIR ? (int)rank * nb : 0);
             const int d = depth();
             int k0, k1;
             stages(d, k0, k1);
-            const int boxes = nb > kHalf / 2 && !SPLIT ? 0 : (nb + kBoxRows - 1) / kBoxRows;  // 0: one of kHalf rows
+            const auto boxes_of = [&](int n) { return n > kHalf / 2 && !SPLIT ? 0 : (n + kBoxRows - 1) / kBoxRows; };  // 0: one of kHalf rows
+            const int boxes = boxes_of(nb);
+            // and of a second product
+            const int nb2 = kBlocks > 1 && blocks_of() > 1 ? half_of(1) : 0, b2 = t.row0 + kBlock + (int)rank * nb2, boxes2 = boxes_of(nb2);
             const int q_atoms = nb > 64 ? 2 : 1;
             if constexpr (GATHER && !kWeights) {  // four rows a lane; places past the tile read zeros
                 int v[4];
@@ -271,7 +292,8 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 const int r0 = k * kDepth;
                 if constexpr (!kWeights) {
                     if (elect_one()) {
-                        const uint32_t q_rows = GATHER ? (uint32_t)nb : (uint32_t)(boxes ? boxes * kBoxRows : kHalf);
+                        uint32_t q_rows = GATHER ? (uint32_t)nb : (uint32_t)(boxes ? boxes * kBoxRows : kHalf);
+                        if (kBlocks > 1 && nb2) q_rows += (uint32_t)(boxes2 ? boxes2 * kBoxRows : kHalf);
                         if (rank == 0) mbar_arrive_expect_tx(full + 8 * s, S::kCtas * ((uint32_t)kHalf + q_rows) * 128);
                         if constexpr (kAcrossP) {
                             tma_3d<PAIR>(at, &maps.p, f0, r0, t.e, bar);
@@ -280,9 +302,12 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                             tma_3d<PAIR>(at, &maps.p, r0, f0, t.e, bar);
                         }
                         if constexpr (!GATHER) {
-                            if (boxes == 0) tma_2d<PAIR>(q, &maps.q, r0, b0, bar);
-                            for (int b = 0; b < boxes; ++b)
-                                tma_2d<PAIR>(q + b * kBoxRows * 128, &maps.q_small, r0, b0 + b * kBoxRows, bar);
+                            const auto block = [&](uint32_t to, int y, int n) {
+                                if (n == 0) tma_2d<PAIR>(to, &maps.q, r0, y, bar);
+                                for (int b = 0; b < n; ++b) tma_2d<PAIR>(to + b * kBoxRows * 128, &maps.q_small, r0, y + b * kBoxRows, bar);
+                            };
+                            block(q, b0, boxes);
+                            if (kBlocks > 1 && nb2) block(q + S::kBlockBytes, b2, boxes2);
                         } else {
 #pragma unroll 4
                             for (int i = 0; i < nb / 4; ++i) tma_rows<PAIR>(q + i * 512, &maps.q_rows, r0, quads[i], bar);
@@ -352,16 +377,20 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
         if (rank == 0) {
             uint32_t it = 0, n = 0;
             bool ok = true;
-            for (; ok && tiles.next(t, lane); ++n) {
-                const uint32_t buf = n & 1u;
-                ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(acc_empty + 8 * buf, ((n >> 1) & 1u) ^ 1u, ctl));
-                if (!ok) break;
-                fence_after();
+            while (ok && tiles.next(t, lane)) {
                 // FP32 sums; the operands' type; which of them run across the rows; N / 8, M / 16
                 const uint32_t type = p.dtype == BN_BF16 ? 1u : 0u;
-                const uint32_t idesc = (1u << 4) | (type << 7) | (type << 10) | ((kAcrossP ? 1u : 0u) << 15) |
-                                       ((kAcrossQ ? 1u : 0u) << 16) | (((uint32_t)columns_of() >> 3) << 17) | ((uint32_t)(kTile >> 4) << 24);
-                const uint32_t acc = tmem + buf * kRows;
+                const uint32_t kind = (1u << 4) | (type << 7) | (type << 10) | ((kAcrossP ? 1u : 0u) << 15) |
+                                      ((kAcrossQ ? 1u : 0u) << 16) | ((uint32_t)(kTile >> 4) << 24);
+                const int blocks = blocks_of();
+                // the accumulator of block b, in turn, once it has been taken out
+                const auto accumulator = [&](int b) {
+                    const uint32_t i = n + (uint32_t)b;
+                    return __all_sync(kAll, wait_phase<PAIR, kPipe>(acc_empty + 8 * (i & 1u), ((i >> 1) & 1u) ^ 1u, ctl));
+                };
+                ok = accumulator(0);
+                if (!ok) break;
+                fence_after();
                 const int d = depth();
                 int k0, k1;
                 stages(d, k0, k1);
@@ -372,24 +401,38 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                     fence_after();
                     const uint32_t at = base + s * S::kStageBytes;
                     const uint64_t dp = kAcrossP ? across_desc(at) : rows_desc(at);
-                    const uint64_t dq = kAcrossQ ? across_desc(at + S::kOffQ) : rows_desc(at + S::kOffQ);
                     // 16 values: 32 bytes along a row, or 16 rows of 128 bytes
                     constexpr uint32_t kP = kAcrossP ? 128 : 2, kQ = kAcrossQ ? 128 : 2;
-                    if (elect_one()) {
-                        if (k * kDepth + kDepth <= d) {  // unrolled: the issuing thread sets the pace
 #pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, k > k0 || j > 0);
-                        } else {
-                            const int steps = (d - k * kDepth + 15) / 16;
-                            for (int j = 0; j < steps; ++j)
-                                product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, k > k0 || j > 0);
+                    for (int b = 0; b < kBlocks; ++b) {
+                        if (b > 0 && b >= blocks) break;
+                        if (b > 0 && k == k0) {
+                            ok = accumulator(b);
+                            if (!ok) break;
+                            fence_after();
                         }
-                        commit<PAIR>(empty + 8 * s);
-                        if (k == k1 - 1) commit<PAIR>(acc_full + 8 * buf);
+                        const uint32_t acc = tmem + ((n + b) & 1u) * kBlock;
+                        const uint32_t idesc = kind | (((uint32_t)columns_of(b) >> 3) << 17);
+                        const uint32_t from = at + S::kOffQ + b * S::kBlockBytes;
+                        const uint64_t dq = kAcrossQ ? across_desc(from) : rows_desc(from);
+                        if (elect_one()) {
+                            if (k * kDepth + kDepth <= d) {  // unrolled: the issuing thread sets the pace
+#pragma unroll
+                                for (int j = 0; j < 4; ++j)
+                                    product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, k > k0 || j > 0);
+                            } else {
+                                const int steps = (d - k * kDepth + 15) / 16;
+                                for (int j = 0; j < steps; ++j)
+                                    product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, k > k0 || j > 0);
+                            }
+                            if (b == blocks - 1) commit<PAIR>(empty + 8 * s);
+                            if (k == k1 - 1) commit<PAIR>(acc_full + 8 * ((n + b) & 1u));
+                        }
                     }
+                    if (!ok) break;
                 }
-                if (kWeights && ok && k0 == k1 && elect_one()) commit<PAIR>(acc_full + 8 * buf);
+                if (kWeights && ok && k0 == k1 && elect_one()) commit<PAIR>(acc_full + 8 * (n & 1u));
+                n += (uint32_t)blocks;
             }
             // Every product has ended before tensor memory is freed.  Only this CTA waits, so
             // only its barrier is told: an arrival at the other's could come after it left.
@@ -404,28 +447,29 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
         const int half = (warp - 2) >> 2;  // of a pair's columns
         const bool fp16 = p.dtype == BN_FP16;
         uint32_t n = 0, stored = 0;
-        for (; tiles.next(t, lane); ++n) {
-            const uint32_t buf = n & 1u;
-            // this warp's columns: at most 128
-            const int cut = PAIR ? (t.rows + 31) / 32 * 16 : t.rows;
-            const int lo = half ? cut : 0, hi = half ? t.rows : min(cut, t.rows);
-            if (!__all_sync(kAll, wait_phase<PAIR, kPipe>(acc_full + 8 * buf, (n >> 1) & 1u, ctl))) break;
+        // accumulator i is full; it has been taken out
+        const auto taken = [&](uint32_t i) {
+            const bool ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(acc_full + 8 * (i & 1u), (i >> 1) & 1u, ctl));
             fence_after();
-            const uint32_t acc = tmem + ((uint32_t)(quad * 32) << 16) + buf * kRows;
+            return ok;
+        };
+        const auto release = [&](uint32_t i) {
+            fence_before();
+            __syncwarp();
+            if (lane == 0) {
+                if (PAIR) arrive_first(acc_empty + 8 * (i & 1u));
+                else mbar_arrive(acc_empty + 8 * (i & 1u));
+            }
+        };
+        for (; tiles.next(t, lane); n += (uint32_t)blocks_of()) {
+            if (!taken(n)) break;
+            const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), acc = lanes + (n & 1u) * kBlock;
             const long long row0 = t.row0;
             const int f0 = t.f * kTile + (int)rank * kHalf + quad * 32;
-            const auto release = [&]() {
-                fence_before();
-                __syncwarp();
-                if (lane == 0) {
-                    if (PAIR) arrive_first(acc_empty + 8 * buf);
-                    else mbar_arrive(acc_empty + 8 * buf);
-                }
-            };
             if constexpr (SPLIT) {
                 // Every CTA of the cluster finishes its share of the rows: the parts of a row
                 // come to it from all of them and are added in the order of the sum.
-                const int share = (columns_of() + (int)parts_n - 1) / (int)parts_n;
+                const int share = (columns_of(0) + (int)parts_n - 1) / (int)parts_n;
                 if (!__all_sync(kAll, wait_phase<true, kPipe>(joinable, (n & 1u) ^ 1u, ctl))) break;
                 const int r0 = (int)part * share, r1 = min(r0 + share, t.rows);
                 if (quad == 0 && lane == 0) mbar_arrive_expect_tx(joined, parts_n * (uint32_t)max(r1 - r0, 0) * 512u);
@@ -449,7 +493,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                         }
                     }
                 }
-                release();
+                release(n);
                 if (!__all_sync(kAll, wait_phase<true, kPipe>(joined, n & 1u, ctl))) break;
                 uint16_t *out = static_cast<uint16_t *>(p.out) + (row0 + r0) * p.F + f0 + lane;
                 const float *from = parts + quad * 32 + lane;
@@ -487,7 +531,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                             }
                         }
                     }
-                    if (c + width >= end) release();
+                    if (c + width >= end) release(n);
                     // the copy that read this box last has ended
                     asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(S::kOutBoxes - 1) : "memory");
                     __syncwarp();
@@ -511,31 +555,56 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                     }
                 }
-                if (half * 128 >= end) release();
+                if (half * 128 >= end) release(n);
             } else {
                 // the whole tile in 16 bits in registers, so that the next product can start
-                uint32_t packed[8][8];
-#pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    if (lo + 16 * b < hi) {
-                        uint32_t v[16];
-                        read16(acc + lo + 16 * b, v);
-#pragma unroll
-                        for (int i = 0; i < 8; ++i)
-                            packed[b][i] = round16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), fp16);
-                    }
-                }
-                release();
                 const int f = f0 + (lane & ~7);
-                uint16_t *out = static_cast<uint16_t *>(p.out) + (row0 + (lane & 7)) * p.F + f;
+                // this warp's columns of a block: at most 128
+                const auto range = [&](int q, int &lo, int &hi) {
+                    const int rows = rows_of(q), cut = PAIR ? (rows + 31) / 32 * 16 : rows;
+                    lo = half ? cut : 0;
+                    hi = half ? rows : min(cut, rows);
+                };
+                uint32_t packed[kBlocks][8][8];
+                bool ok = true;
 #pragma unroll
-                for (int b = 0; b < 8; ++b) {
-                    if (lo + 16 * b < hi) {
+                for (int q = 0; q < kBlocks; ++q) {
+                    if (q > 0 && q >= blocks_of()) break;
+                    if (q > 0 && !taken(n + q)) {
+                        ok = false;
+                        break;
+                    }
+                    int lo, hi;
+                    range(q, lo, hi);
+                    const uint32_t from = lanes + ((n + q) & 1u) * kBlock + lo;
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const uint4 v = transpose8(packed[b] + 4 * h, lane);
-                            const int c = lo + 16 * b + 8 * h;
-                            if (c + (lane & 7) < hi && f < p.F) *reinterpret_cast<uint4 *>(out + (long long)c * p.F) = v;
+                    for (int b = 0; b < 8; ++b) {
+                        if (lo + 16 * b < hi) {
+                            uint32_t v[16];
+                            read16(from + 16 * b, v);
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                packed[q][b][i] = round16(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1]), fp16);
+                        }
+                    }
+                    release(n + q);
+                }
+                if (!ok) break;
+#pragma unroll
+                for (int q = 0; q < kBlocks; ++q) {
+                    if (q > 0 && q >= blocks_of()) break;
+                    int lo, hi;
+                    range(q, lo, hi);
+                    uint16_t *out = static_cast<uint16_t *>(p.out) + (row0 + q * kBlock + (lane & 7)) * p.F + f;
+#pragma unroll
+                    for (int b = 0; b < 8; ++b) {
+                        if (lo + 16 * b < hi) {
+#pragma unroll
+                            for (int h = 0; h < 2; ++h) {
+                                const uint4 v = transpose8(packed[q][b] + 4 * h, lane);
+                                const int c = lo + 16 * b + 8 * h;
+                                if (c + (lane & 7) < hi && f < p.F) *reinterpret_cast<uint4 *>(out + (long long)c * p.F) = v;
+                            }
                         }
                     }
                 }
@@ -635,27 +704,31 @@ cudaError_t launch_shape(const LinearArgs &p, const LinearMaps &maps, int sms, b
 // the copy rate first): 10 experts with one row, 512 x 8192 12.6: 29.3 / 19.6 (by 3); one
 // expert, 16 rows, 4096 x 8192 10.0: 28.4 / 16.8 (4); 8 rows, 2048 x 8192 5.0: 28.3 / 13.8
 // (8); 512 x 512 5.5 / 6.4 (2): too short.
-// Pairs go by rounds of tiles over the device (groups are taken to leave half a tile
-// each).  A pair's tile fills shared memory as long as a CTA's does, but has more to
-// lose at a group's end: 1.5 of it.  Measured, one CTA / pairs (us): 4096 tokens with 8 of 64
-// experts of 4096 x 5120 1096 / 918, dx 1104 / 909; 2000 with 8 of 32, 1024 x 4096 141 /
-// 117; one expert, 8192 x 8192 and as many rows 870 / 620; 1024 with 2 of 8, 2048 x 2048
-// 34.8 / 38.9.  A weight gradient's tiles are all whole: 333 with 4 of 16, 1024 x 2048
-// 47 / 37; 4096 with 8 of 64, 5120 x 2048 913 / 612.
+// Pairs and their rows go by rounds of tiles over the device (groups are taken to leave half
+// a tile each).  A pair's tile fills shared memory as long as a CTA's does, but has more to
+// lose at a group's end: 4/3 of it (of few rounds 3/2).  A tall tile takes as long as two.
+// Measured, one CTA / pairs / tall pairs (us): 4096 tokens with 8 of 64 experts of 4096 x
+// 5120 1094 / 866 / 958, dx 1096 / 852 / 918; 2000 with 8 of 32, 1024 x 4096 135 / 119 / 133;
+// one expert, 8192 x 8192 and as many rows 870 / 596 / 549, 1024 rows 135 / 96 / 88, 512
+// 72 / 57 / 86; 1000 with 8 of 64, 4096 x 4096 387 / 363 / 406; 1024 with 2 of 8, 2048 x
+// 2048 33 / 37 / 39.  A weight gradient's tiles are all whole: 333 with 4 of 16, 1024 x 2048
+// 47 / 37; 4096 with 8 of 64, 5120 x 2048 913 / 612 (both before its way out by TMA).
 int choose_shape(LinearArgs &p, int mode, int sms)
 {
     const long long groups = p.E < p.M ? p.E : p.M;
-    const auto rounds = [&](int tile, int units) {
-        const long long even = p.M / tile + groups / 2;
-        const long long rows = mode == kWeightGrad ? (long long)p.E * ((p.K + tile - 1) / tile) : even > groups ? even : groups;
+    const auto rounds = [&](int height, int tile, int units) {
+        const long long even = p.M / height + groups / 2;
+        const long long rows = mode == kWeightGrad ? (long long)p.E * ((p.K + height - 1) / height) : even > groups ? even : groups;
         return (rows * ((p.F + tile - 1) / tile) + units - 1) / units;
     };
     p.split = 1;
-    if (mode == kWeightGrad) return rounds(256, sms / 2) < rounds(128, sms) ? kPair : kOne;
+    if (mode == kWeightGrad) return rounds(256, 256, sms / 2) < rounds(128, 128, sms) ? kPair : kOne;
     const long long nk = (p.D + kDepth - 1) / kDepth;
     p.split = choose_split(most_tiles<kSplit>(p, mode), nk, 8, (most_tiles<kOne>(p, mode) + sms - 1) / sms * nk, sms);
     if (p.split > 1) return kSplit;
-    return 3 * rounds(256, sms / 2) < 2 * rounds(128, sms) ? kPair : kOne;
+    const long long one = rounds(128, 128, sms), pair = rounds(256, 256, sms / 2);
+    if (one <= 8 ? 3 * pair >= 2 * one : 4 * pair >= 3 * one) return kOne;
+    return 2 * rounds(512, 256, sms / 2) <= pair ? kTall : kPair;
 }
 
 template <int MODE>
@@ -670,6 +743,7 @@ cudaError_t launch_mode(LinearArgs p, const LinearMaps &maps, int sms, bool pdl,
     }
     if constexpr (MODE != kWeightGrad) {
         if (shape == kSplit) return launch_shape<MODE, kSplit, false>(p, maps, sms, pdl, st);
+        if (shape == kTall) return launch_shape<MODE, kTall, false>(p, maps, sms, pdl, st);
     }
     return shape == kPair ? launch_shape<MODE, kPair, false>(p, maps, sms, pdl, st) : launch_shape<MODE, kOne, false>(p, maps, sms, pdl, st);
 }
