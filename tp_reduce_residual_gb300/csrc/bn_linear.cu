@@ -29,7 +29,7 @@
 // for the device, clusters of CTAs each sum a part.
 //
 // Measured.  What one SM takes in (60 bytes a cycle) bounds pairs: 4096 tokens with 8 of
-// 64 experts of 4096 x 5120 866 us (1.59 PFLOP/s), their last tiles not full; one expert of 8192
+// 64 experts of 4096 x 5120 852 us (1.61 PFLOP/s), their tiles not full; one expert of 8192
 // x 8192 and as many rows 549 us by tall pairs (2.00 PFLOP/s).  Rows by index cost the
 // place in the workspace, 70 us of 1020.  Few rows: the stream of weights; 100 tokens with 8 of
 // 256 experts of 6144 x 512 179 us (6.7 TB/s), one token with 10 of 512 x 8192 19 us (4.4).
@@ -212,7 +212,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
         if constexpr (kWeights)
             return WeightTiles<kTile>(p.E, p.K, p.F, (unsigned)unit, (unsigned)units);
         else
-            return Tiles<kRows>(start, cum, p.E, (unsigned)((p.F + kTile - 1) / kTile), (unsigned)unit, (unsigned)units);
+            return Tiles<kRows, PAIR ? S::kStep : 0>(start, cum, p.E, (unsigned)((p.F + kTile - 1) / kTile), (unsigned)unit, (unsigned)units);
     }();
     Tile t = {};
     // the length of a tile's sum

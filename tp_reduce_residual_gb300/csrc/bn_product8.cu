@@ -208,7 +208,7 @@ product8_kernel(const __grid_constant__ Maps8 maps, const __grid_constant__ Prod
     ctl.err = p.err;
     ctl.spin = false;
     ctl.pipe_polls = kMaxSpins;
-    Tiles<kRows> tiles(start, cum, p.E, (unsigned)((p.N + kTile - 1) / kTile), (unsigned)unit, (unsigned)units);
+    Tiles<kRows, PAIR ? S::kStep : 0> tiles(start, cum, p.E, (unsigned)((p.N + kTile - 1) / kTile), (unsigned)unit, (unsigned)units);
     Tile t = {};
     const uint32_t nk = (uint32_t)(p.K + kDepth - 1) / kDepth;
     // the stages of the sum that this CTA takes
