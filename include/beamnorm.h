@@ -511,10 +511,11 @@ BN_API bn_status bn_quantize_int8(const void *x, bn_dtype dtype, long long ld, i
 BN_API bn_status bn_dequantize_int8(const int8_t *data, const float *scales, int M, int K,
                                     void *out, bn_dtype dtype, void *stream);
 
-/* Bytes of the workspace that bn_expert_product_int8 needs (the rows' codes in 16 bits),
- * 0 on invalid arguments or no rows.  Pure host logic.
+/* Bytes of workspace with which bn_expert_product_int8 brings the rows' codes to 16 bits
+ * once, ahead of the product, for large groups; 0 where it does so as fast itself (or on
+ * invalid arguments).  Pure host logic.
  * Source: no passage: library utility. */
-BN_API size_t bn_expert_product_int8_workspace_bytes(int M, int K);
+BN_API size_t bn_expert_product_int8_workspace_bytes(int M, int E, int N, int K);
 
 /* out[m, n] = bf16(alpha * a_scales[m] * w_scales[e, n] * sum over k of a[m, k] * w[e, n, k])
  * for the rows m of group e.  The sum is exact (32-bit integers), for any codes in
@@ -523,9 +524,11 @@ BN_API size_t bn_expert_product_int8_workspace_bytes(int M, int K);
  *   w, w_scales  [E, N, K] codes and [E, N] FP32: a scale for each output channel
  *   offsets      [E + 1] int32, or NULL when E == 1 (every row)
  *   out          [M, N] BF16; rows before the first offset and past the last are zeros
- *   workspace    device memory of bn_expert_product_int8_workspace_bytes() or more,
- *                16-byte aligned.  Nothing in it is kept
- * Two kernels on `stream`.  N is a multiple of 8, K of 16, at most 131056.  Offsets that
+ *   workspace    device memory of workspace_bytes, 16-byte aligned, or NULL; used where
+ *                it holds bn_expert_product_int8_workspace_bytes() (not 0), for two kernels
+ *                on `stream` instead of one.  Nothing in it is kept; the results are the
+ *                same, up to three times slower without
+ * N is a multiple of 8, K of 16, at most 131056.  Offsets that
  * fall or leave [0, M] set BN_DEVERR_OFFSETS; they are clamped.
  * Source: none -- the pages take the experts' rows as given; it has no counterpart there. */
 BN_API bn_status bn_expert_product_int8(const int8_t *a, const float *a_scales, int M,

@@ -121,14 +121,16 @@ def test_quantised_rows_and_weights():
 
 
 def test_workspace_and_offsets():
-    a, w = make([20, 30], 64, 64)
-    n = experts.product_int8_workspace_bytes(50, 64)
-    assert n == 50 * 64 * 2
+    a, w = make([2000, 3000], 1024, 64)
+    n = experts.product_int8_workspace_bytes(5000, 2, 1024, 64)
+    assert n == 5000 * 64 * 2
     ws = torch.full((n + 64,), 255, dtype=torch.uint8, device="cuda")
     check(a, w, workspace=ws[:n])
     assert (ws[n:] == 255).all()
-    with pytest.raises(bn.BeamNormError, match="workspace"):
-        experts.expert_product(a, w, workspace=ws[:n - 16])
+    ws.fill_(255)
+    check(a, w, workspace=ws[:n - 16])  # too small: not used
+    assert (ws == 255).all()
+    a, w = make([20, 30], 64, 64)
     experts.expert_product(experts.Int8(a.data, a.scales, torch.tensor([0, 60, 50], dtype=torch.int32, device="cuda")), w)
     assert bn.check_device_error(raise_on_error=False) == bn.DEVERR_OFFSETS
     empty = experts.Int8(a.data[:0], a.scales[:0], torch.zeros(3, dtype=torch.int32, device="cuda"))

@@ -114,7 +114,7 @@ PRODUCT = dict(a=at(0), a_scales=at(1), M=40, w=at(2), w_scales=at(3), E=4, N=32
     (dict(M=-1), 1, "M=-1"), (dict(E=0), 1, "E=0"), (dict(E=2000), 2, "E=2000"), (dict(N=12), 1, "N=12"), (dict(N=1 << 21), 2, "N="), (dict(K=40), 1, "K=40"),
     (dict(K=131072), 2, "K=131072"), (dict(offsets=None), 1, "offsets"), (dict(alpha=math.inf), 1, "alpha"), (dict(a=None), 1, "a is NULL"),
     (dict(a_scales=at(1) + 2), 1, "a_scales"), (dict(w=at(2) + 8), 1, "w is not"), (dict(w_scales=None), 1, "w_scales is NULL"), (dict(out=None), 1, "out is NULL"),
-    (dict(ws=None), 1, "workspace is NULL"), (dict(bytes=40 * 64 * 2 - 1), 1, "workspace of"), (dict(ws=at(0)), 1, "workspace overlaps a"),
+    (dict(ws=at(6) + 8), 1, "workspace is not"), (dict(ws=at(0)), 1, "workspace overlaps a"),
     (dict(out=at(2)), 1, "out overlaps w"),
 ])
 def test_product_int8_refuses(L, kw, status, needle):
@@ -135,8 +135,9 @@ def test_no_rows_is_no_work(L):
 def test_workspace_bytes(L):
     assert experts.linear_workspace_bytes(32, 64) == 0 and experts.linear_workspace_bytes(33, 64) == 33 * 128
     assert experts.linear_workspace_bytes(100, 60) == 0
-    assert experts.product_int8_workspace_bytes(3, 64) == 384 and experts.product_int8_workspace_bytes(0, 64) == 0
-    assert experts.product_int8_workspace_bytes(2 ** 20, 131056) == 2 ** 21 * 131056
+    assert experts.product_int8_workspace_bytes(30, 4, 4096, 8192) == 0 and experts.product_int8_workspace_bytes(0, 1, 64, 64) == 0
+    assert experts.product_int8_workspace_bytes(2 ** 20, 8, 4096, 131056) == 2 ** 21 * 131056
+    assert experts.product_int8_workspace_bytes(800, 256, 6144, 1024) == 0  # a few rows for every expert
 
 
 def test_binding_refuses_what_is_not_on_a_gpu():

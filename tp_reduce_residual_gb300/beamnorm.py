@@ -151,7 +151,7 @@ def load() -> ctypes.CDLL:
             "bn_swiglu_backward": [_P, _I, _L, _I, _I, _P, _L, _P, _P],
             "bn_quantize_int8": [_P, _I, _L, _I, _P, _I, _I, _P, _P, _P],
             "bn_dequantize_int8": [_P, _P, _I, _I, _P, _I, _P],
-            "bn_expert_product_int8_workspace_bytes": [_I, _I],
+            "bn_expert_product_int8_workspace_bytes": [_I, _I, _I, _I],
             "bn_expert_product_int8": [_P, _P, _I, _P, _P, _I, _I, _I, _P, _F, _P, _P, ctypes.c_size_t, _P],
         }
         for name, args in sig.items():

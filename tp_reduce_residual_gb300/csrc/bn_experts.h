@@ -146,7 +146,9 @@ cudaError_t launch_linear(const LinearArgs &, LinearMode mode, const void *x, lo
 cudaError_t launch_swiglu(const SwigluArgs &, int dtype, bool backward, int sms, bool pdl, cudaStream_t);
 cudaError_t launch_quantize_int8(const Int8Args &, int dtype, bool pdl, cudaStream_t);
 cudaError_t launch_dequantize_int8(const Int8Args &, int dtype, bool pdl, cudaStream_t);
-// workspace: 2 M K bytes, for the rows widened to FP16 (large groups).
+// Whether pairs of CTAs serve the product; `split`: the CTAs that share a tile's sum, if not.
+bool product8_pairs(const Product8Args &, int sms, int *split);
+// workspace: 2 M K bytes, for the rows widened to FP16 where pairs serve, or null: no pairs.
 cudaError_t launch_product8(Product8Args, const int8_t *w, void *workspace, int sms, bool pdl, cudaStream_t);
 // out [M, K] dense: row rows[m] of x at place m (16-bit values).
 cudaError_t launch_place_rows(const void *x, long long ld, int x_rows, const int32_t *rows, int M, int K, void *out, unsigned *err,

@@ -1,7 +1,7 @@
 // bn_experts_abi.cu -- the C entry points around the experts: host-side
 // validation and launches.  Like the rest of the ABI, arguments are checked
-// before any CUDA call, and each call enqueues one kernel (two for a quantisation
-// or a linear layer with a workspace) or nothing.
+// before any CUDA call, and each call enqueues one kernel (two for a call that
+// goes through a workspace) or nothing.
 #include <cmath>
 
 #include <cuda_runtime.h>
@@ -17,6 +17,7 @@ namespace {
 // Rows and slots are counted in int32, rounded up to tiles and blocks.
 constexpr long long kMaxRows = (1LL << 31) - 1024;
 constexpr int kMaxInt8K = 131056;
+constexpr int kNominalSms = 152;  // of a GB300, where no device is asked
 
 size_t dtype_size(int dtype) { return dtype == BN_FP32 ? 4 : 2; }
 
@@ -671,9 +672,16 @@ bn_status bn_dequantize_int8(const int8_t *data, const float *scales, int M, int
                     "launching dequantize_int8");
 }
 
-size_t bn_expert_product_int8_workspace_bytes(int M, int K)
+size_t bn_expert_product_int8_workspace_bytes(int M, int E, int N, int K)
 {
-    return M > 0 && K >= 16 && K % 16 == 0 ? (size_t)M * K * 2 : 0;
+    if (M < 1 || E < 1 || N < 8 || N % 8 != 0 || K < 16 || K % 16 != 0) return 0;
+    Product8Args p = {};
+    p.M = M;
+    p.E = E;
+    p.N = N;
+    p.K = K;
+    int split;
+    return product8_pairs(p, kNominalSms, &split) ? (size_t)M * K * 2 : 0;
 }
 
 bn_status bn_expert_product_int8(const int8_t *a, const float *a_scales, int M, const int8_t *w, const float *w_scales,
@@ -695,9 +703,7 @@ bn_status bn_expert_product_int8(const int8_t *a, const float *a_scales, int M, 
     BN_TRY(check_ptr16(w, "w"));
     BN_TRY(check_ptr4(w_scales, "w_scales"));
     BN_TRY(check_ptr16(out, "out"));
-    BN_TRY(check_ptr16(workspace, "workspace"));
-    const size_t need = bn_expert_product_int8_workspace_bytes(M, K);
-    BN_REQUIRE(workspace_bytes >= need, "workspace of %zu bytes is below %zu", workspace_bytes, need);
+    BN_TRY(check_ptr16(workspace, "workspace", false));
     const Range writes[] = {{out, (size_t)M * N * 2, "out"}, {workspace, workspace_bytes, "workspace"}};
     const Range reads[] = {{a, (size_t)M * K, "a"},
                            {a_scales, (size_t)M * 4, "a_scales"},
@@ -719,7 +725,8 @@ bn_status bn_expert_product_int8(const int8_t *a, const float *a_scales, int M, 
     p.alpha = alpha;
     p.out = out;
     p.err = d->err;
-    return launched(launch_product8(p, w, workspace, d->sms, dependent_launch(), (cudaStream_t)stream),
+    void *wide = workspace_bytes >= (size_t)M * K * 2 ? workspace : nullptr;
+    return launched(launch_product8(p, w, wide, d->sms, dependent_launch(), (cudaStream_t)stream),
                     "launching expert_product_int8");
 }
 

@@ -548,13 +548,15 @@ cudaError_t launch_shape8(const Product8Args &p, const Maps8 &maps, int sms, boo
     return launch_kernel(k, dim3((unsigned)grid), dim3(S::kThreads), S::smem(p.E), pdl, ctas, st, maps, p);
 }
 
+}  // namespace
+
 // Which shape: pairs where that makes fewer rounds of tiles over the device (groups are taken to
 // leave half a tile each).  Measured, narrow / pairs (us in a graph): 100 tokens with 8 of 256
 // experts of 6144 x 1024 180 / 181 (as many rounds); 500 with 8 of 64, 2048 x 2048 102 / 63;
 // 333 with 4 of 16, 1024 x 2048 26.7 / 19.6; 256 with 2 of 8, 4096 x 4096 59 / 37; 4096 with 8 of
 // 64, 4096 x 5120 2869 / 938.  A narrow tile's sum is split as in bn_linear.cu; a join costs
 // 5 stages of 128 values.
-bool choose_pairs(Product8Args &p, int sms)
+bool product8_pairs(const Product8Args &p, int sms, int *split)
 {
     const long long groups = p.E < p.M ? p.E : p.M, nk = (p.K + kDepth - 1) / kDepth;
     const auto rounds = [&](int rows, int tile, int units) {
@@ -563,19 +565,17 @@ bool choose_pairs(Product8Args &p, int sms)
     };
     constexpr int kRows = Shape8<false>::kRows;
     const long long tiles = ((long long)p.M + groups * (kRows - 1)) / kRows * ((p.N + 127) / 128);
-    p.split = choose_split(tiles, nk, 5, (tiles + sms - 1) / sms * nk, sms);
-    if (p.split > 1) return false;
+    *split = choose_split(tiles, nk, 5, (tiles + sms - 1) / sms * nk, sms);
+    if (*split > 1 || p.M <= kRows) return false;
     return rounds(Shape8<true>::kRows, Shape8<true>::kTile, sms / 2) < rounds(kRows, 128, sms);
 }
-
-}  // namespace
 
 cudaError_t launch_product8(Product8Args p, const int8_t *w, void *workspace, int sms, bool pdl, cudaStream_t st)
 {
     cudaError_t e = tensor_maps_ready();
     if (e != cudaSuccess) return e;
     Maps8 m;
-    const bool pair = choose_pairs(p, sms);
+    const bool pair = product8_pairs(p, sms, &p.split) && workspace;
     if (pair) {
         const long long n = (long long)p.M * p.K / 16, blocks = (n + 255) / 256, most = 16LL * sms;
         e = launch_kernel(widen_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, pdl, 1, st,

@@ -307,9 +307,9 @@ def expert_product(a, w, scale: float = 1.0, out=None, workspace=None, stream=No
     """out [M,N] BF16: each row of ``a`` ([M,K], grouped by ``a.offsets``) times
     its group's weights of ``w`` ([E,N,K]; [N,K] is one expert), times ``scale``
     and the operands' scales.  Both are FP4 or both Int8, whose sums are exact.  Rows
-    before the first group and past the last are zeros.  Int8 rows go through a
-    ``workspace`` (a 1-D uint8 tensor of ``product_int8_workspace_bytes``; by default one is
-    allocated for the call); FP4 ones take none."""
+    before the first group and past the last are zeros.  Int8 rows of large groups go
+    through a ``workspace`` (a 1-D uint8 tensor of ``product_int8_workspace_bytes``; by
+    default one is allocated for the call); FP4 ones take none."""
     if isinstance(a, Int8):
         return _expert_product_int8(a, w, scale, out, workspace, stream)
     if workspace is not None:
@@ -371,11 +371,11 @@ def linear_workspace_bytes(M: int, K: int) -> int:
     return (_bn._lib or _bn.load()).bn_expert_linear_workspace_bytes(M, K)
 
 
-def _place_workspace(workspace, rp, M, K, dev, stream):
-    """The caller's workspace, or one for the call from its stream's pool: address, bytes, and the tensor to keep."""
+def _call_workspace(workspace, n, dev, stream):
+    """The caller's workspace, or one of n bytes for the call from its stream's pool: address, bytes, and the
+    tensor to keep."""
     if workspace is not None:
         return (*_bn._workspace(workspace, dev), workspace)
-    n = linear_workspace_bytes(M, K) if rp is not None else 0
     if n == 0:
         return None, 0, None
     workspace = torch.empty(n, dtype=_UINT8, device=dev) if stream is None else _bn._empty((n,), _UINT8, dev, stream)
@@ -400,7 +400,7 @@ def expert_linear(x, w, offsets=None, rows=None, out=None, workspace=None, strea
         raise ValueError(f"x has rows of {x.shape[1]} values, w of {K}")
     op = _groups(offsets, E, dev)
     out, yp = _out(out, "out", x.dtype, (M, N), dev, stream)
-    sp, n, workspace = _place_workspace(workspace, rp, M, K, dev, stream)
+    sp, n, workspace = _call_workspace(workspace, linear_workspace_bytes(M, K) if rp is not None else 0, dev, stream)
     _call("bn_expert_linear", (x.data_ptr(), dtype, ld, x.shape[0], rp, M, wp, E, N, K, op, yp, sp, n), dev.index, stream)
     return out
 
@@ -448,7 +448,7 @@ def expert_linear_dw(dy, x, offsets=None, rows=None, dtype=None, dw=None, accumu
     if want not in (x.dtype, _FLOAT32) or (dtype is not None and dtype is not want):
         raise TypeError(f"dw must be {x.dtype} or torch.float32 (got {dtype or want})")
     dw, wp = _out(dw, "dw", want, (N, K) if offsets is None else (E, N, K), dev, stream)
-    sp, n, workspace = _place_workspace(workspace, rp, M, K, dev, stream)
+    sp, n, workspace = _call_workspace(workspace, linear_workspace_bytes(M, K) if rp is not None else 0, dev, stream)
     _call("bn_expert_linear_dw", (dy.data_ptr(), d, ld_dy, M, x.data_ptr(), ld, x.shape[0], rp, E, N, K, op, wp, _DTYPES[want],
                                   1 if accumulate else 0, sp, n), dev.index, stream)
     return dw
@@ -535,9 +535,10 @@ def dequantize_int8(q: Int8, dtype=torch.bfloat16, out=None, stream=None) -> tor
     return out
 
 
-def product_int8_workspace_bytes(M: int, K: int) -> int:
-    """Workspace bytes that ``expert_product`` needs for M Int8 rows of K values."""
-    return (_bn._lib or _bn.load()).bn_expert_product_int8_workspace_bytes(M, K)
+def product_int8_workspace_bytes(M: int, E: int, N: int, K: int) -> int:
+    """Workspace bytes with which ``expert_product`` widens M Int8 rows of K values once
+    for E experts of N rows, or 0 where it needs none."""
+    return (_bn._lib or _bn.load()).bn_expert_product_int8_workspace_bytes(M, E, N, K)
 
 
 def _expert_product_int8(a: Int8, w: Int8, scale, out, workspace, stream) -> torch.Tensor:
@@ -556,11 +557,6 @@ def _expert_product_int8(a: Int8, w: Int8, scale, out, workspace, stream) -> tor
     E, N = shape[:2] if len(shape) == 3 else (1, shape[0])
     op = _groups(a.offsets, E, dev)
     out, yp = _out(out, "out", torch.bfloat16, (M, N), dev, stream)
-    if workspace is not None:
-        xp, n = _bn._workspace(workspace, dev)
-    else:
-        n = product_int8_workspace_bytes(M, K)
-        workspace = torch.empty(n, dtype=_UINT8, device=dev) if stream is None else _bn._empty((n,), _UINT8, dev, stream)
-        xp = workspace.data_ptr()
+    xp, n, workspace = _call_workspace(workspace, 0 if workspace is not None else product_int8_workspace_bytes(M, E, N, K), dev, stream)
     _call("bn_expert_product_int8", (ap, sp, M, wp, wsp, E, N, K, op, scale, yp, xp, n), dev.index, stream)
     return out
