@@ -10,8 +10,8 @@
 // One kernel in three modes.  Forward and input gradient: the output's contiguous
 // dimension (n, k: features) is the tensor core's M operand and rows are its N operand, so
 // that the few rows an expert has in a decode batch cost a narrow product and each weight is
-// read once.  Weight gradient: n and k, so that a lane holds a part of a row of dw, which
-// goes out by TMA; its tiles are all whole and its sums short, so their way out counts.  What is
+// read once.  Weight gradient: n and k, so that a lane holds a part of a row of dw; its tiles
+// are all whole and its sums short, so their way out counts.  What is
 // summed over lies along the rows in memory (forward: both operands; input gradient: dy)
 // or across them (w there, both operands of the weight gradient): the tensor core takes
 // either, as a bit of its descriptor.
@@ -33,8 +33,8 @@
 // x 8192 and as many rows 549 us by tall pairs (2.00 PFLOP/s).  Rows by index cost the
 // place in the workspace, 70 us of 1020.  Few rows: the stream of weights; 100 tokens with 8 of
 // 256 experts of 6144 x 512 179 us (6.7 TB/s), one token with 10 of 512 x 8192 19 us (4.4).
-// dw of 4096 tokens with 8 of 64, 5120 x 2048 (1.34 GB) 500 us: shared memory carries the
-// operands and what goes out.
+// dw of 4096 tokens with 8 of 64, 5120 x 2048 (1.34 GB) 470 us, 340 without its way out, 600
+// by transposed pieces of 16 bytes; added to 2.7 GB in FP32 1090 (800 at the copy rate).
 #include "../../include/beamnorm.h"
 #include "bn_device.cuh"
 #include "bn_experts.h"
@@ -68,9 +68,8 @@ struct LinearShape {
     static constexpr int kJoinBytes = SHAPE == kSplit ? (kRows + kMaxSplit) * kHalf * 4 : 0;  // parts of a split sum
     static constexpr int kOutWarps = kPairs ? 8 : 4;
     static constexpr int kThreads = 64 + 32 * kOutWarps;  // copies, products, output
-    // output warps' boxes of 32 rows by 128 bytes on their way to a weight gradient
-    static constexpr int kOutBoxes = SHAPE == kPair ? 1 : 2;
-    static constexpr int kOutBytes = WEIGHTS ? kOutWarps * kOutBoxes * 4096 : 0;
+    // 32 rows by 128 bytes of each output warp, on their way to a weight gradient
+    static constexpr int kOutBytes = WEIGHTS ? kOutWarps * 4096 : 0;
     static constexpr size_t smem(int E) { return 1024 + (size_t)kStages * kStageBytes + kOutBytes + kJoinBytes + 2 * sizeof(int) * (size_t)(E + 1); }
 };
 
@@ -79,7 +78,7 @@ struct LinearMaps {
     CUtensorMap q, q_small;        // the rows' operand: x, or dy of the input gradient, in boxes of 128 (64) and 16 rows
     CUtensorMap p_rows, q_rows;    // row by row: dy and x of the weight gradient, x of the forward
     CUtensorMap p16, p4, q16, q4;  // the weight gradient's in boxes of 16 and 4 rows
-    CUtensorMap out;               // the weight gradient in boxes of 32 rows by 128 bytes
+    CUtensorMap out;               // an FP32 weight gradient that is added to, in boxes of 32 rows by 32
 };
 
 // The weight gradient's tiles: experts one after another, of one expert the tiles along a
@@ -446,7 +445,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
         const int quad = warp & 3;         // the lanes of tensor memory that this warp reads
         const int half = (warp - 2) >> 2;  // of a pair's columns
         const bool fp16 = p.dtype == BN_FP16;
-        uint32_t n = 0, stored = 0;
+        uint32_t n = 0;
         // accumulator i is full; it has been taken out
         const auto taken = [&](uint32_t i) {
             const bool ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(acc_full + 8 * (i & 1u), (i >> 1) & 1u, ctl));
@@ -505,14 +504,16 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 __syncwarp();
                 if (lane < (int)parts_n) arrive_cluster(mapa(joinable, (uint32_t)lane));
             } else if constexpr (kWeights) {
-                // A lane's row of dw, 128 bytes of it at a time through shared memory to a box of
-                // 32 rows; what lies past the matrix is not stored.  Each half has 128 columns.
+                // A lane's row of dw, 128 bytes of it at a time, through shared memory (swizzled, so
+                // that neither way has conflicts), and 4 whole lines a store from there; where it is
+                // added to what dw holds, by TMA, which adds there (loads would wait for DRAM: 2.7
+                // times as long).  Storing by TMA as well took 6 % longer: its rows queue with
+                // those that come in.  Each half has 128 columns.
                 const bool none = depth() == 0;  // an empty group: zeros, or nothing to add
                 const int width = p.out_fp32 ? 32 : 64;
-                const uint32_t boxes = base + kStages * S::kStageBytes + (uint32_t)(warp - 2) * S::kOutBoxes * 4096u;
+                const uint32_t box = base + kStages * S::kStageBytes + (uint32_t)(warp - 2) * 4096u;
                 const int end = none && p.accumulate ? 0 : min(half * 128 + 128, t.rows);
                 for (int c = half * 128; c < end; c += width) {
-                    const uint32_t at = boxes + (uint32_t)(stored++ % S::kOutBoxes) * 4096u;
                     uint32_t v[32];
 #pragma unroll
                     for (int b = 0; b < 2; ++b) {
@@ -532,27 +533,32 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                         }
                     }
                     if (c + width >= end) release(n);
-                    // the copy that read this box last has ended
-                    asm volatile("cp.async.bulk.wait_group.read %0;" ::"n"(S::kOutBoxes - 1) : "memory");
+                    if (p.accumulate) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
                     __syncwarp();
 #pragma unroll
                     for (int i = 0; i < 8; ++i) {
                         const uint4 w = none ? make_uint4(0, 0, 0, 0) : make_uint4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
-                        asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at + (uint32_t)lane * 128u + (uint32_t)((i ^ (lane & 7)) << 4)),
-                                     "r"(w.x), "r"(w.y), "r"(w.z), "r"(w.w) : "memory");
+                        store_shared(box + (uint32_t)lane * 128u + (uint32_t)((i ^ (lane & 7)) << 4), w);
                     }
-                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                    __syncwarp();
-                    if (lane == 0) {  // always this lane: copies are counted by thread
-                        if (f0 < p.F) {
-                            if (p.accumulate)
-                                asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&maps.out),
-                                             "r"(t.row0 + c), "r"(f0), "r"(t.e), "r"(at) : "memory");
-                            else
-                                asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&maps.out),
-                                             "r"(t.row0 + c), "r"(f0), "r"(t.e), "r"(at) : "memory");
+                    if (p.accumulate) {
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                        if (lane == 0 && f0 < p.F) {  // what lies past the matrix is not added
+                            asm volatile("cp.reduce.async.bulk.tensor.3d.global.shared::cta.add.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(&maps.out),
+                                         "r"(t.row0 + c), "r"(f0), "r"(t.e), "r"(box) : "memory");
+                            asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                         }
-                        asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                        continue;
+                    }
+                    __syncwarp();
+                    const int k = t.row0 + c + (lane & 7) * (width / 8);
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) {
+                        const int r = 4 * i + (lane >> 3);
+                        const uint4 w = load_shared(box + (uint32_t)r * 128u + (uint32_t)(((lane ^ r) & 7) << 4));
+                        const long long at = ((long long)t.e * p.F + f0 + r) * p.K + k;
+                        if (f0 + r < p.F && k < p.K)
+                            *reinterpret_cast<uint4 *>(static_cast<char *>(p.out) + (p.out_fp32 ? 4 * at : 2 * at)) = w;
                     }
                 }
                 if (half * 128 >= end) release(n);
@@ -610,8 +616,6 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 }
             }
         }
-        // the last boxes have left shared memory, and are written
-        if constexpr (kWeights) asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");
         if constexpr (!kWeights) {  // rows of no group: before the first, and past the last
             const long long step = (long long)gridDim.x * (S::kThreads - 64);
             uint4 *out = static_cast<uint4 *>(p.out);
@@ -622,6 +626,8 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
             };
             zeros(0, start[0]);
             zeros(start[p.E], p.M);
+        } else {
+            asm volatile("cp.async.bulk.wait_group 0;" ::: "memory");  // the last boxes have been added
         }
     }
     fence_before();
@@ -652,9 +658,9 @@ cudaError_t make_linear_maps(LinearMaps *m, const LinearArgs &p, LinearMode mode
         if (e == cudaSuccess) e = matrix(&m->q_rows, x, n, p.K, ld, 1);
         if (e == cudaSuccess) e = matrix(&m->q16, x, n, p.K, ld, 16);
         if (e == cudaSuccess) e = matrix(&m->q4, x, n, p.K, ld, 4);
-        if (e == cudaSuccess)
-            e = make_map<3>(&m->out, p.out_fp32 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT32 : type, p.out_fp32 ? 4 : 2, p.out,
-                            {(cuuint64_t)p.K, (cuuint64_t)p.F, (cuuint64_t)p.E}, {p.out_fp32 ? 32u : 64u, 32, 1}, CU_TENSOR_MAP_SWIZZLE_128B);
+        if (e == cudaSuccess && p.accumulate)
+            e = make_map<3>(&m->out, CU_TENSOR_MAP_DATA_TYPE_FLOAT32, 4, p.out, {(cuuint64_t)p.K, (cuuint64_t)p.F, (cuuint64_t)p.E}, {32, 32, 1},
+                            CU_TENSOR_MAP_SWIZZLE_128B);
         m->q_small = m->q;
         return e;
     }
@@ -663,12 +669,12 @@ cudaError_t make_linear_maps(LinearMaps *m, const LinearArgs &p, LinearMode mode
                     CU_TENSOR_MAP_SWIZZLE_128B);
     if (p.rows) {
         if (e == cudaSuccess) e = matrix(&m->q_rows, x, p.x_rows, p.D, ld, 1);
-        m->out = m->q = m->q_small = m->p_rows = m->p16 = m->p4 = m->q16 = m->q4 = m->q_rows;
+        m->q = m->q_small = m->p_rows = m->p16 = m->p4 = m->q16 = m->q4 = m->q_rows;
         return e;
     }
     if (e == cudaSuccess) e = matrix(&m->q, x, p.M, p.D, ld, kHalf);
     if (e == cudaSuccess) e = matrix(&m->q_small, x, p.M, p.D, ld, kBoxRows);
-    m->out = m->p_rows = m->q_rows = m->p16 = m->p4 = m->q16 = m->q4 = m->q_small;
+    m->p_rows = m->q_rows = m->p16 = m->p4 = m->q16 = m->q4 = m->q_small;
     return e;
 }
 
@@ -712,7 +718,7 @@ cudaError_t launch_shape(const LinearArgs &p, const LinearMaps &maps, int sms, b
 // one expert, 8192 x 8192 and as many rows 870 / 596 / 549, 1024 rows 135 / 96 / 88, 512
 // 72 / 57 / 86; 1000 with 8 of 64, 4096 x 4096 387 / 363 / 406; 1024 with 2 of 8, 2048 x
 // 2048 33 / 37 / 39.  A weight gradient's tiles are all whole: 333 with 4 of 16, 1024 x 2048
-// 47 / 37; 4096 with 8 of 64, 5120 x 2048 913 / 612 (both before its way out by TMA).
+// 47 / 37; 4096 with 8 of 64, 5120 x 2048 913 / 612 (both before its way out in whole lines).
 int choose_shape(LinearArgs &p, int mode, int sms)
 {
     const long long groups = p.E < p.M ? p.E : p.M;
@@ -790,7 +796,7 @@ cudaError_t launch_linear(const LinearArgs &p, LinearMode mode, const void *x, l
 {
     const cudaError_t ready = tensor_maps_ready();
     if (ready != cudaSuccess) return ready;
-    LinearMaps maps;
+    LinearMaps maps = {};
     const cudaError_t e = make_linear_maps(&maps, p, mode, x, ld, w, w_ld);
     if (e != cudaSuccess) return e;
     switch (mode) {

@@ -257,6 +257,18 @@ __device__ __forceinline__ uint4 transpose8(const uint32_t *w, int lane)
     return lane & 4 ? make_uint4(o0, o1, b[1][0], b[1][1]) : make_uint4(b[0][0], b[0][1], o0, o1);
 }
 
+__device__ __forceinline__ uint4 load_shared(uint32_t addr)
+{
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr) : "memory");
+    return v;
+}
+
+__device__ __forceinline__ void store_shared(uint32_t addr, const uint4 &v)
+{
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(addr), "r"(v.x), "r"(v.y), "r"(v.z), "r"(v.w) : "memory");
+}
+
 // A value into the shared memory of a CTA of the cluster, counted on its barrier there.
 __device__ __forceinline__ void send_cluster(uint32_t addr, uint32_t v, uint32_t bar)
 {
