@@ -326,3 +326,19 @@ def test_captured_and_replayed():
 def test_tall_tiles(sizes, N, K):
     """A few large groups: pairs whose tiles have 512 rows, with odd last tiles of one block and of two."""
     check(make(sizes, N, K, "bf16", seed=13, before=1, after=40), whole=True)
+
+
+@pytest.mark.parametrize("N,K", [(72, 200), (2048, 1536)])
+def test_long_gradients_keep_32_bits(N, K):
+    """Sums of one sign over 8192 rows.  The tensor core's sums lose at most 2^-23 a step of 16 rows, in runs of
+    256 rows: 16 * 2^-23 of a run; 32 runs are added, 2^-24 of the sum each: 32 * 2^-24."""
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, dy = (torch.rand(8200, n, generator=g, device="cuda").bfloat16() for n in (K, N))
+    o = torch.tensor([0, 8192, 8200], dtype=torch.int32, device="cuda")
+    dw = experts.expert_linear_dw(dy, x, o, dtype=torch.float32)
+    for e, s in ((0, slice(0, 8192)), (1, slice(8192, 8200))):
+        want = dy[s].double().T @ x[s].double()
+        assert ((dw[e].double() - want).abs() <= (16 * 2.0 ** -23 + 32 * 2.0 ** -24) * want).all()
+    want = dy[:8192].double().T @ x[:8192].double()
+    half = experts.expert_linear_dw(dy, x, o)[0].double()  # runs of 4096 rows: 256 steps
+    assert ((half - want).abs() <= (2.0 ** -8 + 256 * 2.0 ** -23 + 2.0 ** -23) * want).all()

@@ -216,6 +216,10 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
     Tile t = {};
     // the length of a tile's sum
     const auto depth = [&]() { return kWeights ? max(start[t.e + 1] - start[t.e], 0) : p.D; };
+    // The tensor core drops what its FP32 sums cannot hold, always towards zero: 1e-9 of the
+    // sum a value (2e-6 over 1024 rows of one sign).  A weight gradient in FP32 is summed so over
+    // 4 stages, one in 16 bits over 64, and those sums are added with rounding.
+    const int run = p.out_fp32 ? 4 : 64;
     // the stages of it that this CTA sums
     const auto stages = [&](int d, int &k0, int &k1) {
         const int nk = (d + kDepth - 1) / kDepth;
@@ -395,6 +399,12 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 stages(d, k0, k1);
                 for (int k = k0; k < k1; ++k, ++it) {
                     const uint32_t s = it % kStages;
+                    const bool first = kWeights ? k % run == 0 : k == k0;
+                    if (kWeights && first && k > 0) {  // on to the other accumulator
+                        ++n;
+                        ok = accumulator(0);
+                        if (!ok) break;
+                    }
                     ok = __all_sync(kAll, wait_phase<PAIR, kPipe>(full + 8 * s, (it / kStages) & 1u, ctl));
                     if (!ok) break;
                     fence_after();
@@ -418,14 +428,14 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                             if (k * kDepth + kDepth <= d) {  // unrolled: the issuing thread sets the pace
 #pragma unroll
                                 for (int j = 0; j < 4; ++j)
-                                    product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, k > k0 || j > 0);
+                                    product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, !first || j > 0);
                             } else {
                                 const int steps = (d - k * kDepth + 15) / 16;
                                 for (int j = 0; j < steps; ++j)
-                                    product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, k > k0 || j > 0);
+                                    product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, !first || j > 0);
                             }
                             if (b == blocks - 1) commit<PAIR>(empty + 8 * s);
-                            if (k == k1 - 1) commit<PAIR>(acc_full + 8 * ((n + b) & 1u));
+                            if (k == k1 - 1 || (kWeights && (k + 1) % run == 0)) commit<PAIR>(acc_full + 8 * ((n + b) & 1u));
                         }
                     }
                     if (!ok) break;
@@ -460,7 +470,9 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 else mbar_arrive(acc_empty + 8 * (i & 1u));
             }
         };
-        for (; tiles.next(t, lane); n += (uint32_t)blocks_of()) {
+        // a tile's accumulators: its products, or the runs of a weight gradient's sum
+        const auto sums_of = [&]() { return kWeights ? max((depth() + kDepth * run - 1) / (kDepth * run), 1) : blocks_of(); };
+        for (; tiles.next(t, lane); n += (uint32_t)sums_of()) {
             if (!taken(n)) break;
             const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), acc = lanes + (n & 1u) * kBlock;
             const long long row0 = t.row0;
@@ -513,26 +525,9 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 const int width = p.out_fp32 ? 32 : 64;
                 const uint32_t box = base + kStages * S::kStageBytes + (uint32_t)(warp - 2) * 4096u;
                 const int end = none && p.accumulate ? 0 : min(half * 128 + 128, t.rows);
-                for (int c = half * 128; c < end; c += width) {
-                    uint32_t v[32];
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        uint32_t x[16];
-                        if (p.out_fp32) {
-                            read16(acc + c + 16 * b, x);
-#pragma unroll
-                            for (int i = 0; i < 16; ++i) v[16 * b + i] = x[i];
-                        } else {
-#pragma unroll
-                            for (int h = 0; h < 2; ++h) {
-                                read16(acc + c + 32 * b + 16 * h, x);
-#pragma unroll
-                                for (int i = 0; i < 8; ++i)
-                                    v[16 * b + 8 * h + i] = round16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), fp16);
-                            }
-                        }
-                    }
-                    if (c + width >= end) release(n);
+                const int runs = sums_of();
+                // 128 bytes of every lane's row, at column c
+                const auto emit = [&](int c, const uint32_t *v) {
                     if (p.accumulate) asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");  // the last box has been read
                     __syncwarp();
 #pragma unroll
@@ -548,7 +543,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                                          "r"(t.row0 + c), "r"(f0), "r"(t.e), "r"(box) : "memory");
                             asm volatile("cp.async.bulk.commit_group;" ::: "memory");
                         }
-                        continue;
+                        return;
                     }
                     __syncwarp();
                     const int k = t.row0 + c + (lane & 7) * (width / 8);
@@ -560,8 +555,66 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                         if (f0 + r < p.F && k < p.K)
                             *reinterpret_cast<uint4 *>(static_cast<char *>(p.out) + (p.out_fp32 ? 4 * at : 2 * at)) = w;
                     }
+                };
+                if (runs == 1) {
+                    for (int c = half * 128; c < end; c += width) {
+                        uint32_t v[32];
+#pragma unroll
+                        for (int b = 0; b < 2; ++b) {
+                            uint32_t x[16];
+                            if (p.out_fp32) {
+                                read16(acc + c + 16 * b, x);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) v[16 * b + i] = x[i];
+                            } else {
+#pragma unroll
+                                for (int h = 0; h < 2; ++h) {
+                                    read16(acc + c + 32 * b + 16 * h, x);
+#pragma unroll
+                                    for (int i = 0; i < 8; ++i)
+                                        v[16 * b + 8 * h + i] = round16(__uint_as_float(x[2 * i]), __uint_as_float(x[2 * i + 1]), fp16);
+                                }
+                            }
+                        }
+                        if (c + width >= end) release(n);
+                        emit(c, v);
+                    }
+                    if (half * 128 >= end) release(n);
+                } else {
+                    float sums[128];
+                    bool ok = true;
+#pragma unroll
+                    for (int i = 0; i < 128; ++i) sums[i] = 0.0f;
+                    for (int u = 0; u < runs; ++u) {
+                        ok = u == 0 || taken(n + u);
+                        if (!ok) break;
+                        const uint32_t from = lanes + ((n + u) & 1u) * kBlock + half * 128;
+#pragma unroll
+                        for (int b = 0; b < 8; ++b) {
+                            if (half * 128 + 16 * b < end) {
+                                uint32_t x[16];
+                                read16(from + 16 * b, x);
+#pragma unroll
+                                for (int i = 0; i < 16; ++i) sums[16 * b + i] += __uint_as_float(x[i]);
+                            }
+                        }
+                        release(n + u);
+                    }
+                    if (!ok) break;
+                    if (p.out_fp32) {
+#pragma unroll
+                        for (int q = 0; q < 4; ++q)
+                            if (half * 128 + 32 * q < end) emit(half * 128 + 32 * q, reinterpret_cast<const uint32_t *>(sums) + 32 * q);
+                    } else {
+#pragma unroll
+                        for (int q = 0; q < 2; ++q) {
+                            uint32_t v[32];
+#pragma unroll
+                            for (int i = 0; i < 32; ++i) v[i] = round16(sums[64 * q + 2 * i], sums[64 * q + 2 * i + 1], fp16);
+                            if (half * 128 + 64 * q < end) emit(half * 128 + 64 * q, v);
+                        }
+                    }
                 }
-                if (half * 128 >= end) release(n);
             } else {
                 // the whole tile in 16 bits in registers, so that the next product can start
                 const int f = f0 + (lane & ~7);
