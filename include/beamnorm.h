@@ -492,19 +492,28 @@ BN_API bn_status bn_swiglu(const void *x, bn_dtype dtype, long long ld, int M, i
 BN_API bn_status bn_swiglu_backward(const void *x, bn_dtype dtype, long long ld, int M, int F,
                                     const void *dy, long long ld_dy, void *dx, void *stream);
 
+/* Bytes of workspace with which bn_quantize_int8 quantises the x_rows rows of x once and
+ * copies them to the M places that take them, or 0 where that does not pay.  Pure host
+ * logic.
+ * Source: no passage: library utility. */
+BN_API size_t bn_quantize_int8_workspace_bytes(int x_rows, int M, int K);
+
 /* Rows in 8-bit integers with a scale a row: row m is row rows[m] (or m) of x.
  *   x        [x_rows, K] BF16, FP16 or FP32, rows of 16-byte pieces `ld` elements apart
  *   rows     [M] int32 or NULL; values outside [0, x_rows) set
  *            BN_DEVERR_PERM_RANGE and read row 0
  *   data     [M, K]: codes in [-127, 127]
  *   scales   [M] FP32: max|x| of the row / 127, rounded; a value is code * scale
+ *   workspace  device memory of workspace_bytes, 16-byte aligned, or NULL; used when rows
+ *            is given and it holds bn_quantize_int8_workspace_bytes() (not 0), for two
+ *            kernels on `stream` instead of one.  Nothing in it is kept
  * K is a multiple of 16, at most 131056.  Codes are x / scale to the nearest whole
  * number, half way to the even one, exactly decided.  A row with an infinity or a NaN
  * gets a NaN scale and codes 0.
  * Source: none -- it has no counterpart on the pages. */
 BN_API bn_status bn_quantize_int8(const void *x, bn_dtype dtype, long long ld, int x_rows,
                                   const int32_t *rows, int M, int K, int8_t *data, float *scales,
-                                  void *stream);
+                                  void *workspace, size_t workspace_bytes, void *stream);
 
 /* The values [M, K] of such rows in BF16, FP16 or FP32: code * scale in FP32, rounded.
  * Source: none -- it has no counterpart on the pages. */

@@ -342,3 +342,15 @@ def test_long_gradients_keep_32_bits(N, K):
     want = dy[:8192].double().T @ x[:8192].double()
     half = experts.expert_linear_dw(dy, x, o)[0].double()  # runs of 4096 rows: 256 steps
     assert ((half - want).abs() <= (2.0 ** -8 + 256 * 2.0 ** -23 + 2.0 ** -23) * want).all()
+
+
+def test_many_experts():
+    """1024 experts, most of them empty, a few large."""
+    g = torch.Generator().manual_seed(3)
+    sizes = [0] * 1024
+    for e in torch.randint(0, 1024, (300,), generator=g).tolist():
+        sizes[e] += 1
+    sizes[5], sizes[1023] = 300, 40
+    for gather in (False, True):
+        check(make(sizes, 72, 40, "bf16", gather=gather, before=1, after=2), whole=True)
+    check(make([0] * 1023 + [3], 128, 1024, "fp16", gather=True), whole=True)

@@ -175,3 +175,13 @@ def test_streams_and_graphs():
         for g, _ in graphs:
             g.replay()
         assert all(torch.equal(out, expected(a, w)) for _, out in graphs)
+
+
+def test_many_experts():
+    g = torch.Generator().manual_seed(3)
+    sizes = [0] * 1024
+    for e in torch.randint(0, 1024, (300,), generator=g).tolist():
+        sizes[e] += 1
+    sizes[5], sizes[1023] = 300, 40
+    check(*make(sizes, 72, 48, before=1, after=2))
+    check(*make([0] * 1023 + [3], 128, 2048))

@@ -182,3 +182,22 @@ def test_int8_weights():
     assert torch.equal(q.data.view(120, 80), codes) and torch.equal(q.scales.view(-1), scales)
     assert experts.dequantize_int8(q).shape == (3, 40, 80)
     assert experts.quantize_int8(w[0, :0]).data.shape == (0, 80)
+
+
+@pytest.mark.parametrize("n,M,K", [(500, 5000, 4096), (3000, 9000, 3008), (1, 20000, 1040)])
+def test_int8_repeated_rows_through_a_workspace(n, M, K):
+    """Rows quantised once and copied: the codes and scales of place by place."""
+    x = torch.randn(n, K, generator=gen(n), device="cuda").bfloat16()
+    x[0, 3] = float("nan")
+    rows = torch.randint(0, n, (M,), generator=gen(M), device="cuda").to(torch.int32)
+    rows[7], rows[M - 1] = n, -5
+    size = experts.quantize_int8_workspace_bytes(n, M, K)
+    assert size == n * (K + 4)
+    ws = torch.full((size + 32,), 255, dtype=torch.uint8, device="cuda")
+    once = experts.quantize_int8(x, rows=rows, workspace=ws[:size])
+    assert bn.check_device_error(raise_on_error=False) == bn.DEVERR_PERM_RANGE and (ws[size:] == 255).all()
+    ws.fill_(255)
+    each = experts.quantize_int8(x, rows=rows, workspace=ws[:16])
+    assert bn.check_device_error(raise_on_error=False) == bn.DEVERR_PERM_RANGE and (ws == 255).all()
+    assert torch.equal(once.data, each.data) and torch.equal(once.scales.nan_to_num(-1), each.scales.nan_to_num(-1))
+    assert experts.quantize_int8_workspace_bytes(100, 199, 65536) == 0 and experts.quantize_int8_workspace_bytes(100, 800, 1024) == 0

@@ -86,14 +86,14 @@ def test_swiglu_backward_refuses(L, kw, status, needle):
     refuses(L, "bn_swiglu_backward", status, needle, *dict(args, **kw).values())
 
 
-INT8 = dict(x=at(0), dtype=0, ld=64, x_rows=20, rows=at(1), M=40, K=64, data=at(2), scales=at(3), stream=None)
+INT8 = dict(x=at(0), dtype=0, ld=64, x_rows=20, rows=at(1), M=40, K=64, data=at(2), scales=at(3), ws=at(4), bytes=1360, stream=None)
 
 
 @pytest.mark.parametrize("kw,status,needle", [
     (dict(dtype=4), 1, "dtype"), (dict(K=24, ld=24), 1, "K=24"), (dict(K=0), 1, "K=0"), (dict(K=131072, ld=131072), 2, "K=131072"), (dict(ld=56), 1, "ld=56"),
     (dict(ld=68), 1, "ld=68"), (dict(dtype=2, ld=66), 1, "ld=66"), (dict(M=-1), 1, "M=-1"), (dict(rows=None), 1, "no rows are given"),
     (dict(x_rows=0), 1, "no rows"), (dict(x=at(0) + 4), 1, "x is not"), (dict(data=None), 1, "data is NULL"), (dict(scales=at(3) + 2), 1, "scales"),
-    (dict(data=at(0)), 1, "data overlaps x"), (dict(scales=at(2)), 1, "overlaps"),
+    (dict(data=at(0)), 1, "data overlaps x"), (dict(ws=at(4) + 8), 1, "workspace is not"), (dict(ws=at(0)), 1, "workspace overlaps x"), (dict(scales=at(2)), 1, "overlaps"),
 ])
 def test_quantize_int8_refuses(L, kw, status, needle):
     refuses(L, "bn_quantize_int8", status, needle, *dict(INT8, **kw).values())

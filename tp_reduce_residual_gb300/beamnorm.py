@@ -43,7 +43,8 @@ EXPORTS = (
     "bn_quantize_fp4_workspace_bytes",
     "bn_dequantize_fp4", "bn_expert_product",
     "bn_expert_linear_workspace_bytes", "bn_expert_linear", "bn_expert_linear_dx",
-    "bn_expert_linear_dw", "bn_swiglu", "bn_swiglu_backward", "bn_quantize_int8", "bn_dequantize_int8",
+    "bn_expert_linear_dw", "bn_swiglu", "bn_swiglu_backward", "bn_quantize_int8", "bn_quantize_int8_workspace_bytes",
+    "bn_dequantize_int8",
     "bn_expert_product_int8_workspace_bytes", "bn_expert_product_int8",
 )
 
@@ -149,7 +150,8 @@ def load() -> ctypes.CDLL:
                                     _P],
             "bn_swiglu": [_P, _I, _L, _I, _I, _P, _P],
             "bn_swiglu_backward": [_P, _I, _L, _I, _I, _P, _L, _P, _P],
-            "bn_quantize_int8": [_P, _I, _L, _I, _P, _I, _I, _P, _P, _P],
+            "bn_quantize_int8": [_P, _I, _L, _I, _P, _I, _I, _P, _P, _P, ctypes.c_size_t, _P],
+            "bn_quantize_int8_workspace_bytes": [_I, _I, _I],
             "bn_dequantize_int8": [_P, _P, _I, _I, _P, _I, _P],
             "bn_expert_product_int8_workspace_bytes": [_I, _I, _I, _I],
             "bn_expert_product_int8": [_P, _P, _I, _P, _P, _I, _I, _I, _P, _F, _P, _P, ctypes.c_size_t, _P],
@@ -163,6 +165,7 @@ def load() -> ctypes.CDLL:
         L.bn_finalize_workspace_bytes.restype = ctypes.c_size_t
         L.bn_fp4_scale_bytes.restype = ctypes.c_size_t
         L.bn_quantize_fp4_workspace_bytes.restype = ctypes.c_size_t
+        L.bn_quantize_int8_workspace_bytes.restype = ctypes.c_size_t
         L.bn_expert_linear_workspace_bytes.restype = ctypes.c_size_t
         L.bn_expert_product_int8_workspace_bytes.restype = ctypes.c_size_t
         L.bn_last_error.restype = ctypes.c_char_p

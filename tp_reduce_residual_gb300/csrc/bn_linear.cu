@@ -17,10 +17,10 @@
 // either, as a bit of its descriptor.
 // Persistent CTAs walk the output tiles; stages of 64 values of the sum are filled by
 // TMA (128-byte swizzle), one thread issues the products, the output warps take an
-// accumulator out while the next one is filled.  Rows given by index are fetched four
-// at a time by their indexes, so x is never copied.  A group's last rows in the weight
-// gradient come the same way: an index outside x reads zeros, where a box would
-// bring in the next group's rows.
+// accumulator out while the next one is filled.  A few rows given by index are fetched four
+// at a time by their indexes; more go to their places in a workspace first.  A group's
+// last rows in the weight gradient come by index too: one outside x reads zeros, where a
+// box would bring in the next group's rows.
 //
 // Shapes, as in bn_product.cu: one CTA with tiles of 128 x 128, or a pair of CTAs
 // (cta_group::2) with tiles of 256 x 256 of which each loads half of either operand.  Tall
@@ -807,9 +807,10 @@ cudaError_t launch_mode(LinearArgs p, const LinearMaps &maps, int sms, bool pdl,
     return shape == kPair ? launch_shape<MODE, kPair, false>(p, maps, sms, pdl, st) : launch_shape<MODE, kOne, false>(p, maps, sms, pdl, st);
 }
 
-// Rows of x at their places, densely.  A warp a row at a time.
+// Rows of x at their places, densely, and their scales if there are any.  A warp a row
+// at a time.
 __global__ void __launch_bounds__(256) place_rows_kernel(const uint4 *x, long long ld, int x_rows, const int32_t *rows, int M,
-                                                         int vectors, uint4 *out, unsigned *err)
+                                                         int vectors, uint4 *out, const float *scales, float *out_scales, unsigned *err)
 {
     griddep_launch_dependents();
     griddep_wait();
@@ -820,6 +821,7 @@ __global__ void __launch_bounds__(256) place_rows_kernel(const uint4 *x, long lo
             if (lane == 0) atomicOr(err, BN_DEVERR_PERM_RANGE);
             r = 0;
         }
+        if (scales && lane == 0) out_scales[m] = __ldg(scales + r);
         const uint4 *from = x + (long long)r * ld;
         uint4 *to = out + m * vectors;
         int i = lane;
@@ -836,12 +838,12 @@ __global__ void __launch_bounds__(256) place_rows_kernel(const uint4 *x, long lo
 
 }  // namespace
 
-cudaError_t launch_place_rows(const void *x, long long ld, int x_rows, const int32_t *rows, int M, int K, void *out, unsigned *err,
-                              int sms, bool pdl, cudaStream_t st)
+cudaError_t launch_place_rows(const void *x, long long ld, int x_rows, const int32_t *rows, int M, int K, void *out, const float *scales,
+                              float *out_scales, unsigned *err, int sms, bool pdl, cudaStream_t st)
 {
     const long long blocks = ((long long)M + 7) / 8, most = 8LL * sms;
     return launch_kernel(place_rows_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, pdl, 1, st,
-                         static_cast<const uint4 *>(x), ld / 8, x_rows, rows, M, K / 8, static_cast<uint4 *>(out), err);
+                         static_cast<const uint4 *>(x), ld / 8, x_rows, rows, M, K / 8, static_cast<uint4 *>(out), scales, out_scales, err);
 }
 
 cudaError_t launch_linear(const LinearArgs &p, LinearMode mode, const void *x, long long ld, const void *w, long long w_ld, int sms,

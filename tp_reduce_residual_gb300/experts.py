@@ -483,10 +483,20 @@ def swiglu_backward(x, dy, dx=None, stream=None) -> torch.Tensor:
     return dx
 
 
-def quantize_int8(x, rows=None, offsets=None, data=None, scales=None, stream=None) -> Int8:
+@functools.lru_cache(maxsize=256)
+def quantize_int8_workspace_bytes(n: int, M: int, K: int) -> int:
+    """Workspace bytes with which ``quantize_int8`` quantises n rows once for M places, or
+    0 where that does not pay."""
+    return (_bn._lib or _bn.load()).bn_quantize_int8_workspace_bytes(n, M, K)
+
+
+def quantize_int8(x, rows=None, offsets=None, data=None, scales=None, workspace=None, stream=None) -> Int8:
     """Rows of ``x`` ([n,K], or [groups,n,K] such as weights, whose rows are the output
     channels; BF16, FP16 or FP32) in 8-bit integers with a scale a row.  ``rows`` (int32
-    [M]) picks the rows; ``offsets`` are kept with the result."""
+    [M]) picks the rows; ``offsets`` are kept with the result.  Where many places take
+    the same row, rows are quantised once into a ``workspace`` (a 1-D uint8 tensor of
+    ``quantize_int8_workspace_bytes``; by default one is allocated for the call) and copied
+    from there: the same result."""
     if not isinstance(x, torch.Tensor):
         raise TypeError("x must be a torch.Tensor")
     lead = None
@@ -509,7 +519,9 @@ def quantize_int8(x, rows=None, offsets=None, data=None, scales=None, stream=Non
     shape = lead if lead is not None else (M,)
     data, dp = _out(data, "data", torch.int8, (*shape, K), dev, stream)
     scales, sp = _out(scales, "scales", _FLOAT32, tuple(shape), dev, stream)
-    _call("bn_quantize_int8", (x.data_ptr(), dtype, ld, n, rp, M, K, dp, sp), dev.index, stream)
+    need = quantize_int8_workspace_bytes(n, M, K) if workspace is None and rp is not None else 0
+    wp, wn, workspace = _call_workspace(workspace, need, dev, stream)
+    _call("bn_quantize_int8", (x.data_ptr(), dtype, ld, n, rp, M, K, dp, sp, wp, wn), dev.index, stream)
     return Int8(data, scales, offsets)
 
 
