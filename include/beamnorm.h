@@ -469,8 +469,11 @@ BN_API bn_status bn_expert_linear_dx(const void *dy, bn_dtype dtype, long long l
                                      void *dx, void *stream);
 
 /* dw of bn_expert_linear, in `dtype` or BN_FP32 (dw_dtype).  With accumulate != 0
- * (BN_FP32 only) the sums are added to what dw holds, and dw of an empty group stays.
- * Every sum has one order: equal calls give equal bits.
+ * (BN_FP32 only) the sums are added to what dw holds (values below 2^-126 may count as
+ * 0 there), and dw of an empty group stays.  The tensor core drops what its FP32 sums
+ * cannot hold, at most 2^-23 of the sum for 16 rows; so they run over 256 rows (BN_FP32)
+ * or 4096, and those sums are added with rounding.  Every sum has one order: equal calls
+ * give equal bits.  dw is 16-byte aligned.
  * Source: none -- it has no counterpart on the pages. */
 BN_API bn_status bn_expert_linear_dw(const void *dy, bn_dtype dtype, long long ld_dy, int M,
                                      const void *x, long long ld, int x_rows, const int32_t *rows,

@@ -194,11 +194,13 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
         fence_mbarrier_init();
     }
     if (warp == 2) tmem_alloc<PAIR>(smem_addr(&tmem_slot), S::kColumns);
+    __syncwarp();
+    if constexpr (PAIR || SPLIT) cluster_arrive();  // this CTA's barriers are ready
     griddep_wait();
     group_tiles<kRows>(p.offsets, p.M, p.E, S::kThreads, start, cum, p.err);
     fence_before();
     __syncthreads();
-    if constexpr (PAIR || SPLIT) cluster_sync_all();  // the cluster's barriers are ready
+    if constexpr (PAIR || SPLIT) cluster_wait();  // and the other CTAs'
     fence_after();
     const uint32_t tmem = tmem_slot;
 
@@ -487,20 +489,18 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 const uint32_t mine = smem_addr(parts) + 4u * (uint32_t)(quad * 32 + lane) + part * (uint32_t)share * 512u;
                 int owner = 0, at = 0;  // the CTA that takes a row, and the row's place there
                 uint32_t to = mapa(mine, 0), bar = mapa(joined, 0);
+#pragma unroll 1
+                for (int b = 0; 16 * b < t.rows; ++b) {
+                    uint32_t v[16];
+                    read16(acc + 16 * b, v);
 #pragma unroll
-                for (int b = 0; b < kRows / 16; ++b) {
-                    if (16 * b < t.rows) {
-                        uint32_t v[16];
-                        read16(acc + 16 * b, v);
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            if (16 * b + i < t.rows) send_cluster(to + (uint32_t)at * 512u, v[i], bar);
-                            if (++at == share) {
-                                at = 0;
-                                owner = min(owner + 1, (int)parts_n - 1);
-                                to = mapa(mine, (uint32_t)owner);
-                                bar = mapa(joined, (uint32_t)owner);
-                            }
+                    for (int i = 0; i < 16; ++i) {
+                        if (16 * b + i < t.rows) send_cluster(to + (uint32_t)at * 512u, v[i], bar);
+                        if (++at == share) {
+                            at = 0;
+                            owner = min(owner + 1, (int)parts_n - 1);
+                            to = mapa(mine, (uint32_t)owner);
+                            bar = mapa(joined, (uint32_t)owner);
                         }
                     }
                 }

@@ -183,11 +183,13 @@ product8_kernel(const __grid_constant__ Maps8 maps, const __grid_constant__ Prod
         fence_mbarrier_init();
     }
     if (warp == 3) tmem_alloc<PAIR>(smem_addr(&tmem_slot), kTmemColumns);
+    __syncwarp();
+    if (PAIR || parts_n > 1) cluster_arrive();  // this CTA's barriers are ready
     griddep_wait();
     group_tiles<kRows>(p.offsets, p.M, p.E, S::kThreads, start, cum, p.err);
     fence_before();
     __syncthreads();
-    if (PAIR || parts_n > 1) cluster_sync_all();  // the cluster's barriers are ready
+    if (PAIR || parts_n > 1) cluster_wait();  // and the other CTAs'
     fence_after();
     const uint32_t tmem = tmem_slot;
 

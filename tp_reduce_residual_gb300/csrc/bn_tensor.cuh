@@ -29,25 +29,26 @@ __device__ __forceinline__ bool elect_one()
 }
 
 // The groups' first rows (start) and the row tiles of TILE rows before each group
-// (cum), E + 1 of either, in shared memory.  The caller synchronises its threads.
+// (cum), E + 1 of either, in shared memory.  The caller synchronises its threads.  The
+// first warp loads the offsets for itself, so that it waits for one load, not for a
+// barrier after it (which took 2400 cycles of a call with 256 experts).
 template <int TILE>
 __device__ __forceinline__ void group_tiles(const int32_t *offsets, int M, int E, int threads, int *start, int *cum, unsigned *err)
 {
-    for (int e = threadIdx.x; e <= E; e += threads) {
-        const int o = offsets ? __ldg(offsets + e) : e * M;
-        if (o < 0 || o > M) atomicOr(err, BN_DEVERR_OFFSETS);
-        start[e] = min(max(o, 0), M);
-    }
-    __syncthreads();
+    const auto offset = [&](int e) { return offsets ? __ldg(offsets + e) : e * M; };
+    const auto inside = [&](int o) { return min(max(o, 0), M); };
     if (threadIdx.x < 32) {  // a lane takes its share of consecutive groups
         const int lane = threadIdx.x;
         const int share = (E + 31) / 32, e0 = min(lane * share, E), e1 = min(e0 + share, E);
-        const auto tiles_of = [&](int e) { return (max(start[e + 1] - start[e], 0) + TILE - 1) / TILE; };
-        int n = 0;
+        int n = 0, from = inside(offset(e0));
         bool falls = false;  // a falling offset: an empty group
+#pragma unroll 8
         for (int e = e0; e < e1; ++e) {
-            n += tiles_of(e);
-            falls |= start[e + 1] < start[e];
+            const int to = inside(offset(e + 1));
+            cum[e] = n;
+            n += (max(to - from, 0) + TILE - 1) / TILE;
+            falls |= to < from;
+            from = to;
         }
         if (falls) atomicOr(err, BN_DEVERR_OFFSETS);
         int before = n;
@@ -56,14 +57,22 @@ __device__ __forceinline__ void group_tiles(const int32_t *offsets, int M, int E
             const int v = __shfl_up_sync(kAll, before, o);
             if (lane >= o) before += v;
         }
-        before -= n;
-        for (int e = e0; e < e1; ++e) {
-            cum[e] = before;
-            before += tiles_of(e);
-        }
         if (lane == 31) cum[E] = before;
+        before -= n;
+#pragma unroll 8
+        for (int e = e0; e < e1; ++e) cum[e] += before;
+    }
+    for (int e = threadIdx.x; e <= E; e += threads) {
+        const int o = offset(e);
+        if (o < 0 || o > M) atomicOr(err, BN_DEVERR_OFFSETS);
+        start[e] = inside(o);
     }
 }
+
+// The cluster's barrier in two halves: what its threads did before arriving is seen by all
+// that have waited.
+__device__ __forceinline__ void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+__device__ __forceinline__ void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 
 struct Tile {
     int e, f, row0, rows, stile;
