@@ -354,3 +354,12 @@ def test_many_experts():
     for gather in (False, True):
         check(make(sizes, 72, 40, "bf16", gather=gather, before=1, after=2), whole=True)
     check(make([0] * 1023 + [3], 128, 1024, "fp16", gather=True), whole=True)
+
+
+def test_no_row_in_any_group():
+    for gather in (False, True):
+        check(make([0, 0, 0], 64, 512, "bf16", before=3, after=300, gather=gather), whole=True)
+    d = make([0, 0], 64, 512, "bf16", after=7)
+    dw = torch.full((2, 64, 512), 3.0, device="cuda")
+    experts.expert_linear_dw(d["dy"], d["x"], d["offsets"], dw=dw, accumulate=True)
+    assert (dw == 3).all()

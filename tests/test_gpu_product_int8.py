@@ -185,3 +185,8 @@ def test_many_experts():
     sizes[5], sizes[1023] = 300, 40
     check(*make(sizes, 72, 48, before=1, after=2))
     check(*make([0] * 1023 + [3], 128, 2048))
+
+
+def test_no_row_in_any_group():
+    check(*make([0, 0, 0], 64, 512, before=3, after=300))
+    check(*make([0, 0, 0], 64, 512, after=9000))

@@ -201,3 +201,24 @@ def test_int8_repeated_rows_through_a_workspace(n, M, K):
     assert bn.check_device_error(raise_on_error=False) == bn.DEVERR_PERM_RANGE and (ws == 255).all()
     assert torch.equal(once.data, each.data) and torch.equal(once.scales.nan_to_num(-1), each.scales.nan_to_num(-1))
     assert experts.quantize_int8_workspace_bytes(100, 199, 65536) == 0 and experts.quantize_int8_workspace_bytes(100, 800, 1024) == 0
+
+
+def test_callers_streams():
+    """Outputs and workspaces come from the caller's stream's pool; two streams at once."""
+    x = torch.randn(600, 1024, generator=gen(1), device="cuda").bfloat16()
+    dy = torch.randn(600, 512, generator=gen(2), device="cuda").bfloat16()
+    rows = torch.arange(600, device="cuda").repeat(40).to(torch.int32)
+    assert experts.quantize_int8_workspace_bytes(600, 24000, 1024) > 0
+    want = experts.swiglu(x), experts.swiglu_backward(x, dy), experts.quantize_int8(x, rows=rows)
+    torch.cuda.synchronize()
+    streams = torch.cuda.Stream(), torch.cuda.Stream()
+    got = []
+    for _ in range(3):
+        for s in streams:
+            q = experts.quantize_int8(x, rows=rows, stream=s)
+            got.append((experts.swiglu(x, stream=s), experts.swiglu_backward(x, dy, stream=s.cuda_stream), q, experts.dequantize_int8(q, stream=s)))
+    for s in streams:
+        s.synchronize()
+    for y, dx, q, v in got:
+        assert torch.equal(y, want[0]) and torch.equal(dx, want[1]) and torch.equal(q.data, want[2].data) and torch.equal(q.scales, want[2].scales)
+        assert torch.equal(v, experts.dequantize_int8(want[2]))

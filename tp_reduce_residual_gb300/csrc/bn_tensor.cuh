@@ -344,7 +344,7 @@ EncodeFn g_encode;
 cudaError_t g_encode_status = cudaErrorUnknown;
 std::once_flag g_encode_once;
 
-// The driver's encoder of tensor maps, looked up once.
+// CUDA's encoder of tensor maps, looked up once.
 cudaError_t tensor_maps_ready()
 {
     std::call_once(g_encode_once, []() {
