@@ -201,7 +201,9 @@ __global__ void __launch_bounds__(256, H <= 5 ? 5 : 4) quantize_int8_kernel(cons
     else store(std::false_type{});
 }
 
-// A thread's codes are those of 16 bytes of values; W threads of a row.
+// A thread's codes are those of 16 bytes of values, so that every store is whole; W threads of
+// a row.  32768 rows of 5120 to BF16 77 us (75 at the copy rate; 16 codes a thread, whose two
+// stores are 32 bytes apart, 100).
 template <typename T, int W>
 __global__ void __launch_bounds__(256) dequantize_int8_kernel(const __grid_constant__ Int8Args a)
 {

@@ -808,7 +808,8 @@ cudaError_t launch_mode(LinearArgs p, const LinearMaps &maps, int sms, bool pdl,
 }
 
 // Rows of x at their places, densely, and their scales if there are any.  A warp a row
-// at a time.
+// at a time, four 16-byte loads a lane in flight; the writes bound it (32768 rows of 10 KB
+// from 4096 in 70 us, 4.8 TB/s written).
 __global__ void __launch_bounds__(256) place_rows_kernel(const uint4 *x, long long ld, int x_rows, const int32_t *rows, int M,
                                                          int vectors, uint4 *out, const float *scales, float *out_scales, unsigned *err)
 {

@@ -504,7 +504,8 @@ product8_kernel(const __grid_constant__ Maps8 maps, const __grid_constant__ Prod
     }
 }
 
-// Codes as FP16, 16 a thread.
+// Codes as FP16, 16 a thread: 16 bytes in and 32 out, which memory bounds (8192 rows of
+// 5120 from a cold cache in 26 us, 4.8 TB/s).
 __global__ void __launch_bounds__(256) widen_kernel(const uint4 *codes, long long n, uint4 *out)
 {
     griddep_launch_dependents();
