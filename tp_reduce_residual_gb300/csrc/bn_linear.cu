@@ -45,7 +45,7 @@ namespace bn {
 namespace {
 
 constexpr int kHalf = 128;      // features, and at most rows, that one CTA loads for a tile
-constexpr int kDepth = 64;      // summed values of a stage: 128 bytes
+constexpr int kDepth = kSumStage;  // summed values of a stage: 128 bytes
 constexpr int kBoxRows = 16;    // rows of the smaller box
 constexpr int kAtom = 64 * 128; // bytes of 64 features or rows by 64 values, where the sum runs across rows
 
@@ -224,7 +224,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
     const int run = p.out_fp32 ? 4 : 64;
     // the stages of it that this CTA sums
     const auto stages = [&](int d, int &k0, int &k1) {
-        const int nk = (d + kDepth - 1) / kDepth;
+        const int nk = sum_stages(d);
         k0 = SPLIT ? (int)(part * (uint32_t)nk / parts_n) : 0;
         k1 = SPLIT ? (int)((part + 1) * (uint32_t)nk / parts_n) : nk;
     };
@@ -473,7 +473,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
             }
         };
         // a tile's accumulators: its products, or the runs of a weight gradient's sum
-        const auto sums_of = [&]() { return kWeights ? max((depth() + kDepth * run - 1) / (kDepth * run), 1) : blocks_of(); };
+        const auto sums_of = [&]() { return kWeights ? sum_runs(depth(), run) : blocks_of(); };
         for (; tiles.next(t, lane); n += (uint32_t)sums_of()) {
             if (!taken(n)) break;
             const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), acc = lanes + (n & 1u) * kBlock;
@@ -782,7 +782,7 @@ int choose_shape(LinearArgs &p, int mode, int sms)
     };
     p.split = 1;
     if (mode == kWeightGrad) return rounds(256, 256, sms / 2) < rounds(128, 128, sms) ? kPair : kOne;
-    const long long nk = (p.D + kDepth - 1) / kDepth;
+    const long long nk = sum_stages(p.D);
     p.split = choose_split(most_tiles<kSplit>(p, mode), nk, 8, (most_tiles<kOne>(p, mode) + sms - 1) / sms * nk, sms);
     if (p.split > 1) return kSplit;
     const long long one = rounds(128, 128, sms), pair = rounds(256, 256, sms / 2);
