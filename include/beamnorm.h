@@ -444,7 +444,8 @@ BN_API size_t bn_expert_linear_workspace_bytes(int M, int K);
  *   dtype    BN_BF16 or BN_FP16: of every matrix (dw may be FP32)
  *   x        [x_rows, K], dy [M, N]: rows ld (ld_dy) elements apart, a multiple of 8
  *   rows     [M] int32 or NULL (then x_rows == M): the row of x at each place; values
- *            outside [0, x_rows) set BN_DEVERR_PERM_RANGE and read row 0
+ *            outside [0, x_rows) set BN_DEVERR_PERM_RANGE and read row 0.  At places
+ *            of no group they are not looked at
  *   w        [E, N, K] dense
  *   offsets  [E + 1] int32, or NULL when E == 1 (every row).  Offsets that fall or
  *            leave [0, M] set BN_DEVERR_OFFSETS; they are clamped

@@ -158,8 +158,9 @@ bool product8_pairs(const Product8Args &, int sms, int *split);
 // workspace: 2 M K bytes, for the rows widened to FP16 where pairs serve, or null: no pairs.
 cudaError_t launch_product8(Product8Args, const int8_t *w, void *workspace, int sms, bool pdl, cudaStream_t);
 // out [M, K] dense: row rows[m] of x at place m (16-bit values); likewise its scale, if scales are given.
-cudaError_t launch_place_rows(const void *x, long long ld, int x_rows, const int32_t *rows, int M, int K, void *out, const float *scales,
-                              float *out_scales, unsigned *err, int sms, bool pdl, cudaStream_t);
+// With the groups' offsets [E + 1], indexes outside x are errors at places of groups alone.
+cudaError_t launch_place_rows(const void *x, long long ld, int x_rows, const int32_t *rows, int M, const int32_t *offsets, int E, int K,
+                              void *out, const float *scales, float *out_scales, unsigned *err, int sms, bool pdl, cudaStream_t st);
 
 // A kernel's attributes, set once per device: dynamic shared memory of up to
 // `bytes`, and clusters of more than 8 CTAs if `wide`.

@@ -157,7 +157,8 @@ bn_status place_rows(LinearArgs &a, const void *&x, long long &ld, int K, void *
 {
     const size_t need = a.rows ? bn_expert_linear_workspace_bytes(a.M, K) : 0;
     if (need == 0 || !workspace || bytes < need) return BN_OK;
-    BN_TRY(launched(launch_place_rows(x, ld, a.x_rows, a.rows, a.M, K, workspace, nullptr, nullptr, d.err, d.sms, dependent_launch(), (cudaStream_t)stream),
+    BN_TRY(launched(launch_place_rows(x, ld, a.x_rows, a.rows, a.M, a.offsets, a.E, K, workspace, nullptr, nullptr, d.err, d.sms,
+                                      dependent_launch(), (cudaStream_t)stream),
                     "launching place_rows"));
     x = workspace;
     ld = K;
@@ -664,8 +665,8 @@ bn_status bn_quantize_int8(const void *x, bn_dtype dtype, long long ld, int x_ro
         a.data = static_cast<int8_t *>(workspace);
         a.scales = reinterpret_cast<float *>(a.data + (size_t)x_rows * K);
         BN_TRY(launched(launch_quantize_int8(a, dtype, dependent_launch(), (cudaStream_t)stream), "launching quantize_int8"));
-        return launched(launch_place_rows(a.data, K / 2, x_rows, rows, M, K / 2, data, a.scales, scales, d->err, d->sms, dependent_launch(),
-                                          (cudaStream_t)stream), "launching place_rows");
+        return launched(launch_place_rows(a.data, K / 2, x_rows, rows, M, nullptr, 0, K / 2, data, a.scales, scales, d->err, d->sms,
+                                          dependent_launch(), (cudaStream_t)stream), "launching place_rows");
     }
     return launched(launch_quantize_int8(a, dtype, dependent_launch(), (cudaStream_t)stream), "launching quantize_int8");
 }

@@ -387,7 +387,8 @@ def expert_linear(x, w, offsets=None, rows=None, out=None, workspace=None, strea
     FP16, any row stride that is a multiple of 8) times its group's weights of ``w``
     ([E,N,K]; [N,K] is one expert), summed in FP32.  ``offsets`` (int32 [E+1]) are the
     groups, ``rows`` (int32 [M]) the row of x at each place, as ``plan`` gives them;
-    without ``rows`` x is grouped already.  Rows of no group are zeros.  More than a few
+    without ``rows`` x is grouped already.  Rows of no group are zeros, whatever ``rows``
+    holds there.  More than a few
     rows by index go through a ``workspace`` (a 1-D uint8 tensor of
     ``linear_workspace_bytes``; by default one is allocated for the call).  One
     workspace serves one call at a time."""
