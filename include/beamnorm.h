@@ -440,7 +440,10 @@ BN_API size_t bn_expert_linear_workspace_bytes(int M, int K);
  *   bn_expert_linear     y[m, n]     = sum over k of x[rows[m], k] * w[e, n, k]
  *   bn_expert_linear_dx  dx[m, k]    = sum over n of dy[m, n] * w[e, n, k]
  *   bn_expert_linear_dw  dw[e, n, k] = sum over the group's m of dy[m, n] * x[rows[m], k]
- * summed in FP32 on the tensor core and rounded once.
+ * summed in FP32 on the tensor core and rounded once.  Its sums drop what they cannot
+ * hold, always towards zero: at most 2^-23 of a sum of one sign for 16 values.  So those
+ * of y and dx run over 16384 values at most (2^-13; half a step of FP16 is 2^-11), and
+ * these are added with rounding; dw has shorter ones, below.
  *   dtype    BN_BF16 or BN_FP16: of every matrix (dw may be FP32)
  *   x        [x_rows, K], dy [M, N]: rows ld (ld_dy) elements apart, a multiple of 8
  *   rows     [M] int32 or NULL (then x_rows == M): the row of x at each place; values
@@ -471,9 +474,8 @@ BN_API bn_status bn_expert_linear_dx(const void *dy, bn_dtype dtype, long long l
 
 /* dw of bn_expert_linear, in `dtype` or BN_FP32 (dw_dtype).  With accumulate != 0
  * (BN_FP32 only) the sums are added to what dw holds (values below 2^-126 may count as
- * 0 there), and dw of an empty group stays.  The tensor core drops what its FP32 sums
- * cannot hold, at most 2^-23 of the sum for 16 rows; so they run over 256 rows (BN_FP32)
- * or 4096, and those sums are added with rounding.  Every sum has one order: equal calls
+ * 0 there), and dw of an empty group stays.  The tensor core's sums run over 256 rows
+ * (BN_FP32) or 4096 and are added with rounding.  Every sum has one order: equal calls
  * give equal bits.  dw is 16-byte aligned.
  * Source: none -- it has no counterpart on the pages. */
 BN_API bn_status bn_expert_linear_dw(const void *dy, bn_dtype dtype, long long ld_dy, int M,

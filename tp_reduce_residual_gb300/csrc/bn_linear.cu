@@ -35,6 +35,8 @@
 // 256 experts of 6144 x 512 179 us (6.7 TB/s), one token with 10 of 512 x 8192 19 us (4.4).
 // dw of 4096 tokens with 8 of 64, 5120 x 2048 (1.34 GB) 470 us, 340 without its way out, 600
 // by transposed pieces of 16 bytes; added to 2.7 GB in FP32 1090 (800 at the copy rate).
+// Sums of more than 16384 values, in runs: 4096 rows of 131072 values by 4096 features 2.8 ms (2.5
+// whole, by tall pairs), 4096 x 32768 x 8192 1.32 either way.
 #include "../../include/beamnorm.h"
 #include "bn_device.cuh"
 #include "bn_experts.h"
@@ -46,6 +48,7 @@ namespace {
 
 constexpr int kHalf = 128;      // features, and at most rows, that one CTA loads for a tile
 constexpr int kDepth = kSumStage;  // summed values of a stage: 128 bytes
+constexpr int kLongStages = 256;   // stages of y and dx that the tensor core sums at a time: 16384 values
 constexpr int kBoxRows = 16;    // rows of the smaller box
 constexpr int kAtom = 64 * 128; // bytes of 64 features or rows by 64 values, where the sum runs across rows
 
@@ -141,14 +144,16 @@ __device__ __forceinline__ uint32_t round16(float a, float b, bool fp16)
     return *reinterpret_cast<const uint32_t *>(&h);
 }
 
-template <int MODE, int SHAPE, bool GATHER>
+// LONG: y or dx whose sums are cut into runs.
+template <int MODE, int SHAPE, bool GATHER, bool LONG>
 __global__ void __launch_bounds__(LinearShape<SHAPE>::kThreads, 1)
 linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ LinearArgs p)
 {
     using S = LinearShape<SHAPE, MODE == kWeightGrad>;
     constexpr bool PAIR = S::kPairs, SPLIT = SHAPE == kSplit;
     constexpr int kStages = S::kStages, kTile = S::kTile, kRows = S::kRows, kBlock = S::kBlock, kBlocks = S::kBlocks;
-    constexpr bool kWeights = MODE == kWeightGrad;
+    constexpr bool kWeights = MODE == kWeightGrad, kRuns = kWeights || LONG;
+    static_assert(!LONG || (!kWeights && kBlocks == 1), "runs take both accumulators in turn");
     constexpr bool kAcrossP = MODE != kForward, kAcrossQ = kWeights;
     extern __shared__ __align__(1024) uint8_t raw[];
     const uint32_t base = (smem_addr(raw) + 1023u) & ~1023u;
@@ -219,9 +224,10 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
     // the length of a tile's sum
     const auto depth = [&]() { return kWeights ? max(start[t.e + 1] - start[t.e], 0) : p.D; };
     // The tensor core drops what its FP32 sums cannot hold, always towards zero: 1e-9 of the
-    // sum a value (2e-6 over 1024 rows of one sign).  A weight gradient in FP32 is summed so over
-    // 4 stages, one in 16 bits over 64, and those sums are added with rounding.
-    const int run = p.out_fp32 ? 4 : 64;
+    // sum a value (2e-6 over 1024 rows of one sign, 1e-3 over 2^20).  A weight gradient in FP32 is summed so over
+    // 4 stages, one in 16 bits over 64, y and dx over kLongStages, and those sums are added with
+    // rounding.
+    const int run = LONG ? kLongStages : p.out_fp32 ? 4 : 64;
     // the stages of it that this CTA sums
     const auto stages = [&](int d, int &k0, int &k1) {
         const int nk = sum_stages(d);
@@ -401,8 +407,8 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 stages(d, k0, k1);
                 for (int k = k0; k < k1; ++k, ++it) {
                     const uint32_t s = it % kStages;
-                    const bool first = kWeights ? k % run == 0 : k == k0;
-                    if (kWeights && first && k > 0) {  // on to the other accumulator
+                    const bool first = kRuns ? (k - k0) % run == 0 : k == k0;
+                    if (kRuns && first && k > k0) {  // on to the other accumulator
                         ++n;
                         ok = accumulator(0);
                         if (!ok) break;
@@ -437,7 +443,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                                     product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, !first || j > 0);
                             }
                             if (b == blocks - 1) commit<PAIR>(empty + 8 * s);
-                            if (k == k1 - 1 || (kWeights && (k + 1) % run == 0)) commit<PAIR>(acc_full + 8 * ((n + b) & 1u));
+                            if (k == k1 - 1 || (kRuns && (k - k0 + 1) % run == 0)) commit<PAIR>(acc_full + 8 * ((n + b) & 1u));
                         }
                     }
                     if (!ok) break;
@@ -472,8 +478,36 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 else mbar_arrive(acc_empty + 8 * (i & 1u));
             }
         };
-        // a tile's accumulators: its products, or the runs of a weight gradient's sum
-        const auto sums_of = [&]() { return kWeights ? sum_runs(depth(), run) : blocks_of(); };
+        // a tile's accumulators: its products, or the runs of a sum
+        int long_runs = 1;
+        if (LONG) {
+            int k0, k1;
+            stages(p.D, k0, k1);
+            long_runs = (k1 - k0 + run - 1) / run;
+        }
+        const auto sums_of = [&]() { return kWeights ? sum_runs(depth(), run) : LONG ? long_runs : blocks_of(); };
+        // the runs of a long sum from column lo to hi, added
+        const auto add_runs = [&](int lo, int hi, auto &sums) {
+            constexpr int kColumns = sizeof(sums) / sizeof(float);
+#pragma unroll
+            for (int i = 0; i < kColumns; ++i) sums[i] = 0.0f;
+            for (int u = 0; u < long_runs; ++u) {
+                if (u > 0 && !taken(n + u)) return false;
+                const uint32_t from = tmem + ((uint32_t)(quad * 32) << 16) + ((n + u) & 1u) * kBlock + lo;
+#pragma unroll
+                for (int b = 0; b < kColumns / 16; ++b) {
+                    if (lo + 16 * b < hi) {
+                        uint32_t v[16];
+                        read16(from + 16 * b, v);
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) sums[16 * b + i] += __uint_as_float(v[i]);
+                    }
+                }
+                release(n + u);
+            }
+            return true;
+        };
+        uint32_t tile = 0;  // tiles of long sums taken
         for (; tiles.next(t, lane); n += (uint32_t)sums_of()) {
             if (!taken(n)) break;
             const uint32_t lanes = tmem + ((uint32_t)(quad * 32) << 16), acc = lanes + (n & 1u) * kBlock;
@@ -483,16 +517,16 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 // Every CTA of the cluster finishes its share of the rows: the parts of a row
                 // come to it from all of them and are added in the order of the sum.
                 const int share = (columns_of(0) + (int)parts_n - 1) / (int)parts_n;
-                if (!__all_sync(kAll, wait_phase<true, kPipe>(joinable, (n & 1u) ^ 1u, ctl))) break;
+                const uint32_t turn = LONG ? tile++ : n;
+                float sums[LONG ? kBlock : 16];
+                if (LONG && !add_runs(0, t.rows, sums)) break;
+                if (!__all_sync(kAll, wait_phase<true, kPipe>(joinable, (turn & 1u) ^ 1u, ctl))) break;
                 const int r0 = (int)part * share, r1 = min(r0 + share, t.rows);
                 if (quad == 0 && lane == 0) mbar_arrive_expect_tx(joined, parts_n * (uint32_t)max(r1 - r0, 0) * 512u);
                 const uint32_t mine = smem_addr(parts) + 4u * (uint32_t)(quad * 32 + lane) + part * (uint32_t)share * 512u;
                 int owner = 0, at = 0;  // the CTA that takes a row, and the row's place there
                 uint32_t to = mapa(mine, 0), bar = mapa(joined, 0);
-#pragma unroll 1
-                for (int b = 0; 16 * b < t.rows; ++b) {
-                    uint32_t v[16];
-                    read16(acc + 16 * b, v);
+                const auto send16 = [&](int b, const uint32_t *v) {
 #pragma unroll
                     for (int i = 0; i < 16; ++i) {
                         if (16 * b + i < t.rows) send_cluster(to + (uint32_t)at * 512u, v[i], bar);
@@ -503,9 +537,21 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                             bar = mapa(joined, (uint32_t)owner);
                         }
                     }
+                };
+                if constexpr (LONG) {
+#pragma unroll
+                    for (int b = 0; b < kBlock / 16; ++b)
+                        if (16 * b < t.rows) send16(b, reinterpret_cast<const uint32_t *>(sums) + 16 * b);
+                } else {
+#pragma unroll 1
+                    for (int b = 0; 16 * b < t.rows; ++b) {
+                        uint32_t v[16];
+                        read16(acc + 16 * b, v);
+                        send16(b, v);
+                    }
+                    release(n);
                 }
-                release(n);
-                if (!__all_sync(kAll, wait_phase<true, kPipe>(joined, n & 1u, ctl))) break;
+                if (!__all_sync(kAll, wait_phase<true, kPipe>(joined, turn & 1u, ctl))) break;
                 uint16_t *out = static_cast<uint16_t *>(p.out) + (row0 + r0) * p.F + f0 + lane;
                 const float *from = parts + quad * 32 + lane;
                 for (int r = r0; r < r1; ++r, out += p.F, from += 128) {
@@ -626,8 +672,18 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 };
                 uint32_t packed[kBlocks][8][8];
                 bool ok = true;
+                if constexpr (LONG) {
+                    float sums[128];
+                    int lo, hi;
+                    range(0, lo, hi);
+                    ok = add_runs(lo, hi, sums);
 #pragma unroll
-                for (int q = 0; q < kBlocks; ++q) {
+                    for (int b = 0; b < 8; ++b)
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) packed[0][b][i] = round16(sums[16 * b + 2 * i], sums[16 * b + 2 * i + 1], fp16);
+                }
+#pragma unroll
+                for (int q = 0; q < (LONG ? 0 : kBlocks); ++q) {
                     if (q > 0 && q >= blocks_of()) break;
                     if (q > 0 && !taken(n + q)) {
                         ok = false;
@@ -743,12 +799,12 @@ long long most_tiles(const LinearArgs &p, int mode)
     return rows * ((p.F + S::kTile - 1) / S::kTile);
 }
 
-template <int MODE, int SHAPE, bool GATHER>
+template <int MODE, int SHAPE, bool GATHER, bool LONG = false>
 cudaError_t launch_shape(const LinearArgs &p, const LinearMaps &maps, int sms, bool pdl, cudaStream_t st)
 {
     using S = LinearShape<SHAPE, MODE == kWeightGrad>;
     static KernelSetup setup;
-    auto *k = linear_kernel<MODE, SHAPE, GATHER>;
+    auto *k = linear_kernel<MODE, SHAPE, GATHER, LONG>;
     const cudaError_t e = setup(k, (int)S::smem(kMaxExperts));
     if (e != cudaSuccess) return e;
     const int ctas = SHAPE == kSplit ? p.split : S::kCtas;
@@ -790,21 +846,32 @@ int choose_shape(LinearArgs &p, int mode, int sms)
     return 2 * rounds(512, 256, sms / 2) <= pair ? kTall : kPair;
 }
 
+// y and dx: a CTA's sum of more than kLongStages stages is cut into runs.  (Runs leave no
+// accumulator for a second product: tall pairs' long sums go to pairs.)
+template <int MODE, bool LONG>
+cudaError_t launch_sums(const LinearArgs &p, int shape, const LinearMaps &maps, int sms, bool pdl, cudaStream_t st)
+{
+    if constexpr (MODE == kForward) {
+        if (p.rows && shape == kSplit) return launch_shape<MODE, kSplit, true, LONG>(p, maps, sms, pdl, st);
+        if (p.rows) return launch_shape<MODE, kOne, true, LONG>(p, maps, sms, pdl, st);
+    }
+    if (shape == kSplit) return launch_shape<MODE, kSplit, false, LONG>(p, maps, sms, pdl, st);
+    if (shape == kOne) return launch_shape<MODE, kOne, false, LONG>(p, maps, sms, pdl, st);
+    if (shape == kPair || LONG) return launch_shape<MODE, kPair, false, LONG>(p, maps, sms, pdl, st);
+    return launch_shape<MODE, LONG ? kPair : kTall, false, LONG>(p, maps, sms, pdl, st);
+}
+
 template <int MODE>
 cudaError_t launch_mode(LinearArgs p, const LinearMaps &maps, int sms, bool pdl, cudaStream_t st)
 {
     const int shape = choose_shape(p, MODE, sms);
-    if constexpr (MODE == kForward) {
-        if (p.rows && shape == kSplit) return launch_shape<MODE, kSplit, true>(p, maps, sms, pdl, st);
-    }
-    if constexpr (MODE != kInputGrad) {
+    if constexpr (MODE == kWeightGrad) {
         if (p.rows) return launch_shape<MODE, kOne, true>(p, maps, sms, pdl, st);
+        return shape == kPair ? launch_shape<MODE, kPair, false>(p, maps, sms, pdl, st) : launch_shape<MODE, kOne, false>(p, maps, sms, pdl, st);
+    } else {
+        return (sum_stages(p.D) + p.split - 1) / p.split > kLongStages ? launch_sums<MODE, true>(p, shape, maps, sms, pdl, st)
+                                                                      : launch_sums<MODE, false>(p, shape, maps, sms, pdl, st);
     }
-    if constexpr (MODE != kWeightGrad) {
-        if (shape == kSplit) return launch_shape<MODE, kSplit, false>(p, maps, sms, pdl, st);
-        if (shape == kTall) return launch_shape<MODE, kTall, false>(p, maps, sms, pdl, st);
-    }
-    return shape == kPair ? launch_shape<MODE, kPair, false>(p, maps, sms, pdl, st) : launch_shape<MODE, kOne, false>(p, maps, sms, pdl, st);
 }
 
 // Whether a place is in a group; without offsets every place is.  Asked by a whole warp.
