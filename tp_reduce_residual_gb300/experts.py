@@ -303,7 +303,7 @@ def dequantize_fp4(q: FP4, dtype=torch.bfloat16, out=None, stream=None) -> torch
     return out
 
 
-def expert_product(a, w, scale: float = 1.0, out=None, workspace=None, stream=None) -> torch.Tensor:
+def expert_product(a, w, scale: float = 1.0, out=None, stream=None, workspace=None) -> torch.Tensor:
     """out [M,N] BF16: each row of ``a`` ([M,K], grouped by ``a.offsets``) times
     its group's weights of ``w`` ([E,N,K]; [N,K] is one expert), times ``scale``
     and the operands' scales.  Both are FP4 or both Int8, whose sums are exact.  Rows
