@@ -465,8 +465,10 @@ BN_API bn_status bn_expert_linear(const void *x, bn_dtype dtype, long long ld, i
                                   const int32_t *offsets, void *y, void *workspace,
                                   size_t workspace_bytes, void *stream);
 
-/* dx of bn_expert_linear, a row for every place (of rows that several places take, the
- * gradients are the sum: bn_finalize_only with weights of 1 adds them up).
+/* dx of bn_expert_linear, a row for every place.  Of rows that several places take the
+ * gradient is the sum over these: bn_finalize_reduce_only with the plan's perm and weights
+ * of 1 gives it in FP32, each shard's sum rounded to BF16 once.  It takes BF16 rows, as
+ * every finalize does: rows in FP16, dx or y, are for the caller to add up.
  * Source: none -- it has no counterpart on the pages. */
 BN_API bn_status bn_expert_linear_dx(const void *dy, bn_dtype dtype, long long ld_dy, int M,
                                      const void *w, int E, int N, int K, const int32_t *offsets,

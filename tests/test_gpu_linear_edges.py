@@ -63,3 +63,22 @@ def test_offsets_that_fall_reach_the_same_rows_by_any_way(offsets):
             assert torch.equal(dw[e], (d["dy"][s].double().T @ x).bfloat16())
             if o[e] >= o[0] and o[e + 1] <= o[3]:  # not among the rows that are cleared before and after
                 assert torch.equal(y[s], (x @ d["w"][e].double().T).bfloat16())
+
+
+def test_gradient_of_rows_taken_several_times():
+    """Small whole numbers: dx is exact, and so is a sum over three places (below 256, BF16's whole numbers)."""
+    g = torch.Generator(device="cuda").manual_seed(4)
+    T, E, k, N, K = 50, 8, 3, 24, 264
+    ids = torch.rand(T, E, generator=g, device="cuda").topk(k).indices.int()
+    plan = experts.plan(ids, E)
+    w = torch.randint(-1, 2, (E, N, K), generator=g, device="cuda").bfloat16()
+    dy = torch.randint(-1, 2, (T * k, N), generator=g, device="cuda").bfloat16()
+    dx = experts.expert_linear_dx(dy, w, plan.offsets)
+    got = bn.finalize_reduce_only(dx[None], plan.perm, torch.ones(1, T, k, device="cuda"), None)
+    expert = torch.arange(E, device="cuda").repeat_interleave(plan.offsets.diff().long())
+    rows = torch.einsum("mn,mnk->mk", dy.double(), w[expert].double())
+    want = torch.zeros(T, K, dtype=torch.float64, device="cuda").index_add_(0, plan.rows.long(), rows)
+    assert got.dtype is torch.float32 and torch.equal(got.double(), want)
+    for fn in (bn.finalize_reduce_only, bn.finalize_only):  # rows in FP16 are refused
+        with pytest.raises(TypeError, match="bfloat16"):
+            fn(dx[None].half(), plan.perm, torch.ones(1, T, k, device="cuda"), None)

@@ -409,7 +409,9 @@ def expert_linear(x, w, offsets=None, rows=None, out=None, workspace=None, strea
 def expert_linear_dx(dy, w, offsets=None, dx=None, stream=None) -> torch.Tensor:
     """Gradient of ``expert_linear`` with respect to the grouped rows: dx [M,K] from ``dy``
     [M,N].  Where ``rows`` took a row several times, its gradient is the sum over its
-    places: ``beamnorm.finalize_only`` with the plan's perm and weights of 1."""
+    places: ``beamnorm.finalize_reduce_only`` with the plan's perm and weights of 1 (FP32,
+    each shard's sum rounded to BF16 once).  It takes BF16 rows, as every finalize does:
+    rows in FP16, dx or the layer's output, are for the caller to add up."""
     ld = _stride(dy, "dy")
     dev = dy.device
     dtype = _dtype(dy, "dy", fp32=False)
