@@ -1,6 +1,7 @@
 """One mixture-of-experts layer from the normed hidden state to the next layer's input, on one GPU.
 
     python examples/moe_layer.py [--tokens T] [--experts E] [--topk K] [--hidden H] [--width F] [--shards R]
+                                 [--format nvfp4|mxfp4|int8|bf16] [--timed N]
 
 The router's logits choose each token's experts (``route``), the token slots are grouped by expert
 (``plan``), the grouped rows go through each shard's slice of the experts' two projections with the
@@ -153,6 +154,7 @@ def main(argv=None):
     for name, value in (("tokens", 64), ("experts", 16), ("topk", 4), ("hidden", 2048), ("width", 1024), ("shards", 2)):
         ap.add_argument(f"--{name}", type=int, default=value)
     ap.add_argument("--format", choices=FORMATS, default="nvfp4")
+    ap.add_argument("--timed", type=int, default=20, help="layers to time; 0: none")
     a = ap.parse_args(argv)
     layer = MoELayer(a.hidden, a.width, a.experts, a.topk, a.shards, a.format)
     g = torch.Generator(device="cuda").manual_seed(1)
@@ -167,14 +169,17 @@ def main(argv=None):
     else:
         dw = torch.randn(a.shards, a.tokens, a.topk, generator=g, device="cuda")
     dh = layer.router_step(h, dw)
-    begin, end = torch.cuda.Event(True), torch.cuda.Event(True)
-    begin.record()
-    for _ in range(20):
-        layer(h, residual)
-    end.record()
-    torch.cuda.synchronize()
-    print(f"{a.tokens} tokens, {a.experts} experts, top {a.topk}, {a.shards} shards, {a.format}: output off by {off:.3f} of "
-          f"32-bit activations, |dh| {float(dh.norm()):.3f}, {begin.elapsed_time(end) / 20 * 1e3:.0f} us a layer")
+    line = (f"{a.tokens} tokens, {a.experts} experts, top {a.topk}, {a.shards} shards, {a.format}: output off by {off:.3f} of "
+            f"32-bit activations, |dh| {float(dh.norm()):.3f}")
+    if a.timed > 0:
+        begin, end = torch.cuda.Event(True), torch.cuda.Event(True)
+        begin.record()
+        for _ in range(a.timed):
+            layer(h, residual)
+        end.record()
+        torch.cuda.synchronize()
+        line += f", {begin.elapsed_time(end) / a.timed * 1e3:.0f} us a layer"
+    print(line)
     return off
 
 
