@@ -96,12 +96,12 @@ struct LinearArgs {
 };
 enum LinearMode { kForward = 0, kInputGrad = 1, kWeightGrad = 2 };
 
-// A sum of d values is taken in stages of kSumStage, and those in runs of `run` stages, of
-// which a sum of no values has one.  Runs are counted from stages: d + 64 * run leaves 31 bits
+// A sum of d values is taken in stages of kSumStage, and those in runs of 2^log stages, of
+// which a sum of no values has one.  Runs are counted from stages: d + 64 * 2^log leaves 31 bits
 // at the longest sums, the rows of a call (2^31 - 1024).
 constexpr int kSumStage = 64;
 __host__ __device__ constexpr int sum_stages(int d) { return (d + kSumStage - 1) / kSumStage; }
-__host__ __device__ constexpr int sum_runs(int d, int run) { return d > 0 ? (sum_stages(d) + run - 1) / run : 1; }
+__host__ __device__ constexpr int sum_runs(int d, int log) { return d > 0 ? (sum_stages(d) + (1 << log) - 1) >> log : 1; }
 
 struct SwigluArgs {
     const void *x;         // [M, 2 F], ld elements between rows: gate and up

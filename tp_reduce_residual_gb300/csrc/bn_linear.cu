@@ -48,7 +48,7 @@ namespace {
 
 constexpr int kHalf = 128;      // features, and at most rows, that one CTA loads for a tile
 constexpr int kDepth = kSumStage;  // summed values of a stage: 128 bytes
-constexpr int kLongStages = 256;   // stages of y and dx that the tensor core sums at a time: 16384 values
+constexpr int kLongLog = 8;     // 2^8 stages of y and dx are summed at a time by the tensor core: 16384 values
 constexpr int kBoxRows = 16;    // rows of the smaller box
 constexpr int kAtom = 64 * 128; // bytes of 64 features or rows by 64 values, where the sum runs across rows
 
@@ -225,9 +225,9 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
     const auto depth = [&]() { return kWeights ? max(start[t.e + 1] - start[t.e], 0) : p.D; };
     // The tensor core drops what its FP32 sums cannot hold, always towards zero: 1e-9 of the
     // sum a value (2e-6 over 1024 rows of one sign, 1e-3 over 2^20).  A weight gradient in FP32 is summed so over
-    // 4 stages, one in 16 bits over 64, y and dx over kLongStages, and those sums are added with
+    // 4 stages, one in 16 bits over 64, y and dx over 2^kLongLog, and those sums are added with
     // rounding.
-    const int run = LONG ? kLongStages : p.out_fp32 ? 4 : 64;
+    const int run_log = LONG ? kLongLog : p.out_fp32 ? 2 : 6, run_mask = (1 << run_log) - 1;
     // the stages of it that this CTA sums
     const auto stages = [&](int d, int &k0, int &k1) {
         const int nk = sum_stages(d);
@@ -407,7 +407,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                 stages(d, k0, k1);
                 for (int k = k0; k < k1; ++k, ++it) {
                     const uint32_t s = it % kStages;
-                    const bool first = kRuns ? (k - k0) % run == 0 : k == k0;
+                    const bool first = kRuns ? ((k - k0) & run_mask) == 0 : k == k0;
                     if (kRuns && first && k > k0) {  // on to the other accumulator
                         ++n;
                         ok = accumulator(0);
@@ -443,7 +443,7 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
                                     product16<PAIR>(acc, dp + kP * j, dq + kQ * j, idesc, !first || j > 0);
                             }
                             if (b == blocks - 1) commit<PAIR>(empty + 8 * s);
-                            if (k == k1 - 1 || (kRuns && (k - k0 + 1) % run == 0)) commit<PAIR>(acc_full + 8 * ((n + b) & 1u));
+                            if (k == k1 - 1 || (kRuns && ((k - k0 + 1) & run_mask) == 0)) commit<PAIR>(acc_full + 8 * ((n + b) & 1u));
                         }
                     }
                     if (!ok) break;
@@ -483,9 +483,9 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
         if (LONG) {
             int k0, k1;
             stages(p.D, k0, k1);
-            long_runs = (k1 - k0 + run - 1) / run;
+            long_runs = (k1 - k0 + run_mask) >> run_log;
         }
-        const auto sums_of = [&]() { return kWeights ? sum_runs(depth(), run) : LONG ? long_runs : blocks_of(); };
+        const auto sums_of = [&]() { return kWeights ? sum_runs(depth(), run_log) : LONG ? long_runs : blocks_of(); };
         // the runs of a long sum from column lo to hi, added
         const auto add_runs = [&](int lo, int hi, auto &sums) {
             constexpr int kColumns = sizeof(sums) / sizeof(float);
@@ -846,7 +846,7 @@ int choose_shape(LinearArgs &p, int mode, int sms)
     return 2 * rounds(512, 256, sms / 2) <= pair ? kTall : kPair;
 }
 
-// y and dx: a CTA's sum of more than kLongStages stages is cut into runs.  (Runs leave no
+// y and dx: a CTA's sum of more than 2^kLongLog stages is cut into runs.  (Runs leave no
 // accumulator for a second product: tall pairs' long sums go to pairs.)
 template <int MODE, bool LONG>
 cudaError_t launch_sums(const LinearArgs &p, int shape, const LinearMaps &maps, int sms, bool pdl, cudaStream_t st)
@@ -869,7 +869,7 @@ cudaError_t launch_mode(LinearArgs p, const LinearMaps &maps, int sms, bool pdl,
         if (p.rows) return launch_shape<MODE, kOne, true>(p, maps, sms, pdl, st);
         return shape == kPair ? launch_shape<MODE, kPair, false>(p, maps, sms, pdl, st) : launch_shape<MODE, kOne, false>(p, maps, sms, pdl, st);
     } else {
-        return (sum_stages(p.D) + p.split - 1) / p.split > kLongStages ? launch_sums<MODE, true>(p, shape, maps, sms, pdl, st)
+        return (sum_stages(p.D) + p.split - 1) / p.split > 1 << kLongLog ? launch_sums<MODE, true>(p, shape, maps, sms, pdl, st)
                                                                       : launch_sums<MODE, false>(p, shape, maps, sms, pdl, st);
     }
 }
