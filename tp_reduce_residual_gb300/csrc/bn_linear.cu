@@ -874,18 +874,10 @@ cudaError_t launch_mode(LinearArgs p, const LinearMaps &maps, int sms, bool pdl,
     }
 }
 
-// Whether a place is in a group; without offsets every place is.  Asked by a whole warp.
-__device__ __forceinline__ bool in_a_group(const int32_t *offsets, int E, long long m)
-{
-    bool in = !offsets;
-    for (int e = threadIdx.x & 31; offsets && e < E; e += 32) in |= __ldg(offsets + e) <= m && m < __ldg(offsets + e + 1);
-    return __any_sync(kAll, in);
-}
-
 // Rows of x at their places, densely, and their scales if there are any.  A warp a row
 // at a time, four 16-byte loads a lane in flight; the writes bound it (32768 rows of 10 KB
 // from 4096 in 81 us of a call's, 4.1 TB/s written).  With the groups' offsets an index outside x is an
-// error at a place of a group alone; elsewhere the place stays as it is.
+// error between the first and the last alone; row 0 is placed for it anywhere.
 __global__ void __launch_bounds__(256) place_rows_kernel(const uint4 *x, long long ld, int x_rows, const int32_t *rows, int M,
                                                          const int32_t *offsets, int E, int vectors, uint4 *out, const float *scales,
                                                          float *out_scales, unsigned *err)
@@ -896,8 +888,8 @@ __global__ void __launch_bounds__(256) place_rows_kernel(const uint4 *x, long lo
     for (long long m = (long long)blockIdx.x * 8 + (threadIdx.x >> 5); m < M; m += warps) {
         int r = __ldg(rows + m);
         if ((unsigned)r >= (unsigned)x_rows) {
-            if (!in_a_group(offsets, E, m)) continue;
-            if (lane == 0) atomicOr(err, BN_DEVERR_PERM_RANGE);
+            const bool used = !offsets || (__ldg(offsets) <= m && m < __ldg(offsets + E));
+            if (used && lane == 0) atomicOr(err, BN_DEVERR_PERM_RANGE);
             r = 0;
         }
         if (scales && lane == 0) out_scales[m] = __ldg(scales + r);
