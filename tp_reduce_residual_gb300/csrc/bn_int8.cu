@@ -13,7 +13,7 @@
 // it is read once; what a longer row has beyond that is read again from L2.  Memory bounds
 // rows in their places: 32768 of 5120 in 88 us (75 at the copy rate), 32768 of 2048 in 37
 // (30).  Rows repeated from 4096 come from L2, in 80 us: about 7 instructions a value and
-// the wait for the row's largest; quantised once into a workspace and copied 49.  Between 64 and 128 bytes a thread: with 8 vectors held for
+// the wait for the row's largest; quantised once into a workspace and copied 42.  Between 64 and 128 bytes a thread: with 8 vectors held for
 // rows of 5 a thread 92 us, with a warp a row of 20 a thread 117.
 #include <type_traits>
 

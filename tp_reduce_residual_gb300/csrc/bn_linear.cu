@@ -28,13 +28,15 @@
 // to fill for 64, at no overlap of a tile's way out with the next.  Where tiles are too few
 // for the device, clusters of CTAs each sum a part.
 //
-// Measured.  What one SM takes in (60 bytes a cycle) bounds pairs: 4096 tokens with 8 of
-// 64 experts of 4096 x 5120 852 us (1.61 PFLOP/s), their tiles not full; one expert of 8192
-// x 8192 and as many rows 549 us by tall pairs (2.00 PFLOP/s).  Rows by index cost the
-// place in the workspace, 70 us of 1020.  Few rows: the stream of weights; 100 tokens with 8 of
-// 256 experts of 6144 x 512 179 us (6.7 TB/s), one token with 10 of 512 x 8192 19 us (4.4).
-// dw of 4096 tokens with 8 of 64, 5120 x 2048 (1.34 GB) 470 us, 340 without its way out, 600
-// by transposed pieces of 16 bytes; added to 2.7 GB in FP32 1090 (800 at the copy rate).
+// Measured, a call alone (back to back under the power cap).  What one SM takes in (60 bytes a
+// cycle) bounds pairs: 4096 tokens with 8 of 64 experts of 4096 x 5120 845 us (955; 1.63
+// PFLOP/s), their tiles not full; one expert of 8192 x 8192 and as many rows 554 us (625) by
+// tall pairs (1.99 PFLOP/s).  Rows by index cost their way to the workspace, 67 of 912 us (1001).
+// Few rows: the stream of weights; 100 tokens with 8 of 256 experts of 6144 x 512 171 us
+// (6.7 TB/s), one token with 10 of 512 x 8192 18.6 us (4.5).
+// dw of 4096 tokens with 8 of 64, 5120 x 2048 (1.34 GB) 486 us (529); before its way out in
+// whole lines 600 by transposed pieces of 16 bytes, 340 without any.  In FP32 (2.7 GB, sums of 512 rows
+// in runs) 666 us (690) for 472 at the copy rate, and added to what is there 1110 (1095) for 874.
 // Sums of more than 16384 values, in runs: 4096 rows of 131072 values by 4096 features 2.8 ms (2.5
 // whole, by tall pairs), 4096 x 32768 x 8192 1.32 either way.
 #include "../../include/beamnorm.h"
@@ -876,7 +878,7 @@ cudaError_t launch_mode(LinearArgs p, const LinearMaps &maps, int sms, bool pdl,
 
 // Rows of x at their places, densely, and their scales if there are any.  A warp a row
 // at a time, four 16-byte loads a lane in flight; the writes bound it (32768 rows of 10 KB
-// from 4096 in 81 us of a call's, 4.1 TB/s written).  With the groups' offsets an index outside x is an
+// from 4096 in 67 us alone, 5.0 TB/s written, 81 back to back).  With the groups' offsets an index outside x is an
 // error between the first and the last alone; row 0 is placed for it anywhere.
 __global__ void __launch_bounds__(256) place_rows_kernel(const uint4 *x, long long ld, int x_rows, const int32_t *rows, int M,
                                                          const int32_t *offsets, int E, int vectors, uint4 *out, const float *scales,
@@ -912,7 +914,7 @@ __global__ void __launch_bounds__(256) place_rows_kernel(const uint4 *x, long lo
 cudaError_t launch_place_rows(const void *x, long long ld, int x_rows, const int32_t *rows, int M, const int32_t *offsets, int E, int K,
                               void *out, const float *scales, float *out_scales, unsigned *err, int sms, bool pdl, cudaStream_t st)
 {
-    const long long blocks = ((long long)M + 7) / 8, most = 10LL * sms;  // 8: 83.5 us for 81
+    const long long blocks = ((long long)M + 7) / 8, most = 10LL * sms;  // 8 a SM: 83.5 us for 81
     return launch_kernel(place_rows_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, pdl, 1, st,
                          static_cast<const uint4 *>(x), ld / 8, x_rows, rows, M, offsets, E, K / 8, static_cast<uint4 *>(out), scales, out_scales,
                          err);

@@ -22,10 +22,10 @@
 // as every feature tile reads them again.
 //
 // Measured.  Few rows: the stream of weights; 100 tokens with 8 of 256 experts of 6144 x
-// 1024 (1.17 GB reached) 179 us, 6.5 TB/s; one token with 10 of 1024 x 8192 (84 MB) 24.5 us, of
+// 1024 (1.17 GB reached) 172 us, 6.8 TB/s; one token with 10 of 1024 x 8192 (84 MB) 22.6 us, of
 // which the first codes take 2.3 to arrive.  Rings: with one ring for codes and products 28
 // us, with the rows widened ahead 26; with 16 widening warps no faster.  Large groups: 4096
-// tokens with 8 of 64, 4096 x 5120: 950 us, 1.44 PFLOP/s; without the widening stores 11 % less
+// tokens with 8 of 64, 4096 x 5120: 922 us alone, 1.49 PFLOP/s, 964 back to back; without the widening stores 11 % less
 // time, with one product in eight 16 % less, with neither 20 %: the copies' 64 bytes a
 // cycle and SM (60 is what one takes in), which wider tiles would lower, but 256 sums a
 // lane pair do not fit the registers beside the widening warps.

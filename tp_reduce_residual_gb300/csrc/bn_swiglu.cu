@@ -11,7 +11,8 @@
 // takes 16 bytes of each operand at a time; rows whose length or alignment does not allow that
 // go value by value.  32768 rows of 2048: 74 us with 8 blocks an SM that stride (60 at the
 // copy rate; 78 with a block for every 256 vectors, 80 with two vectors in flight a thread),
-// the gradient 102 with a block for every 256 vectors (100; 117 striding).
+// the gradient 96 with a block for every 256 vectors (100 at the copy rate, but the last of its output
+// stays in L2; 117 striding).
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
