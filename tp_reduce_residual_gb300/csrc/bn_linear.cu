@@ -226,9 +226,9 @@ linear_kernel(const __grid_constant__ LinearMaps maps, const __grid_constant__ L
     // the length of a tile's sum
     const auto depth = [&]() { return kWeights ? max(start[t.e + 1] - start[t.e], 0) : p.D; };
     // The tensor core drops what its FP32 sums cannot hold, always towards zero: 1e-9 of the
-    // sum a value (2e-6 over 1024 rows of one sign, 1e-3 over 2^20).  A weight gradient in FP32 is summed so over
-    // 4 stages, one in 16 bits over 64, y and dx over 2^kLongLog, and those sums are added with
-    // rounding.
+    // sum a value (2e-6 over 1024 rows of one sign, 1e-3 over 2^20).  A weight gradient in FP32
+    // is summed so over 4 stages, one in 16 bits over 64, y and dx over 2^kLongLog, and those
+    // sums are added with rounding.
     const int run_log = LONG ? kLongLog : p.out_fp32 ? 2 : 6, run_mask = (1 << run_log) - 1;
     // the stages of it that this CTA sums
     const auto stages = [&](int d, int &k0, int &k1) {
@@ -878,8 +878,8 @@ cudaError_t launch_mode(LinearArgs p, const LinearMaps &maps, int sms, bool pdl,
 
 // Rows of x at their places, densely, and their scales if there are any.  A warp a row
 // at a time, four 16-byte loads a lane in flight; the writes bound it (32768 rows of 10 KB
-// from 4096 in 67 us alone, 5.0 TB/s written, 81 back to back).  With the groups' offsets an index outside x is an
-// error between the first and the last alone; row 0 is placed for it anywhere.
+// from 4096 in 67 us alone, 5.0 TB/s written, 82 back to back).  With the groups' offsets an index
+// outside x is an error between the first and the last alone; row 0 is placed for it anywhere.
 __global__ void __launch_bounds__(256) place_rows_kernel(const uint4 *x, long long ld, int x_rows, const int32_t *rows, int M,
                                                          const int32_t *offsets, int E, int vectors, uint4 *out, const float *scales,
                                                          float *out_scales, unsigned *err)
@@ -914,7 +914,7 @@ __global__ void __launch_bounds__(256) place_rows_kernel(const uint4 *x, long lo
 cudaError_t launch_place_rows(const void *x, long long ld, int x_rows, const int32_t *rows, int M, const int32_t *offsets, int E, int K,
                               void *out, const float *scales, float *out_scales, unsigned *err, int sms, bool pdl, cudaStream_t st)
 {
-    const long long blocks = ((long long)M + 7) / 8, most = 10LL * sms;  // 8 a SM: 83.5 us for 81
+    const long long blocks = ((long long)M + 7) / 8, most = 8LL * sms;
     return launch_kernel(place_rows_kernel, dim3((unsigned)(blocks < most ? blocks : most)), dim3(256), 0, pdl, 1, st,
                          static_cast<const uint4 *>(x), ld / 8, x_rows, rows, M, offsets, E, K / 8, static_cast<uint4 *>(out), scales, out_scales,
                          err);
